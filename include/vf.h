@@ -352,6 +352,66 @@ int vf_profile_read(vf_net* net, int kind, long long* launches, double* total_ms
 int vf_concretize_dense_noalloc(const float* lambda, long long lambda_bstride, int R, const float* W, const float* b,
                                 const float* centres, float eps, int B, int n_in, int n_out, float* lb, void* stream);
 
+/* ------------------------------------------------------------------------------------------------------------
+ * Dense layers and gradients on raw pointers, for evaluating, training or repairing a network beside its bounds. The
+ * page has no counterpart of these entry points. No handle: the caller owns every buffer and the workspace
+ * ([device], 256-byte aligned, used only by work enqueued by the call, so calls that may overlap on the GPU need a
+ * workspace each). Nothing is kept from one call for the next and nothing synchronises, so a call can be captured in a
+ * CUDA graph. All matrices of a call have one element type; sums are held in fp32 or more and every output is
+ * rounded to the element type once. Row strides (ld*) are in elements, at least the row's length; any alignment of
+ * the element type is served. Results do not change from run to run. Outputs must not overlap inputs, save where
+ * an entry point says so. */
+typedef enum { VF_F32 = 0, VF_BF16 = 1, VF_F16 = 2 } vf_dtype;
+typedef enum {
+    VF_ACT_NONE = 0,
+    VF_ACT_RELU = 1, /* z < 0 ? 0 : z, slope 0 at 0 */
+    VF_ACT_GELU = 2, /* z Phi(z), Phi the normal distribution (not its tanh approximation) */
+    VF_ACT_SILU = 3  /* z / (1 + exp(-z)) */
+} vf_act;
+
+/* Bytes of workspace that vf_linear (grad = 0) or vf_linear_grad (grad = 1) may need for these sizes, whatever the
+ * strides and alignment. May be 0. [host] */
+int vf_linear_workspace(int dtype, long long M, int N, int K, int grad, size_t* bytes);
+
+/* Dense layer with bias, residual and activation:  y = act(z),  z = x W^T + b + r.
+ * x [M, K], W [N, K], b [N] or NULL, r [M, N] or NULL, y [M, N]; z [M, N] or NULL receives the pre-activation that
+ * vf_linear_grad reads (y itself is formed from the unrounded z). With r the output of an earlier layer this is the
+ * closing layer of a residual block, as VF_ADD followed by VF_RELU. y may be r (same pointer and stride).
+ * K = 0 gives act(b + r); M = 0 or N = 0 is a no-op. A non-finite input makes the outputs that depend on it
+ * non-finite, not necessarily the value IEEE arithmetic would give. */
+int vf_linear(int dtype, int act, const void* x, long long ldx, const void* W, long long ldw, const void* b,
+              const void* r, long long ldr, long long M, int N, int K, void* y, long long ldy, void* z, long long ldz,
+              void* work, size_t work_bytes, void* stream);
+
+/* Backward pass of vf_linear for dy [M, N], the gradient of y:  g = dy act'(z),
+ *   dx [M, K] = g W,  dW [N, K] = g^T x,  db [N] = sum over rows of g,  dr [M, N] = g.
+ * Every output may be NULL (not computed); z may be NULL for VF_ACT_NONE, W without dx, x without dW. Outputs are
+ * written, not accumulated; M = 0 writes zeros to dW and db, N = 0 zeros to dx. For 16-bit types g is rounded to the
+ * element type where it enters the products (relu's and none's g is exact); db adds the unrounded g. */
+int vf_linear_grad(int dtype, int act, const void* dy, long long lddy, const void* z, long long ldz, const void* x,
+                   long long ldx, const void* W, long long ldw, long long M, int N, int K, void* dx, long long lddx,
+                   void* dW, long long lddw, void* db, void* dr, long long lddr, void* work, size_t work_bytes,
+                   void* stream);
+
+/* Device-wide synchronising check of vf_linear and vf_linear_grad on the current device: VF_ERR_TIMEOUT if one of
+ * their kernels gave up a bounded wait since the last check, in which case that call's outputs are not valid; clears
+ * the flag. */
+int vf_ops_check(void);
+
+/* Global L2 norm of n gradients and their scaling to a largest norm, without a host synchronisation:
+ *   *norm = scale * sqrt(sum over all elements of g^2),   out = g * scale * (norm > max_norm ? max_norm / norm : 1).
+ * grads, outs [host] n device pointers; sizes [host] elements of each (contiguous; 0 allowed); dtypes [host] vf_dtype of
+ * each (input and output alike; they may differ between gradients); norm [device] one float. scale >= 0 undoes a loss
+ * scale (1 for none); max_norm >= 0, INFINITY to measure and scale only. outs[t] is grads[t] itself (in place) or
+ * overlaps no gradient and no other output; overlaps are refused. A norm that is not finite clips nothing: the gradients
+ * are scaled by `scale` alone and *norm reports it. Squares are summed in fp64 beyond 32 terms, with
+ * no overflow or underflow for finite elements. The slope gradients of vf_alpha_grad and vf_alpha_beta_grad and the
+ * weight gradients of vf_linear_grad are the intended input. The workspace is vf_clip_workspace(n) bytes (of
+ * the current device). */
+int vf_clip_workspace(int n, size_t* bytes /*[host]*/);
+int vf_clip_grad_norm(int n, const void* const* grads, void* const* outs, const long long* sizes, const int* dtypes,
+                      float scale, float max_norm, float* norm, void* work, size_t work_bytes, void* stream);
+
 /* Number of kernel launches the library has enqueued on this handle since creation. */
 long long vf_launch_count(const vf_net* net);
 

@@ -1,0 +1,240 @@
+// Global L2 norm of a list of gradients, and the gradients scaled down to a largest norm.
+//
+//   norm = scale * sqrt(sum_t sum_i g_ti^2),  out_ti = g_ti * f,  f = scale * (max_norm / norm if norm > max_norm else 1)
+//
+// Two passes over the list: no element may be written before the norm over all of them is known. Each pass is one
+// launch per MAX_TENSORS tensors; the table of pointers travels in the kernel's parameters, so nothing is copied to the
+// device and a captured launch keeps its own table. Pass 1 leaves one partial sum per block, pass 2 adds them in a
+// fixed order in every block: no atomics, the same bits on every run.
+//
+// Squares are added in fp32 over one thread's 64 bytes (at most 32 terms) and in fp64 beyond that. Where such a
+// partial sum leaves the range in which fp32 squares are exact enough (overflow above 1e19, underflow below 1e-15 per
+// element), that thread's elements are squared again in fp64, so norms of any finite fp32 or bf16 values come out.
+#include <algorithm>
+
+#include "vf_internal.cuh"
+#include "vf_ops.cuh"
+
+namespace vf {
+
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int MAX_TENSORS = 100;            // 3.2 KB of the 4 KB parameter space
+constexpr int CHUNK_BYTES = THREADS * 64;   // one block iteration: four 16-byte loads per thread
+constexpr int BLOCKS_PER_SM = 8;
+
+struct Table {
+    const void* in[MAX_TENSORS];
+    void* out[MAX_TENSORS];
+    long long size[MAX_TENSORS];
+    int first[MAX_TENSORS + 1];  // first chunk of each tensor
+    unsigned char dtype[MAX_TENSORS];
+    int n;
+};
+
+__host__ __device__ __forceinline__ int chunk_elems(int dtype) { return CHUNK_BYTES / (dtype == VF_F32 ? 4 : 2); }
+
+template <typename T, int N>
+struct alignas(16) Vec {
+    T v[N];
+};
+
+// Sum of squares of n <= 32 values, see the header.
+template <typename T>
+__device__ __forceinline__ double squares(const T* v, int n) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+        const float x = to_f32(v[i]);
+        s = fmaf(x, x, s);
+    }
+    if (!(s < 3e38f) || s < 1e-30f) {
+        double d = 0.0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const double x = (double)to_f32(v[i]);
+            d = fma(x, x, d);
+        }
+        return d;
+    }
+    return (double)s;
+}
+
+// One chunk of a tensor: elements [e0, e1). `head` elements come before the first 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ double chunk_squares(const T* __restrict__ p, long long e0, long long e1) {
+    constexpr int N = 16 / sizeof(T);
+    const T* q = p + e0;
+    const int len = (int)(e1 - e0);
+    const int head = min(len, (int)(((16 - (reinterpret_cast<uintptr_t>(q) & 15)) & 15) / sizeof(T)));
+    const int nv = (len - head) / N;
+    const Vec<T, N>* b = reinterpret_cast<const Vec<T, N>*>(q + head);
+    double d = 0.0;
+    if (nv == 4 * THREADS) {
+        T v[4 * N];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) *reinterpret_cast<Vec<T, N>*>(v + u * N) = b[threadIdx.x + u * THREADS];
+        d = squares(v, 4 * N);
+    } else {
+        for (int i = threadIdx.x; i < nv; i += THREADS) {
+            const Vec<T, N> w = b[i];
+            d += squares(w.v, N);
+        }
+    }
+    if (threadIdx.x < head) d += squares(q + threadIdx.x, 1);
+    const int tail = head + nv * N + threadIdx.x;
+    if (tail < len) d += squares(q + tail, 1);
+    return d;
+}
+
+__device__ __forceinline__ double block_sum(double d) {
+    __shared__ double w[THREADS / 32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = d;
+    __syncthreads();
+    double t = 0.0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) t += w[i];
+    return t;
+}
+
+__global__ void __launch_bounds__(THREADS) clip_norm_k(const __grid_constant__ Table tab, double* part) {
+    double d = 0.0;
+    int t = 0;
+    for (int c = blockIdx.x; c < tab.first[tab.n]; c += gridDim.x) {
+        while (c >= tab.first[t + 1]) ++t;
+        const long long e = chunk_elems(tab.dtype[t]);
+        const long long e0 = (c - tab.first[t]) * e, e1 = min(tab.size[t], e0 + e);
+        switch (tab.dtype[t]) {
+            case VF_F32: d += chunk_squares((const float*)tab.in[t], e0, e1); break;
+            case VF_BF16: d += chunk_squares((const __nv_bfloat16*)tab.in[t], e0, e1); break;
+            default: d += chunk_squares((const __half*)tab.in[t], e0, e1); break;
+        }
+    }
+    const double s = block_sum(d);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const T* p, T* out, long long e0, long long e1, float f) {
+    constexpr int N = 16 / sizeof(T);
+    const T* q = p + e0;
+    T* o = out + e0;
+    const int len = (int)(e1 - e0);
+    const int head = min(len, (int)(((16 - (reinterpret_cast<uintptr_t>(q) & 15)) & 15) / sizeof(T)));
+    if (((reinterpret_cast<uintptr_t>(q) ^ reinterpret_cast<uintptr_t>(o)) & 15) != 0) {
+        for (int i = threadIdx.x; i < len; i += THREADS) o[i] = from_f32<T>(to_f32(q[i]) * f);
+        return;
+    }
+    const int nv = (len - head) / N;
+    const Vec<T, N>* b = reinterpret_cast<const Vec<T, N>*>(q + head);
+    Vec<T, N>* ob = reinterpret_cast<Vec<T, N>*>(o + head);
+    if (nv == 4 * THREADS) {
+        Vec<T, N> v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = b[threadIdx.x + u * THREADS];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[u].v[i] = from_f32<T>(to_f32(v[u].v[i]) * f);
+            ob[threadIdx.x + u * THREADS] = v[u];
+        }
+    } else {
+        for (int i = threadIdx.x; i < nv; i += THREADS) {
+            Vec<T, N> w = b[i];
+#pragma unroll
+            for (int k = 0; k < N; ++k) w.v[k] = from_f32<T>(to_f32(w.v[k]) * f);
+            ob[i] = w;
+        }
+    }
+    if (threadIdx.x < head) o[threadIdx.x] = from_f32<T>(to_f32(q[threadIdx.x]) * f);
+    const int tail = head + nv * N + threadIdx.x;
+    if (tail < len) o[tail] = from_f32<T>(to_f32(q[tail]) * f);
+}
+
+__global__ void __launch_bounds__(THREADS)
+clip_scale_k(const __grid_constant__ Table tab, const double* part, int nparts, float scale, float max_norm, float* norm,
+             int write_norm) {
+    double d = 0.0;
+    for (int i = threadIdx.x; i < nparts; i += THREADS) d += part[i];
+    const double n = (double)scale * sqrt(block_sum(d));
+    if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
+    const bool clip = n > (double)max_norm && !isinf(n);  // NaN compares false
+    const float f = (float)(clip ? (double)scale * ((double)max_norm / n) : (double)scale);
+    int t = 0;
+    for (int c = blockIdx.x; c < tab.first[tab.n]; c += gridDim.x) {
+        while (c >= tab.first[t + 1]) ++t;
+        if (tab.in[t] == tab.out[t] && f == 1.f) continue;
+        const long long e = chunk_elems(tab.dtype[t]);
+        const long long e0 = (c - tab.first[t]) * e, e1 = min(tab.size[t], e0 + e);
+        switch (tab.dtype[t]) {
+            case VF_F32: chunk_scale((const float*)tab.in[t], (float*)tab.out[t], e0, e1, f); break;
+            case VF_BF16: chunk_scale((const __nv_bfloat16*)tab.in[t], (__nv_bfloat16*)tab.out[t], e0, e1, f); break;
+            default: chunk_scale((const __half*)tab.in[t], (__half*)tab.out[t], e0, e1, f); break;
+        }
+    }
+}
+
+cudaError_t grid_limit(int* blocks) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    *blocks = sms * BLOCKS_PER_SM;
+    return e;
+}
+
+// Fills `tab` with tensors from index *t on, as many as fit; advances *t.
+void fill(const ClipList& l, int* t, Table* tab) {
+    tab->n = 0;
+    tab->first[0] = 0;
+    for (; *t < l.n && tab->n < MAX_TENSORS; ++*t) {
+        if (l.size[*t] == 0) continue;
+        const int k = tab->n;
+        const long long e = chunk_elems(l.dtype[*t]);
+        const long long chunks = (l.size[*t] + e - 1) / e;
+        if (tab->first[k] + chunks > 0x7fffffffLL) break;  // chunk numbers stay ints; the next launch takes it
+        tab->in[k] = l.in[*t];
+        tab->out[k] = l.out[*t];
+        tab->size[k] = l.size[*t];
+        tab->dtype[k] = (unsigned char)l.dtype[*t];
+        tab->first[k + 1] = tab->first[k] + (int)chunks;
+        tab->n = k + 1;
+    }
+}
+
+}  // namespace
+
+long long clip_work_doubles(int n, int sms) {
+    // a launch ends early only when 2^31 chunks (32 TiB) are reached, so ceil(n / MAX_TENSORS) launches always do
+    return (long long)std::max(1, (n + MAX_TENSORS - 1) / MAX_TENSORS) * sms * BLOCKS_PER_SM;
+}
+
+cudaError_t launch_clip(const ClipList& l, float scale, float max_norm, float* norm, double* work, cudaStream_t s) {
+    int limit = 0;
+    cudaError_t e = grid_limit(&limit);
+    if (e != cudaSuccess) return e;
+    Table tab;
+    int parts = 0;
+    for (int t = 0; t < l.n;) {
+        fill(l, &t, &tab);
+        if (tab.n == 0) continue;
+        const int grid = std::min(tab.first[tab.n], limit);
+        clip_norm_k<<<grid, THREADS, 0, s>>>(tab, work + parts);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        parts += grid;
+    }
+    bool wrote = false;
+    for (int t = 0; t < l.n || !wrote;) {
+        fill(l, &t, &tab);
+        if (tab.n == 0 && wrote) continue;
+        clip_scale_k<<<std::max(1, std::min(tab.first[tab.n], limit)), THREADS, 0, s>>>(tab, work, parts, scale, max_norm,
+                                                                                       norm, wrote ? 0 : 1);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        wrote = true;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace vf

@@ -1,0 +1,213 @@
+// C entry points of the dense-layer and gradient operators: argument checks, workspace sizes and the choice of kernel.
+// Handle-less like vf_concretize: everything a call needs is in its arguments, and the caller owns the workspace.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <new>
+#include <vector>
+
+#include "vf.h"
+#include "vf_internal.cuh"
+#include "vf_ops.cuh"
+
+using namespace vf;
+
+namespace {
+
+int ops_fail(int code, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    return set_last_error(code, buf);
+}
+
+#define OPS_TRY(call)                \
+    do {                             \
+        const int rc_ = (call);      \
+        if (rc_ != VF_OK) return rc_; \
+    } while (0)
+
+int elem_bytes(int dtype) { return dtype == VF_F32 ? 4 : 2; }
+
+int check_kind(int dtype, int act) {
+    if (dtype != VF_F32 && dtype != VF_BF16 && dtype != VF_F16) return ops_fail(VF_ERR_ARG, "unknown dtype %d", dtype);
+    if (act < VF_ACT_NONE || act > VF_ACT_SILU) return ops_fail(VF_ERR_ARG, "unknown activation %d", act);
+    return VF_OK;
+}
+
+int check_sizes(long long M, int N, int K) {
+    if (M < 0 || N < 0 || K < 0) return ops_fail(VF_ERR_ARG, "negative size: M %lld, N %d, K %d", M, N, K);
+    // tile coordinates are 32-bit, with room for one tile past the end
+    if (M > 0x7fffff00LL || N > 0x7fffff00 || K > 0x7fffff00)
+        return ops_fail(VF_ERR_UNSUPPORTED, "M %lld, N %d and K %d must stay below 2^31 - 256", M, N, K);
+    return VF_OK;
+}
+
+// A row-major matrix argument: present, aligned to its element, rows at least `cols` apart.
+int check_matrix(const char* name, const void* p, long long rows, long long cols, long long ld, int dtype) {
+    if (rows == 0 || cols == 0) return VF_OK;
+    if (p == nullptr) return ops_fail(VF_ERR_ARG, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(p) % elem_bytes(dtype) != 0)
+        return ops_fail(VF_ERR_ARG, "%s is not aligned to its element", name);
+    if (ld < cols && rows > 1)
+        return ops_fail(VF_ERR_ARG, "%s: row stride %lld is below its %lld columns", name, ld, cols);
+    if (ld > (1LL << 40)) return ops_fail(VF_ERR_ARG, "%s: row stride %lld is not one", name, ld);
+    return VF_OK;
+}
+
+int check_vector(const char* name, const void* p, int dtype) {
+    if (reinterpret_cast<uintptr_t>(p) % elem_bytes(dtype) != 0)
+        return ops_fail(VF_ERR_ARG, "%s is not aligned to its element", name);
+    return VF_OK;
+}
+
+int check_work(const void* work, size_t have, size_t need) {
+    if (need == 0) return VF_OK;
+    if (work == nullptr || have < need)
+        return ops_fail(VF_ERR_WORKSPACE, "workspace of %zu bytes, this call needs %zu", work == nullptr ? 0 : have, need);
+    if (reinterpret_cast<uintptr_t>(work) % 256 != 0) return ops_fail(VF_ERR_ARG, "workspace is not 256-byte aligned");
+    return VF_OK;
+}
+
+int launched(cudaError_t e) {
+    return e == cudaSuccess ? VF_OK : ops_fail(VF_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+}
+
+int sm_count(int* sms) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    return e == cudaSuccess ? VF_OK : ops_fail(VF_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
+}
+
+struct Range {
+    uintptr_t lo, hi;
+    int t;
+};
+
+// Every output range is disjoint from every other output and from every input but, exactly, its own.
+int check_overlaps(const ClipList& l) {
+    try {
+        std::vector<Range> outs;
+        outs.reserve(l.n);
+        for (int t = 0; t < l.n; ++t) {
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(l.out[t]);
+            if (l.size[t] > 0) outs.push_back(Range{lo, lo + (uintptr_t)l.size[t] * elem_bytes(l.dtype[t]), t});
+        }
+        std::sort(outs.begin(), outs.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+        for (size_t i = 1; i < outs.size(); ++i)
+            if (outs[i].lo < outs[i - 1].hi)
+                return ops_fail(VF_ERR_ARG, "outputs %d and %d overlap", outs[i - 1].t, outs[i].t);
+        for (int t = 0; t < l.n; ++t) {
+            if (l.size[t] == 0) continue;
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(l.in[t]);
+            const uintptr_t hi = lo + (uintptr_t)l.size[t] * elem_bytes(l.dtype[t]);
+            // the outputs are disjoint and sorted: the first that ends after lo is the only one to begin looking at
+            auto it = std::upper_bound(outs.begin(), outs.end(), lo, [](uintptr_t v, const Range& r) { return v < r.hi; });
+            for (; it != outs.end() && it->lo < hi; ++it)
+                if (it->t != t || it->lo != lo)
+                    return ops_fail(VF_ERR_ARG, "gradient %d overlaps output %d", t, it->t);
+        }
+    } catch (const std::bad_alloc&) {
+        return ops_fail(VF_ERR_WORKSPACE, "out of host memory");
+    }
+    return VF_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int vf_linear_workspace(int dtype, long long M, int N, int K, int grad, size_t* bytes) {
+    if (bytes == nullptr) return ops_fail(VF_ERR_ARG, "NULL pointer");
+    OPS_TRY(check_kind(dtype, VF_ACT_NONE));
+    OPS_TRY(check_sizes(M, N, K));
+    (void)grad;
+    *bytes = 0;
+    return VF_OK;
+}
+
+int vf_linear(int dtype, int act, const void* x, long long ldx, const void* W, long long ldw, const void* b,
+              const void* r, long long ldr, long long M, int N, int K, void* y, long long ldy, void* z, long long ldz,
+              void* work, size_t work_bytes, void* stream) {
+    OPS_TRY(check_kind(dtype, act));
+    OPS_TRY(check_sizes(M, N, K));
+    if (M == 0 || N == 0) return VF_OK;
+    OPS_TRY(check_matrix("x", x, M, K, ldx, dtype));
+    OPS_TRY(check_matrix("W", W, N, K, ldw, dtype));
+    OPS_TRY(check_vector("b", b, dtype));
+    if (r != nullptr) OPS_TRY(check_matrix("r", r, M, N, ldr, dtype));
+    OPS_TRY(check_matrix("y", y, M, N, ldy, dtype));
+    if (z != nullptr) OPS_TRY(check_matrix("z", z, M, N, ldz, dtype));
+    OPS_TRY(check_work(work, work_bytes, 0));
+    const LinearFwd p{dtype, act, x, ldx, W, ldw, b, r, ldr, M, N, K, y, ldy, z, ldz};
+    return launched(launch_linear_ffma(p, (cudaStream_t)stream));
+}
+
+int vf_linear_grad(int dtype, int act, const void* dy, long long lddy, const void* z, long long ldz, const void* x,
+                   long long ldx, const void* W, long long ldw, long long M, int N, int K, void* dx, long long lddx,
+                   void* dW, long long lddw, void* db, void* dr, long long lddr, void* work, size_t work_bytes,
+                   void* stream) {
+    OPS_TRY(check_kind(dtype, act));
+    OPS_TRY(check_sizes(M, N, K));
+    OPS_TRY(check_matrix("dy", dy, M, N, lddy, dtype));
+    if (act != VF_ACT_NONE) OPS_TRY(check_matrix("z", z, M, N, ldz, dtype));
+    if (dx != nullptr) {
+        OPS_TRY(check_matrix("W", W, N, K, ldw, dtype));
+        OPS_TRY(check_matrix("dx", dx, M, K, lddx, dtype));
+    }
+    if (dW != nullptr) {
+        OPS_TRY(check_matrix("x", x, M, K, ldx, dtype));
+        OPS_TRY(check_matrix("dW", dW, N, K, lddw, dtype));
+    }
+    OPS_TRY(check_vector("db", db, dtype));
+    if (dr != nullptr) OPS_TRY(check_matrix("dr", dr, M, N, lddr, dtype));
+    OPS_TRY(check_work(work, work_bytes, 0));
+    const LinearGrad p{dtype, act, dy, lddy, z, ldz, x, ldx, W, ldw, M, N, K, dx, lddx, dW, lddw, db, dr, lddr};
+    return launched(launch_linear_grad_ffma(p, (cudaStream_t)stream));
+}
+
+int vf_ops_check(void) {
+    const cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return ops_fail(VF_ERR_CUDA, "asynchronous CUDA error: %s", cudaGetErrorString(e));
+    return VF_OK;
+}
+
+int vf_clip_workspace(int n, size_t* bytes) {
+    if (bytes == nullptr) return ops_fail(VF_ERR_ARG, "NULL pointer");
+    if (n < 0) return ops_fail(VF_ERR_ARG, "negative number of gradients");
+    int sms = 0;
+    OPS_TRY(sm_count(&sms));
+    *bytes = (size_t)clip_work_doubles(n, sms) * sizeof(double);
+    return VF_OK;
+}
+
+int vf_clip_grad_norm(int n, const void* const* grads, void* const* outs, const long long* sizes, const int* dtypes,
+                      float scale, float max_norm, float* norm, void* work, size_t work_bytes, void* stream) {
+    if (n < 0) return ops_fail(VF_ERR_ARG, "negative number of gradients");
+    if (norm == nullptr || (n > 0 && (!grads || !outs || !sizes || !dtypes))) return ops_fail(VF_ERR_ARG, "NULL pointer");
+    if (!std::isfinite(scale) || scale < 0.f) return ops_fail(VF_ERR_NONFINITE, "scale must be finite and >= 0");
+    if (std::isnan(max_norm) || max_norm < 0.f) return ops_fail(VF_ERR_ARG, "max_norm must be >= 0");
+    const ClipList l{n, grads, outs, sizes, dtypes};
+    long long bytes = 0;
+    for (int t = 0; t < n; ++t) {
+        OPS_TRY(check_kind(dtypes[t], VF_ACT_NONE));
+        if (sizes[t] < 0 || sizes[t] > (1LL << 42)) return ops_fail(VF_ERR_ARG, "gradient %d has %lld elements", t, sizes[t]);
+        OPS_TRY(check_matrix("gradient", grads[t], 1, sizes[t], sizes[t], dtypes[t]));
+        OPS_TRY(check_matrix("output", outs[t], 1, sizes[t], sizes[t], dtypes[t]));
+        bytes += sizes[t] * elem_bytes(dtypes[t]);
+        if (bytes > (1LL << 44)) return ops_fail(VF_ERR_UNSUPPORTED, "gradients of over 16 TiB");
+    }
+    OPS_TRY(check_overlaps(l));
+    size_t need = 0;
+    OPS_TRY(vf_clip_workspace(n, &need));
+    OPS_TRY(check_work(work, work_bytes, need));
+    return launched(launch_clip(l, scale, max_norm, norm, (double*)work, (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,123 @@
+// Shared by the dense-layer and gradient operators (k_linear.cu, k_linear_tc.cu, k_clip.cu, vf_ops.cu): element
+// types, activations and the launch interfaces. Nothing here is part of the public ABI (include/vf.h).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "vf.h"
+
+namespace vf {
+
+// ------------------------------------------------------------------------------------------ element types
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) {
+    return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) {
+    return __float2half_rn(v);
+}
+
+// -------------------------------------------------------------------------------------------- activations
+// Evaluated in fp32. gelu is z Phi(z) with Phi(z) = erfc(-z / sqrt 2) / 2, which keeps its relative accuracy for
+// negative z where 1 + erf(z / sqrt 2) cancels. relu passes NaN on (z < 0 is false for it); gelu and silu take their
+// limit 0 at -inf.
+__device__ __forceinline__ float act_value(float z, int act) {
+    switch (act) {
+        case VF_ACT_RELU: return z < 0.f ? 0.f : z;
+        case VF_ACT_GELU: {
+            const float phi = 0.5f * erfcf(z * -0.70710678118654752f);
+            return phi == 0.f ? 0.f : z * phi;
+        }
+        case VF_ACT_SILU: {
+            const float e = expf(-z);
+            return isinf(e) ? 0.f : z / (1.f + e);
+        }
+        default: return z;
+    }
+}
+// dy act'(z); relu'(0) = 0, and relu selects instead of multiplying, so an infinite dy behind a closed ReLU stays 0.
+// silu' = s (1 + z (1 - s)) with 1 - s formed as e s (e = exp(-z)), so it does not cancel for large z; where e
+// overflows (z < -88) the slope is below 1e-36 and taken as 0. Beyond |z| = 80 gelu's slope, and above 80 silu's, are
+// their limits in fp32; the clamps keep 0 * inf away there.
+__device__ __forceinline__ float act_grad(float dy, float z, int act) {
+    if (act == VF_ACT_NONE) return dy;
+    if (act == VF_ACT_RELU) return z <= 0.f ? 0.f : dy;
+    if (z > 80.f) z = 80.f;
+    if (act == VF_ACT_GELU) {
+        if (z < -80.f) z = -80.f;
+        return dy * (0.5f * erfcf(z * -0.70710678118654752f) + z * (0.39894228040143268f * expf(-0.5f * z * z)));
+    }
+    const float e = expf(-z);
+    const float s = 1.f / (1.f + e);
+    return s == 0.f ? 0.f : dy * (s * (1.f + z * (e * s)));
+}
+
+// ------------------------------------------------------------------------------------------ launch interfaces
+// One dense layer, forward: y = act(z), z = x W^T + b + r. Row strides in elements.
+struct LinearFwd {
+    int dtype, act;
+    const void* x;
+    long long ldx;
+    const void* W;
+    long long ldw;
+    const void* b;  // or nullptr
+    const void* r;  // or nullptr
+    long long ldr;
+    long long M;
+    int N, K;
+    void* y;
+    long long ldy;
+    void* z;  // or nullptr
+    long long ldz;
+};
+
+// Its backward pass: g = dy act'(z); dx = g W, dW = g^T x, db = sum_m g, dr = g (any output may be nullptr).
+struct LinearGrad {
+    int dtype, act;
+    const void* dy;
+    long long lddy;
+    const void* z;  // nullptr only for VF_ACT_NONE
+    long long ldz;
+    const void* x;
+    long long ldx;
+    const void* W;
+    long long ldw;
+    long long M;
+    int N, K;
+    void* dx;
+    long long lddx;
+    void* dW;
+    long long lddw;
+    void* db;
+    void* dr;
+    long long lddr;
+};
+
+// FFMA kernels (k_linear.cu): any strides and alignment, no workspace.
+cudaError_t launch_linear_ffma(const LinearFwd& p, cudaStream_t s);
+cudaError_t launch_linear_grad_ffma(const LinearGrad& p, cudaStream_t s);
+
+// Gradient norm and clipping (k_clip.cu); ranges as in vf_clip_grad_norm. `work` holds clip_work_doubles(n, SMs) doubles.
+struct ClipList {
+    int n;
+    const void* const* in;
+    void* const* out;
+    const long long* size;
+    const int* dtype;
+};
+long long clip_work_doubles(int n, int sms);
+cudaError_t launch_clip(const ClipList& l, float scale, float max_norm, float* norm, double* work, cudaStream_t s);
+
+}  // namespace vf

@@ -27,7 +27,10 @@ SYMBOLS = ["vf_net_create", "vf_net_destroy", "vf_net_node_size", "vf_net_total_
            "vf_crown_backward", "vf_concretize", "vf_verify_batch", "vf_sync", "vf_last_error",
            "vf_profile_enable", "vf_profile_read", "vf_launch_count", "vf_net_check",
            "vf_concretize_dense_noalloc", "vf_alpha_crown", "vf_alpha_grad", "vf_alpha_beta_grad",
-           "vf_net_node_info", "vf_bab_verify", "vf_bab_search", "vf_abi_layout"]
+           "vf_net_node_info", "vf_bab_verify", "vf_bab_search", "vf_abi_layout", "vf_linear_workspace", "vf_linear",
+           "vf_linear_grad", "vf_clip_workspace", "vf_clip_grad_norm", "vf_ops_check"]
+VF_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+VF_ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 NOALLOC_SCRATCH_FLOATS = 1 << 22
 
 
@@ -107,6 +110,12 @@ def lib() -> ctypes.CDLL:
     L.vf_net_node_info.argtypes = [P, I, ctypes.POINTER(I), ctypes.POINTER(I), ctypes.POINTER(I), ctypes.POINTER(LL)]
     L.vf_bab_verify.argtypes = [P, P, F, P, I, ctypes.POINTER(BabOpts), ctypes.POINTER(BabResult), P]
     L.vf_bab_search.argtypes = [BOUND_FN, P, I, I, ctypes.POINTER(BabResult)]
+    SZ = ctypes.c_size_t
+    L.vf_linear_workspace.argtypes = [I, LL, I, I, I, ctypes.POINTER(SZ)]
+    L.vf_linear.argtypes = [I, I, P, LL, P, LL, P, P, LL, LL, I, I, P, LL, P, LL, P, SZ, P]
+    L.vf_linear_grad.argtypes = [I, I, P, LL, P, LL, P, LL, P, LL, LL, I, I, P, LL, P, LL, P, P, LL, P, SZ, P]
+    L.vf_clip_workspace.argtypes = [I, ctypes.POINTER(SZ)]
+    L.vf_clip_grad_norm.argtypes = [I, P, P, P, P, F, F, P, P, SZ, P]
     L.vf_launch_count.argtypes = [P]
     L.vf_launch_count.restype = LL
     _lib = L
@@ -464,6 +473,148 @@ def concretize_dense_noalloc(lam: torch.Tensor, W: torch.Tensor, b: torch.Tensor
     _check(lib().vf_concretize_dense_noalloc(_ptr(lam), bstride, R, _ptr(W), _ptr(b), _ptr(centres), float(eps), B,
                                              n_in, n_out, _ptr(out), _stream_ptr(stream)))
     return out
+
+
+class _On:
+    """The device and stream of one operator call: allocations inside belong to the stream the kernels run on."""
+
+    def __init__(self, device, stream):
+        self.guards = []
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _matrix(name, t, rows, cols, dtype, device):
+    """(pointer, row stride) of a [rows, cols] argument with unit column stride; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype or t.device != device or t.shape != (rows, cols):
+        raise ValueError(f"{name} must be {dtype} [{rows}, {cols}] on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    ld, one = t.stride()
+    if rows <= 1:
+        ld = cols
+    if (one != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name} must have rows of unit stride that do not overlap, got strides {t.stride()}")
+    return t.data_ptr(), ld
+
+
+def _vector(name, t, n, dtype, device):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != device or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} [{n}] on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _layer(x, W, act):
+    """Common checks of a layer's arguments: (dtype, activation, device, M, N, K)."""
+    if x.dtype not in VF_DTYPES:
+        raise ValueError(f"float32, bfloat16 or float16 expected, got {x.dtype}")
+    if act not in VF_ACTS:
+        raise ValueError(f"act must be one of {sorted(VF_ACTS)}, got {act!r}")
+    if not x.is_cuda or x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1]:
+        raise ValueError(f"x [M, K] and W [N, K] on a CUDA device expected, got {list(x.shape)} and {list(W.shape)}")
+    return x.dtype, VF_ACTS[act], x.device, x.shape[0], W.shape[0], x.shape[1]
+
+
+def _linear_work(dtype, M, N, K, grad, device):
+    n = ctypes.c_size_t()
+    _check(lib().vf_linear_workspace(dtype, M, N, K, grad, ctypes.byref(n)))
+    return (torch.empty(n.value, device=device, dtype=torch.uint8) if n.value else None), n.value
+
+
+def linear(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tensor] = None,
+           residual: Optional[torch.Tensor] = None, act: str = "none", want_z: bool = False,
+           out: Optional[torch.Tensor] = None, stream=None):
+    """vf_linear: act(x W^T + b + residual) for x [M, K], W [N, K], b [N], residual [M, N], all of one type (float32,
+    bfloat16 or float16); rows may be any distance apart. act: "none", "relu", "gelu" (normal distribution) or
+    "silu". Returns dict(y=[M, N], z=the pre-activation for linear_grad or None). out: y's buffer; it may be
+    `residual` itself. Runs on the current stream of x's device unless `stream` is given."""
+    dtype, a, dev, M, N, K = _layer(x, W, act)
+    xp, ldx = _matrix("x", x, M, K, dtype, dev)
+    wp, ldw = _matrix("W", W, N, K, dtype, dev)
+    bp = _vector("b", b, N, dtype, dev)
+    rp, ldr = _matrix("residual", residual, M, N, dtype, dev)
+    with _On(dev, stream):
+        y = torch.empty(M, N, device=dev, dtype=dtype) if out is None else out
+        z = torch.empty(M, N, device=dev, dtype=dtype) if want_z else None
+        yp, ldy = _matrix("out", y, M, N, dtype, dev)
+        work, nbytes = _linear_work(VF_DTYPES[dtype], M, N, K, 0, dev)
+        _check(lib().vf_linear(VF_DTYPES[dtype], a, xp, ldx, wp, ldw, bp, rp, ldr, M, N, K, yp, ldy,
+                               None if z is None else z.data_ptr(), N, None if work is None else work.data_ptr(),
+                               nbytes, _stream_ptr()))
+    return {"y": y, "z": z}
+
+
+def linear_grad(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, act: str = "none", z: Optional[torch.Tensor] = None,
+                need: Sequence[str] = ("dx", "dW", "db"), stream=None):
+    """vf_linear_grad: the backward pass of linear for dy [M, N], the gradient of y, and the z that linear returned
+    (not needed for act="none"). Returns dict(dx=[M, K], dW=[N, K], db=[N], dr=[M, N], the gradient of the
+    residual), None for those not in `need`."""
+    dtype, a, dev, M, N, K = _layer(x, W, act)
+    if not set(need) <= {"dx", "dW", "db", "dr"}:
+        raise ValueError(f"need names dx, dW, db and dr, got {list(need)}")
+    if a != 0 and z is None:
+        raise ValueError(f"act={act!r} needs the pre-activation z")
+    dyp, lddy = _matrix("dy", dy, M, N, dtype, dev)
+    zp, ldz = _matrix("z", z, M, N, dtype, dev)
+    xp, ldx = _matrix("x", x, M, K, dtype, dev)
+    wp, ldw = _matrix("W", W, N, K, dtype, dev)
+    with _On(dev, stream):
+        shapes = {"dx": (M, K), "dW": (N, K), "db": (N,), "dr": (M, N)}
+        o = {k: torch.empty(shape, device=dev, dtype=dtype) if k in need else None for k, shape in shapes.items()}
+        p = {k: None if t is None else t.data_ptr() for k, t in o.items()}
+        work, nbytes = _linear_work(VF_DTYPES[dtype], M, N, K, 1, dev)
+        _check(lib().vf_linear_grad(VF_DTYPES[dtype], a, dyp, lddy, zp, ldz, xp, ldx, wp, ldw, M, N, K, p["dx"], K,
+                                    p["dW"], K, p["db"], p["dr"], N, None if work is None else work.data_ptr(), nbytes,
+                                    _stream_ptr()))
+    return o
+
+
+def ops_check():
+    """vf_ops_check: synchronise the current device and raise if a kernel of linear or linear_grad gave up a bounded
+    wait since the last check."""
+    _check(lib().vf_ops_check())
+
+
+def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, scale: float = 1.0,
+                   out: Optional[Sequence[torch.Tensor]] = None, stream=None):
+    """vf_clip_grad_norm: (norm, out). norm is a float32 scalar tensor, scale * the global L2 norm of all gradients;
+    out are the gradients times scale, and times max_norm / norm where the norm is larger than max_norm. Without
+    `out` the gradients are overwritten. They may differ in type; each is contiguous. Nothing synchronises: a norm that
+    is not finite clips nothing and is left for the caller to look at."""
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError(f"{len(grads)} gradients and {len(outs)} outputs")
+    dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+    n = len(grads)
+    gp, op = (ctypes.c_void_p * n)(), (ctypes.c_void_p * n)()
+    sizes, dtypes = (ctypes.c_longlong * n)(), (ctypes.c_int * n)()
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        if g.dtype not in VF_DTYPES or not g.is_cuda or g.device != dev or not g.is_contiguous():
+            raise ValueError(f"gradient {i} must be contiguous float32, bfloat16 or float16 on {dev}, got {g.dtype} on {g.device}")
+        if o is not g and (o.dtype != g.dtype or o.device != dev or o.shape != g.shape or not o.is_contiguous()):
+            raise ValueError(f"out {i} must be contiguous {g.dtype} {list(g.shape)} on {dev}, got {o.dtype} {list(o.shape)}")
+        gp[i], op[i], sizes[i], dtypes[i] = g.data_ptr(), o.data_ptr(), g.numel(), VF_DTYPES[g.dtype]
+    with _On(dev, stream):
+        norm = torch.empty((), device=dev, dtype=torch.float32)
+        nbytes = ctypes.c_size_t()
+        _check(lib().vf_clip_workspace(n, ctypes.byref(nbytes)))
+        work = torch.empty(nbytes.value, device=dev, dtype=torch.uint8)
+        _check(lib().vf_clip_grad_norm(n, gp, op, sizes, dtypes, float(scale), float(max_norm), norm.data_ptr(),
+                                       work.data_ptr(), nbytes.value, _stream_ptr()))
+    return norm, outs
 
 
 def bab_search(evaluate, max_domains: int, batch: int):
