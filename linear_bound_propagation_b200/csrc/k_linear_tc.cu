@@ -1,0 +1,997 @@
+// Dense layer and its backward pass on the 5th-generation tensor cores (sm_100a): tcgen05.mma kind::f16, operands
+// staged by TMA, fp32 accumulators in TMEM.
+//
+// Every product here is  C[j, i] = sum_t A(i, t) B(j, t)  with i the contiguous index of the output:
+//   forward  y[m, n]  : i = n, j = m, t = k;  A = W and B = x, both contiguous along t
+//   dx[m, k]          : i = k, j = m, t = n;  A = W contiguous along i, B = g contiguous along t
+//   dW[n, k]          : i = k, j = n, t = m;  A = x contiguous along i, B = g contiguous along j
+// The tensor cores take either order of either operand (the descriptors' major bits), so nothing is transposed. i runs
+// along the MMA's M (128 TMEM lanes), j along its N: the small dimension of a call of few rows is the one that can be
+// as narrow as 16 columns, and a warp's 32 lanes hold consecutive elements of an output row.
+//
+// fp32 (PL = 3): x = h + m + l, three bf16 pieces of 8 significand bits each, by truncation, so the pieces hold all 24
+// bits and bf16's exponent range is fp32's. Six of the nine products are formed (h h, h m, m h, m m, h l, l h); the
+// three left out are below 2^-24 of the largest. An MMA adds its products to the accumulator with truncation (measured:
+// a sum of positive terms over 512 MMAs comes out 1e-5 low), so the five small products go to an accumulator of their own, and
+// the h h accumulator is added to registers, rounding to nearest, every CHUNK of the reduction.
+//
+// Roles (10 warps, one CTA per SM, persistent over the tiles): warp 0 TMA producer and TMEM owner, warp 1 MMA issuer,
+// warps 2-9 epilogue (TMEM lane quarter warp % 4; 2-5 the first half of the tile's columns, 6-9 the second).
+// When the tiles are too few to fill the SMs, the reduction is split over a cluster of 2, 4 or 8 CTAs, which
+// join their partial tiles through distributed shared memory in rank order. All waits are bounded: on expiry an abort
+// flag stops every role, copies and MMAs in flight are waited for (also bounded), TMEM is freed and a device flag set.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstring>
+#include <type_traits>
+
+#include "tc_ptx.cuh"
+#include "vf_internal.cuh"
+#include "vf_ops.cuh"
+
+namespace vf {
+
+namespace {
+
+using namespace tc;
+
+__device__ int g_ops_timeout;
+
+constexpr int BM = 128;
+constexpr int NUM_THREADS = 320;
+constexpr int EPI_THREADS = 256;
+constexpr int MAX_STAGES = 8;
+constexpr int SMEM_LIMIT = 232448;  // 227 KB, static shared memory included
+constexpr int CHUNK = 8;            // k-blocks of 32 between two additions of the h h accumulator (PL = 3)
+
+template <int PL>
+constexpr int block_k() {
+    return PL == 3 ? 32 : 64;
+}
+
+struct TcProduct {
+    long long I, J;      // output columns (contiguous) and rows
+    int nk;              // blocks of the reduction
+    int a_mn, b_mn;      // operand contiguous along i (j) instead of t
+    int tiles_i;
+    long long tiles;
+    void* out;
+    long long ldo;
+    const void* bias;
+    const void* res;
+    long long ldr;
+    void* zout;
+    long long ldz;
+    int act, vec;        // vec: output, residual and z rows all allow 16-byte accesses
+};
+
+struct TcParams {
+    TcProduct p[2];
+    long long tiles;     // of both products
+    int split;           // CTAs per tile (cluster size)
+    int stages;
+    // column sums of g, joined here: db[n] = sum_q part[q * N + n]
+    const float* part;
+    int nparts, N;
+    void* db;
+};
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// D (tmem) (+)= A (smem) x B (smem), kind::f16.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// Operand of rows x BK elements in shared memory. Contiguous along t: rows of BK elements (128 or 64 bytes, swizzled
+// over as many bytes), 8-row groups one after the other. Contiguous along i or j: atoms of 64 elements x BK steps of t,
+// 128-byte rows swizzled over 128 bytes, 8-step groups 1024 bytes apart, atoms BK * 128 bytes apart.
+template <int BK>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, int mn) {
+    const uint64_t base = (uint64_t)((saddr >> 4) & 0x3FFF) | (1ull << 46);
+    if (mn) return base | ((uint64_t)(BK * 128 / 16) << 16) | (64ull << 32) | (2ull << 61);
+    return base | (1ull << 16) | ((uint64_t)(8 * BK * 2 / 16) << 32) | ((BK == 64 ? 2ull : 4ull) << 61);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]);
+template <>
+__device__ __forceinline__ void tmem_ld<8>(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+                 "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+                 "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+                 : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t saddr, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+template <typename T>
+struct alignas(16) Pack8 {
+    T v[8];
+};
+
+// Eight consecutive outputs i .. i + 7 of row j.
+template <typename T>
+__device__ __forceinline__ void finish8(const TcProduct& p, long long i, long long j, float (&v)[8], const float (&bias)[8]) {
+    const bool full = p.vec && i + 8 <= p.I;
+    if (p.res != nullptr) {
+        const T* r = (const T*)p.res + j * p.ldr + i;
+        if (full) {
+            const Pack8<T> w = *reinterpret_cast<const Pack8<T>*>(r);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] += to_f32(w.v[u]) + bias[u];
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (i + u < p.I) v[u] += to_f32(r[u]) + bias[u];
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] += bias[u];
+    }
+    Pack8<T> w;
+    if (p.zout != nullptr) {
+        T* zp = (T*)p.zout + j * p.ldz + i;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) w.v[u] = from_f32<T>(v[u]);
+        if (full) {
+            *reinterpret_cast<Pack8<T>*>(zp) = w;
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (i + u < p.I) zp[u] = w.v[u];
+        }
+    }
+    switch (p.act) {
+        case VF_ACT_RELU:
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = act_value(v[u], VF_ACT_RELU);
+            break;
+        case VF_ACT_GELU:
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = act_value(v[u], VF_ACT_GELU);
+            break;
+        case VF_ACT_SILU:
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = act_value(v[u], VF_ACT_SILU);
+            break;
+        default: break;
+    }
+    T* o = (T*)p.out + j * p.ldo + i;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) w.v[u] = from_f32<T>(v[u]);
+    if (full) {
+        *reinterpret_cast<Pack8<T>*>(o) = w;
+    } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (i + u < p.I) o[u] = w.v[u];
+    }
+}
+
+constexpr int STG_LD = 36;                             // floats per staged column: 16-byte rows, conflict-free reads
+constexpr int STG_BYTES = 8 * 8 * STG_LD * 4;          // eight warps x eight columns
+
+template <int PL, int BN>
+constexpr int stage_bytes() {
+    return PL * (BM + BN) * block_k<PL>() * 2;
+}
+
+template <typename T, int PL, int BN>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
+            const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
+            const __grid_constant__ TcParams P) {
+    constexpr int BK = block_k<PL>();
+    constexpr int A_PLANE = BM * BK * 2, B_PLANE = BN * BK * 2;
+    constexpr int STAGE = stage_bytes<PL, BN>();
+    constexpr int NB = (PL == 1 || BN <= 128) ? 2 : 1;       // accumulator sets in TMEM
+    constexpr int ACC_COLS = NB * BN;
+    constexpr int USED_COLS = PL == 3 ? 2 * ACC_COLS : ACC_COLS;
+    constexpr int TMEM_COLS = USED_COLS < 32 ? 32 : USED_COLS;
+    constexpr int HALF = BN / 2;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], cor_empty[2], done_bar;
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_sh;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int NS = P.stages;
+    const int S = P.split;
+    const uint32_t rank = S > 1 ? cluster_rank() : 0;
+    const long long tile0 = blockIdx.x / S, tile_step = gridDim.x / S;
+
+    if (threadIdx.x == 0) {
+        abort_sh = 0;
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&acc_full[s], 1);
+            mbar_init(&acc_empty[s], EPI_THREADS);
+            mbar_init(&cor_empty[s], EPI_THREADS);
+        }
+        mbar_init(&done_bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_sh)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_sh;
+    volatile int* abort_flag = &abort_sh;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------------------------------------- TMA producer
+            long long g = 0;
+            for (long long t = tile0; t < P.tiles && !*abort_flag; t += tile_step) {
+                const int w = t >= P.p[0].tiles;
+                const TcProduct& p = P.p[w];
+                const long long u = w ? t - P.p[0].tiles : t;
+                const int i0 = (int)(u % p.tiles_i) * BM, j0 = (int)(u / p.tiles_i) * BN;
+                const CUtensorMap* ma = w ? &tmA1 : &tmA0;
+                const CUtensorMap* mb = w ? &tmB1 : &tmB0;
+                const int kb1 = (int)((long long)p.nk * (rank + 1) / S);
+                for (int kb = (int)((long long)p.nk * rank / S); kb < kb1; ++kb, ++g) {
+                    const int s = (int)(g % NS);
+                    if (g >= NS && !mbar_wait(&empty[s], (uint32_t)((g / NS) - 1) & 1, abort_flag)) break;
+                    uint8_t* st = base + (size_t)s * STAGE;
+                    mbar_expect_tx(&full[s], STAGE);
+#pragma unroll
+                    for (int q = 0; q < PL; ++q) {
+                        uint8_t* a = st + q * A_PLANE;
+                        uint8_t* b = st + PL * A_PLANE + q * B_PLANE;
+                        if (p.a_mn) {
+#pragma unroll
+                            for (int c = 0; c < BM / 64; ++c)
+                                tma_load_3d(a + c * BK * 128, ma, &full[s], i0 + c * 64, kb * BK, q);
+                        } else {
+                            tma_load_3d(a, ma, &full[s], kb * BK, i0, q);
+                        }
+                        if (BN >= 64 && p.b_mn) {
+#pragma unroll
+                            for (int c = 0; c < BN / 64; ++c)
+                                tma_load_3d(b + c * BK * 128, mb, &full[s], j0 + c * 64, kb * BK, q);
+                        } else {
+                            tma_load_3d(b, mb, &full[s], kb * BK, j0, q);
+                        }
+                    }
+                }
+            }
+            if (*abort_flag)  // wait (bounded) for copies that nobody will consume
+                for (long long h = (g > NS ? g - NS : 0); h < g; ++h) {
+                    const long long t0 = clock64();
+                    while (!mbar_test(&full[h % NS], (uint32_t)(h / NS) & 1) && clock64() - t0 < WAIT_CYCLES) {
+                    }
+                }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // --------------------------------------------------------------------------------- MMA issuer
+            long long g = 0, chunks = 0, tiles = 0;
+            bool ok = true;
+            for (long long t = tile0; ok && t < P.tiles && !*abort_flag; t += tile_step, ++tiles) {
+                const TcProduct& p = P.p[t >= P.p[0].tiles];
+                const int kb0 = (int)((long long)p.nk * rank / S), kb1 = (int)((long long)p.nk * (rank + 1) / S);
+                const uint32_t fmt = (PL == 3 || sizeof(T) == 4 || std::is_same<T, __nv_bfloat16>::value) ? 1u : 0u;
+                const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)p.a_mn << 15) |
+                                       ((uint32_t)p.b_mn << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+                // bytes between the K = 16 steps of a stage
+                const uint32_t step_a = p.a_mn ? 2048 : 32, step_b = p.b_mn ? 2048 : 32;
+                const uint32_t cor = tmem + ACC_COLS + (uint32_t)(tiles % NB) * BN;
+                for (int kb = kb0; kb < kb1; ++kb, ++g) {
+                    const int s = (int)(g % NS);
+                    if (!(ok = mbar_wait(&full[s], (uint32_t)(g / NS) & 1, abort_flag))) break;
+                    const bool first = PL == 3 ? (kb - kb0) % CHUNK == 0 : kb == kb0;
+                    const bool last = kb + 1 == kb1 || (PL == 3 && (kb - kb0) % CHUNK == CHUNK - 1);
+                    const uint32_t d = tmem + (uint32_t)(chunks % NB) * BN;
+                    const uint32_t sa = smem_u32(base + (size_t)s * STAGE), sb = sa + PL * A_PLANE;
+                    tc_fence_after();
+                    if (PL == 3) {
+                        if (kb == kb0 && tiles >= NB &&
+                            !(ok = mbar_wait(&cor_empty[tiles % NB], (uint32_t)(tiles / NB - 1) & 1, abort_flag)))
+                            break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk) {
+                            const uint32_t oa = sa + kk * step_a, ob = sb + kk * step_b;
+                            const uint64_t ah = operand_desc<BK>(oa, p.a_mn), bh = operand_desc<BK>(ob, p.b_mn);
+                            const uint64_t am = operand_desc<BK>(oa + A_PLANE, p.a_mn);
+                            const uint64_t bm = operand_desc<BK>(ob + B_PLANE, p.b_mn);
+                            const uint64_t al = operand_desc<BK>(oa + 2 * A_PLANE, p.a_mn);
+                            const uint64_t bl = operand_desc<BK>(ob + 2 * B_PLANE, p.b_mn);
+                            mma_f16_ss(cor, al, bh, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+                            mma_f16_ss(cor, ah, bl, idesc, 1u);
+                            mma_f16_ss(cor, am, bm, idesc, 1u);
+                            mma_f16_ss(cor, am, bh, idesc, 1u);
+                            mma_f16_ss(cor, ah, bm, idesc, 1u);
+                        }
+                    }
+                    if (first && chunks >= NB &&
+                        !(ok = mbar_wait(&acc_empty[chunks % NB], (uint32_t)(chunks / NB - 1) & 1, abort_flag)))
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk)
+                        mma_f16_ss(d, operand_desc<BK>(sa + kk * step_a, p.a_mn), operand_desc<BK>(sb + kk * step_b, p.b_mn),
+                                   idesc, (!first || kk > 0) ? 1u : 0u);
+                    mma_commit(&empty[s]);
+                    if (last) {
+                        mma_commit(&acc_full[chunks % NB]);
+                        ++chunks;
+                    }
+                }
+            }
+            // TMEM is never freed, nor the stages reused, under MMAs in flight: one last commit tracks them all
+            mma_commit(&done_bar);
+            const long long t0 = clock64();
+            while (!mbar_test(&done_bar, 0) && clock64() - t0 < WAIT_CYCLES) {
+            }
+        }
+    } else {
+        // ------------------------------------------------------------------------------------- epilogue
+        const int q = warp & 3, half = warp >= 6;
+        const uint32_t lane_base = ((uint32_t)(q * 32) << 16) + half * HALF;
+        float* stg = reinterpret_cast<float*>(base + (size_t)NS * STAGE) + (warp - 2) * 8 * STG_LD;
+        if (P.db != nullptr)
+            for (long long n = (long long)blockIdx.x * EPI_THREADS + threadIdx.x - 64; n < P.N;
+                 n += (long long)gridDim.x * EPI_THREADS) {
+                float s = 0.f;
+#pragma unroll 8
+                for (int k = 0; k < P.nparts; ++k) s += P.part[(long long)k * P.N + n];
+                ((T*)P.db)[n] = from_f32<T>(s);
+            }
+        long long chunks = 0, tiles = 0;
+        const int tj = lane >> 2, ti = (lane & 3) * 8;  // this thread's part of an 8-column, 32-lane block
+        for (long long t = tile0; t < P.tiles; t += tile_step, ++tiles) {
+            const int w = t >= P.p[0].tiles;
+            const TcProduct& p = P.p[w];
+            const long long u = w ? t - P.p[0].tiles : t;
+            const long long i0 = (u % p.tiles_i) * BM, j0 = (u / p.tiles_i) * BN + half * HALF;
+            const long long i = i0 + q * 32 + ti;
+            float bias[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                bias[k] = (p.bias != nullptr && i + k < p.I) ? to_f32(((const T*)p.bias)[i + k]) : 0.f;
+            const int kb0 = (int)((long long)p.nk * rank / S), kb1 = (int)((long long)p.nk * (rank + 1) / S);
+            uint32_t acc_t = 0;  // TMEM columns that hold this warp's part of the finished tile
+            if (PL == 3) {
+                float acc[HALF];
+#pragma unroll
+                for (int c = 0; c < HALF; ++c) acc[c] = 0.f;
+                const int nc = (kb1 - kb0 + CHUNK - 1) / CHUNK;
+                bool alive = true;
+                for (int ch = 0; ch < nc; ++ch, ++chunks) {
+                    const int b = (int)(chunks % NB);
+                    if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[b], (uint32_t)(chunks / NB) & 1, abort_flag))) {
+                        alive = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    acc_t = tmem + lane_base + b * BN;
+#pragma unroll
+                    for (int c = 0; c < HALF; c += 8) {
+                        uint32_t v[8];
+                        tmem_ld<8>(acc_t + c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) acc[c + k] += __uint_as_float(v[k]);
+                    }
+                    if (ch + 1 < nc) {
+                        tc_fence_before();
+                        mbar_arrive(&acc_empty[b]);
+                    }
+                }
+                if (!alive) break;
+                --chunks;  // the last chunk's columns are released after the epilogue
+                const uint32_t cor_t = tmem + lane_base + ACC_COLS + (uint32_t)(tiles % NB) * BN;
+#pragma unroll
+                for (int c = 0; c < HALF; c += 8) {  // the finished sums go back to TMEM for the rolled loop below
+                    uint32_t v[8];
+                    tmem_ld<8>(cor_t + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) acc[c + k] += __uint_as_float(v[k]);
+                    tmem_st8(acc_t + c, acc + c);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                mbar_arrive(&cor_empty[tiles % NB]);
+            } else {
+                const int b = (int)(chunks % NB);
+                if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[b], (uint32_t)(chunks / NB) & 1, abort_flag))) break;
+                tc_fence_after();
+                acc_t = tmem + lane_base + b * BN;
+            }
+            if (S == 1) {
+                for (int c = 0; c < HALF; c += 8) {
+                    uint32_t v[8];
+                    tmem_ld<8>(acc_t + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) stg[k * STG_LD + lane] = __uint_as_float(v[k]);
+                    __syncwarp();
+                    const float4 lo = *reinterpret_cast<const float4*>(stg + tj * STG_LD + ti);
+                    const float4 hi = *reinterpret_cast<const float4*>(stg + tj * STG_LD + ti + 4);
+                    float o[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    __syncwarp();
+                    const long long j = j0 + c + tj;
+                    if (i < p.I && j < p.J) finish8<T>(p, i, j, o, bias);
+                }
+            } else {
+                // every stage of this tile has been consumed: its shared memory takes the partial tile
+                float* part = reinterpret_cast<float*>(base);
+                for (int c = 0; c < HALF; c += 8) {
+                    uint32_t v[8];
+                    tmem_ld<8>(acc_t + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) part[(half * HALF + c + k) * BM + q * 32 + lane] = __uint_as_float(v[k]);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&acc_empty[chunks % NB]);
+            ++chunks;
+        }
+    }
+
+    if (S > 1) {
+        // one tile per cluster: join the partial tiles, each CTA its share of the columns
+        __syncwarp();
+        cluster_sync_all();
+        if (warp >= 2 && tile0 < P.tiles) {
+            const int w = tile0 >= P.p[0].tiles;
+            const TcProduct& p = P.p[w];
+            const long long u = w ? tile0 - P.p[0].tiles : tile0;
+            const long long i0 = (u % p.tiles_i) * BM, j0 = (u / p.tiles_i) * BN;
+            const uint32_t part = smem_u32(base);
+            const int c0 = BN * (int)rank / S, c1 = BN * ((int)rank + 1) / S;
+            // a thread takes eight lanes of a column: 16 threads per column, 16 columns at a time
+            const int e = threadIdx.x - 64;
+            const long long i = i0 + (e & 15) * 8;
+            for (int c = c0 + (e >> 4); c < c1; c += EPI_THREADS / 16) {
+                const long long j = j0 + c;
+                if (i >= p.I || j >= p.J) continue;
+                float o[8], bias[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    o[k] = 0.f;
+                    bias[k] = (p.bias != nullptr && i + k < p.I) ? to_f32(((const T*)p.bias)[i + k]) : 0.f;
+                }
+                for (int r = 0; r < S; ++r)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] += ld_cluster(part + (c * BM + (e & 15) * 8 + k) * 4, r);
+                finish8<T>(p, i, j, o, bias);
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();  // no CTA leaves while another reads its partial tile
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+    }
+    if (threadIdx.x == 0 && abort_sh) atomicExch(&g_ops_timeout, 1);
+}
+
+// ----------------------------------------------------------------------------------- operands in tensor-core form
+
+// x = h + m + l: three bf16 by truncation, 8 significand bits each. A value that is not finite has m = l = 0.
+__device__ __forceinline__ void split3(float x, uint16_t& h, uint16_t& m, uint16_t& l) {
+    const uint32_t hb = __float_as_uint(x) & 0xffff0000u;
+    h = (uint16_t)(hb >> 16);
+    if (isfinite(x)) {
+        const float r = x - __uint_as_float(hb);
+        const uint32_t mb = __float_as_uint(r) & 0xffff0000u;
+        m = (uint16_t)(mb >> 16);
+        l = (uint16_t)(__float_as_uint(r - __uint_as_float(mb)) >> 16);
+    } else {
+        if (isnan(x)) h = 0x7fff;  // the payload may sit in the bits cut off
+        m = l = 0;
+    }
+}
+
+// Eight values of a row to the planes of the operand at dst (planes `plane` elements apart; PL = 1: the type itself).
+template <typename T>
+__device__ __forceinline__ void store_operand(uint16_t* dst, long long plane, const float (&v)[8]) {
+    if (sizeof(T) == 4) {
+        union {
+            uint16_t s[8];
+            uint4 q;
+        } h, m, l;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) split3(v[u], h.s[u], m.s[u], l.s[u]);
+        *reinterpret_cast<uint4*>(dst) = h.q;
+        *reinterpret_cast<uint4*>(dst + plane) = m.q;
+        *reinterpret_cast<uint4*>(dst + 2 * plane) = l.q;
+    } else {
+        Pack8<T> w;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) w.v[u] = from_f32<T>(v[u]);
+        *reinterpret_cast<Pack8<T>*>(dst) = w;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]) {
+    if (vec && n >= 8) {
+        const Pack8<T> w = *reinterpret_cast<const Pack8<T>*>(p);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = to_f32(w.v[u]);
+    } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = u < n ? to_f32(p[u]) : 0.f;
+    }
+}
+
+// A matrix to lay out: rows x cols, to `planes` planes of rows x ldp (ldp a multiple of 64).
+struct PackJob {
+    const void* src;
+    long long ld, rows;
+    int cols, vec;
+    uint16_t* dst;
+    long long ldp;
+    long long blocks;  // of PACK_ROWS rows x PACK_COLS columns
+    int blocks_c;
+};
+constexpr int PACK_ROWS = 64, PACK_COLS = 256, PACK_THREADS = 256;
+
+template <typename T>
+__device__ void pack_block(const PackJob& j, long long blk) {
+    const long long r0 = blk / j.blocks_c * PACK_ROWS + (threadIdx.x >> 5);
+    const int c = (int)(blk % j.blocks_c) * PACK_COLS + (threadIdx.x & 31) * 8;
+    if (c >= j.cols) return;
+    const long long plane = j.rows * j.ldp;
+#pragma unroll 4
+    for (int k = 0; k < PACK_ROWS / 8; ++k) {
+        const long long r = r0 + k * 8;
+        if (r >= j.rows) break;
+        float v[8];
+        load8((const T*)j.src + r * j.ld + c, j.cols - c, j.vec, v);
+        store_operand<T>(j.dst + r * j.ldp + c, plane, v);
+    }
+}
+
+// g = dy act'(z) of PACK_ROWS rows x PACK_COLS columns: to the operand (dst, unless g is dy itself), to dr, and its column sums
+// over the rows, in fp32, to part[row block][N].
+struct GradJob {
+    const void* dy;
+    long long lddy;
+    const void* z;
+    long long ldz;
+    long long M;
+    int N, act, vec, vec_r;
+    uint16_t* dst;  // or nullptr
+    long long ldp;
+    void* dr;  // or nullptr
+    long long lddr;
+    float* part;  // or nullptr
+    long long blocks;
+    int blocks_c;
+};
+
+template <typename T>
+__device__ void grad_block(const GradJob& j, long long blk) {
+    __shared__ float sums[8][PACK_COLS];
+    const int w = threadIdx.x >> 5;
+    const long long rb = blk / j.blocks_c;
+    const int c0 = (int)(blk % j.blocks_c) * PACK_COLS, cl = (threadIdx.x & 31) * 8, c = c0 + cl;
+    float s[8] = {};
+    if (c < j.N) {
+        const int n = j.N - c;
+#pragma unroll 2
+        for (int k = 0; k < PACK_ROWS / 8; ++k) {
+            const long long r = rb * PACK_ROWS + w + k * 8;
+            if (r >= j.M) break;
+            float v[8];
+            load8((const T*)j.dy + r * j.lddy + c, n, j.vec, v);
+            if (j.act != VF_ACT_NONE) {
+                float z[8];
+                load8((const T*)j.z + r * j.ldz + c, n, j.vec, z);
+                switch (j.act) {
+                    case VF_ACT_RELU:
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) v[u] = act_grad(v[u], z[u], VF_ACT_RELU);
+                        break;
+                    case VF_ACT_GELU:
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) v[u] = act_grad(v[u], z[u], VF_ACT_GELU);
+                        break;
+                    default:
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) v[u] = act_grad(v[u], z[u], VF_ACT_SILU);
+                }
+            }
+            if (j.dst != nullptr) store_operand<T>(j.dst + r * j.ldp + c, j.M * j.ldp, v);
+            if (j.dr != nullptr) {
+                T* o = (T*)j.dr + r * j.lddr + c;
+                Pack8<T> p;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) p.v[u] = from_f32<T>(v[u]);
+                if (j.vec_r && n >= 8) {
+                    *reinterpret_cast<Pack8<T>*>(o) = p;
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (u < n) o[u] = p.v[u];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s[u] += v[u];
+        }
+    }
+    if (j.part == nullptr) return;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) sums[w][cl + u] = s[u];
+    __syncthreads();
+    const int n = c0 + threadIdx.x;
+    if (n < j.N) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t += sums[k][threadIdx.x];
+        j.part[rb * j.N + n] = t;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(PACK_THREADS)
+linear_operands_k(const __grid_constant__ GradJob g, const __grid_constant__ PackJob a, const __grid_constant__ PackJob b) {
+    const long long t = blockIdx.x;
+    if (t < g.blocks)
+        grad_block<T>(g, t);
+    else if (t < g.blocks + a.blocks)
+        pack_block<T>(a, t - g.blocks);
+    else
+        pack_block<T>(b, t - g.blocks - a.blocks);
+}
+
+// ------------------------------------------------------------------------------------------------- host side
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = []() -> EncodeTiledFn {  // thread-safe one-time lookup
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<EncodeTiledFn>(ptr);
+    }();
+    return fn;
+}
+
+// A matrix in tensor-core form: 16-bit planes of rows x cols, rows ld elements apart, 16-byte aligned.
+struct Operand16 {
+    const void* ptr;
+    long long rows, ld;
+    int cols;
+};
+
+// mn: the operand is contiguous along its own index; its box is 64 columns x bk rows (steps of t). Else box of bk
+// columns x `box` rows, swizzled over the bk * 2 bytes of a row.
+bool make_map(CUtensorMap* map, const Operand16& o, int planes, bool mn, int bk, int box, bool bf16) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, (cuuint64_t)planes};
+    cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)o.rows * o.ld * 2};
+    if (planes == 1 && strides[1] >= (1ull << 40)) strides[1] = strides[0];  // of the one plane: never used
+    cuuint32_t boxes[3] = {(cuuint32_t)(mn ? 64 : bk), (cuuint32_t)(mn ? bk : box), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUtensorMapSwizzle swz = (mn || bk == 64) ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(o.ptr),
+              dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool aligned16(const void* p, long long ld, int e) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * e) % 16 == 0;
+}
+
+long long round_up(long long v, long long m) { return (v + m - 1) / m * m; }
+
+// Bytes of the laid-out form of a rows x cols matrix.
+size_t operand_bytes(int dtype, long long rows, long long cols) {
+    return (size_t)round_up((dtype == VF_F32 ? 6 : 2) * rows * round_up(cols, 64), 256);
+}
+
+// Carves the workspace; hands out nullptr-based offsets too when base is nullptr.
+struct Carver {
+    uint8_t* base;
+    size_t used = 0;
+    uint8_t* take(size_t bytes) {
+        uint8_t* p = base + used;
+        used += (size_t)round_up((long long)bytes, 256);
+        return p;
+    }
+};
+
+// The operand as it is where TMA can read it (16-bit type, 16-byte rows), else a job that lays it out.
+Operand16 operand(int dtype, const void* src, long long ld, long long rows, int cols, Carver& w, PackJob* job) {
+    const int e = dtype == VF_F32 ? 4 : 2;
+    *job = PackJob{};
+    if (e == 2 && aligned16(src, ld, e) && ld < (1LL << 38)) return Operand16{src, rows, ld, cols};
+    job->src = src;
+    job->ld = ld;
+    job->rows = rows;
+    job->cols = cols;
+    job->vec = aligned16(src, ld, e);
+    job->ldp = round_up(cols, 64);
+    job->dst = (uint16_t*)w.take(operand_bytes(dtype, rows, cols));
+    job->blocks_c = (cols + PACK_COLS - 1) / PACK_COLS;
+    job->blocks = (rows + PACK_ROWS - 1) / PACK_ROWS * job->blocks_c;
+    return Operand16{job->dst, rows, job->ldp, cols};
+}
+
+cudaError_t launch_operands(int dtype, const GradJob& g, const PackJob& a, const PackJob& b, cudaStream_t s) {
+    const long long blocks = g.blocks + a.blocks + b.blocks;
+    if (blocks == 0) return cudaSuccess;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    switch (dtype) {
+        case VF_F32: linear_operands_k<float><<<(unsigned)blocks, PACK_THREADS, 0, s>>>(g, a, b); break;
+        case VF_BF16: linear_operands_k<__nv_bfloat16><<<(unsigned)blocks, PACK_THREADS, 0, s>>>(g, a, b); break;
+        default: linear_operands_k<__half><<<(unsigned)blocks, PACK_THREADS, 0, s>>>(g, a, b);
+    }
+    return cudaGetLastError();
+}
+
+struct Side {
+    Operand16 o;
+    bool mn;
+};
+
+int sm_count_() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return n;
+}
+
+template <typename T, int PL, int BN>
+cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int count, int sms, cudaStream_t s) {
+    constexpr int BK = block_k<PL>();
+    const bool bf16 = PL == 3 || std::is_same<T, __nv_bfloat16>::value;
+    CUtensorMap ma[2], mb[2];
+    int min_nk = 1 << 30;
+    P.tiles = 0;
+    for (int k = 0; k < count; ++k) {
+        TcProduct& p = P.p[k];
+        p.a_mn = A[k].mn;
+        p.b_mn = B[k].mn;
+        p.tiles_i = (int)((p.I + BM - 1) / BM);
+        p.tiles = (long long)p.tiles_i * ((p.J + BN - 1) / BN);
+        P.tiles += p.tiles;
+        min_nk = std::min(min_nk, p.nk);
+        if (!make_map(&ma[k], A[k].o, PL, A[k].mn, BK, BM, bf16) || !make_map(&mb[k], B[k].o, PL, B[k].mn, BK, BN, bf16))
+            return cudaErrorInvalidValue;
+    }
+    if (count == 0) memset(ma, 0, sizeof(ma)), memset(mb, 0, sizeof(mb));
+    if (count < 2) {
+        ma[1] = ma[0];
+        mb[1] = mb[0];
+        if (count == 1) P.p[1].tiles = 0;
+    }
+    // few tiles: split the reduction over a cluster, each CTA keeping at least two blocks of it
+    P.split = 1;
+    while (count > 0 && P.split < 8 && P.tiles * P.split * 2 <= sms && min_nk >= P.split * 4) P.split *= 2;
+    const int need = stage_bytes<PL, BN>();
+    P.stages = std::min(MAX_STAGES, (SMEM_LIMIT - 1024 - 1024 - STG_BYTES) / need);
+    size_t smem = 1024 + (size_t)P.stages * need + STG_BYTES;
+    auto kern = linear_tc_k<T, PL, BN>;
+    cudaError_t e = allow_dyn_smem((const void*)kern, SMEM_LIMIT - 1024);
+    if (e != cudaSuccess) return e;
+    long long grid = P.split > 1 ? P.tiles * P.split : std::min<long long>(P.tiles, sms);
+    if (P.tiles == 0) grid = std::min<long long>((P.N + EPI_THREADS - 1) / EPI_THREADS, sms);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(NUM_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = P.split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, ma[0], mb[0], ma[1], mb[1], P);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T, int PL>
+cudaError_t launch_pl(TcParams& P, const Side (&A)[2], const Side (&B)[2], int count, cudaStream_t s) {
+    const int sms = sm_count_();
+    if (sms == 0) return cudaErrorInvalidDevice;
+    long long J = 1;
+    bool mn = false;
+    for (int k = 0; k < count; ++k) {
+        J = std::max(J, P.p[k].J);
+        mn = mn || B[k].mn;
+    }
+    if (!mn && J <= 16) return launch_bn<T, PL, 16>(P, A, B, count, sms, s);
+    if (!mn && J <= 32) return launch_bn<T, PL, 32>(P, A, B, count, sms, s);
+    // 256 columns halve the operand reads per MMA; narrower tiles where they fill more of the SMs
+    auto tiles = [&](int bn) {
+        long long n = 0;
+        for (int k = 0; k < count; ++k) n += (P.p[k].I + BM - 1) / BM * ((P.p[k].J + bn - 1) / bn);
+        return n;
+    };
+    auto cost = [&](int bn) { return (tiles(bn) + sms - 1) / sms * (bn + 48); };
+    if (J > 128 && cost(256) <= cost(128) && cost(256) <= cost(64)) return launch_bn<T, PL, 256>(P, A, B, count, sms, s);
+    if (J > 64 && cost(128) <= cost(64)) return launch_bn<T, PL, 128>(P, A, B, count, sms, s);
+    return launch_bn<T, PL, 64>(P, A, B, count, sms, s);
+}
+
+cudaError_t launch_products(int dtype, TcParams& P, const Side (&A)[2], const Side (&B)[2], int count, cudaStream_t s) {
+    switch (dtype) {
+        case VF_F32: return launch_pl<float, 3>(P, A, B, count, s);
+        case VF_BF16: return launch_pl<__nv_bfloat16, 1>(P, A, B, count, s);
+        default: return launch_pl<__half, 1>(P, A, B, count, s);
+    }
+}
+
+int blocks_of(int dtype, long long t) {
+    const int bk = dtype == VF_F32 ? block_k<3>() : block_k<1>();
+    return (int)((t + bk - 1) / bk);
+}
+
+long long row_blocks(long long M) { return (M + PACK_ROWS - 1) / PACK_ROWS; }
+
+}  // namespace
+
+bool linear_tc_supported(long long M, int N, int K) { return M > 0 && N > 0 && K > 0; }
+
+size_t linear_tc_workspace(int dtype, long long M, int N, int K, bool grad) {
+    size_t n = operand_bytes(dtype, M, K) + operand_bytes(dtype, N, K);
+    if (grad) n += operand_bytes(dtype, M, N) + (size_t)round_up(row_blocks(M) * N * 4, 256);
+    return n;
+}
+
+cudaError_t launch_linear_tc(const LinearFwd& f, void* work, cudaStream_t s) {
+    const int e = f.dtype == VF_F32 ? 4 : 2;
+    Carver w{(uint8_t*)work};
+    PackJob jx, jw;
+    Side A[2] = {}, B[2] = {};
+    A[0] = Side{operand(f.dtype, f.W, f.ldw, f.N, f.K, w, &jw), false};
+    B[0] = Side{operand(f.dtype, f.x, f.ldx, f.M, f.K, w, &jx), false};
+    cudaError_t err = launch_operands(f.dtype, GradJob{}, jw, jx, s);
+    if (err != cudaSuccess) return err;
+    TcParams P{};
+    TcProduct& p = P.p[0];
+    p.I = f.N;
+    p.J = f.M;
+    p.nk = blocks_of(f.dtype, f.K);
+    p.out = f.y;
+    p.ldo = f.ldy;
+    p.bias = f.b;
+    p.res = f.r;
+    p.ldr = f.ldr;
+    p.zout = f.z;
+    p.ldz = f.ldz;
+    p.act = f.act;
+    p.vec = aligned16(f.y, f.ldy, e) && (f.r == nullptr || aligned16(f.r, f.ldr, e)) &&
+            (f.z == nullptr || aligned16(f.z, f.ldz, e));
+    return launch_products(f.dtype, P, A, B, 1, s);
+}
+
+cudaError_t launch_linear_grad_tc(const LinearGrad& f, void* work, cudaStream_t s) {
+    const int e = f.dtype == VF_F32 ? 4 : 2;
+    Carver w{(uint8_t*)work};
+    const bool products = f.dx != nullptr || f.dW != nullptr;
+    GradJob gj{};
+    gj.dy = f.dy;
+    gj.lddy = f.lddy;
+    gj.z = f.z;
+    gj.ldz = f.ldz;
+    gj.M = f.M;
+    gj.N = f.N;
+    gj.act = f.act;
+    gj.vec = aligned16(f.dy, f.lddy, e) && (f.act == VF_ACT_NONE || aligned16(f.z, f.ldz, e));
+    gj.dr = f.dr;
+    gj.lddr = f.lddr;
+    gj.vec_r = f.dr != nullptr && aligned16(f.dr, f.lddr, e);
+    Operand16 g{};
+    if (products) {
+        if (e == 2 && f.act == VF_ACT_NONE && aligned16(f.dy, f.lddy, e) && f.lddy < (1LL << 38)) {
+            g = Operand16{f.dy, f.M, f.lddy, f.N};  // dy is g, and TMA can read it
+        } else if (e == 2 && gj.vec_r && f.lddr < (1LL << 38)) {
+            g = Operand16{f.dr, f.M, f.lddr, f.N};  // dr is g
+        } else {
+            gj.ldp = round_up(f.N, 64);
+            gj.dst = (uint16_t*)w.take(operand_bytes(f.dtype, f.M, f.N));
+            g = Operand16{gj.dst, f.M, gj.ldp, f.N};
+        }
+    }
+    if (f.db != nullptr) gj.part = (float*)w.take((size_t)row_blocks(f.M) * f.N * 4);
+    if (gj.dst != nullptr || gj.dr != nullptr || gj.part != nullptr) {
+        gj.blocks_c = (f.N + PACK_COLS - 1) / PACK_COLS;
+        gj.blocks = row_blocks(f.M) * gj.blocks_c;
+    }
+    PackJob jw{}, jx{};
+    Side A[2] = {}, B[2] = {};
+    TcParams P{};
+    int count = 0;
+    if (f.dx != nullptr) {
+        A[count] = Side{operand(f.dtype, f.W, f.ldw, f.N, f.K, w, &jw), true};
+        B[count] = Side{g, false};
+        TcProduct& p = P.p[count++];
+        p.I = f.K;
+        p.J = f.M;
+        p.nk = blocks_of(f.dtype, f.N);
+        p.out = f.dx;
+        p.ldo = f.lddx;
+        p.vec = aligned16(f.dx, f.lddx, e);
+    }
+    if (f.dW != nullptr) {
+        A[count] = Side{operand(f.dtype, f.x, f.ldx, f.M, f.K, w, &jx), true};
+        B[count] = Side{g, true};
+        TcProduct& p = P.p[count++];
+        p.I = f.K;
+        p.J = f.N;
+        p.nk = blocks_of(f.dtype, f.M);
+        p.out = f.dW;
+        p.ldo = f.lddw;
+        p.vec = aligned16(f.dW, f.lddw, e);
+    }
+    cudaError_t err = launch_operands(f.dtype, gj, jw, jx, s);
+    if (err != cudaSuccess) return err;
+    if (count == 0 && f.db == nullptr) return cudaSuccess;
+    P.part = gj.part;
+    P.nparts = (int)row_blocks(f.M);
+    P.N = f.N;
+    P.db = f.db;
+    return launch_products(f.dtype, P, A, B, count, s);
+}
+
+// Reads and clears the flag of expired waits (the device is idle when this is called).
+cudaError_t ops_take_timeout(int* flag) {
+    cudaError_t e = cudaMemcpyFromSymbol(flag, g_ops_timeout, sizeof(int));
+    if (e != cudaSuccess || *flag == 0) return e;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_ops_timeout, &zero, sizeof(int));
+}
+
+}  // namespace vf

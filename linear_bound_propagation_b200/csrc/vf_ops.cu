@@ -119,6 +119,9 @@ int check_overlaps(const ClipList& l) {
     return VF_OK;
 }
 
+// Products too small to fill a few tensor-core tiles, and empty ones, run on the FFMA kernels.
+bool use_tc(long long M, int N, int K) { return linear_tc_supported(M, N, K) && (double)M * N * K >= 32768.0; }
+
 }  // namespace
 
 extern "C" {
@@ -127,8 +130,7 @@ int vf_linear_workspace(int dtype, long long M, int N, int K, int grad, size_t* 
     if (bytes == nullptr) return ops_fail(VF_ERR_ARG, "NULL pointer");
     OPS_TRY(check_kind(dtype, VF_ACT_NONE));
     OPS_TRY(check_sizes(M, N, K));
-    (void)grad;
-    *bytes = 0;
+    *bytes = use_tc(M, N, K) ? linear_tc_workspace(dtype, M, N, K, grad != 0) : 0;
     return VF_OK;
 }
 
@@ -144,9 +146,10 @@ int vf_linear(int dtype, int act, const void* x, long long ldx, const void* W, l
     if (r != nullptr) OPS_TRY(check_matrix("r", r, M, N, ldr, dtype));
     OPS_TRY(check_matrix("y", y, M, N, ldy, dtype));
     if (z != nullptr) OPS_TRY(check_matrix("z", z, M, N, ldz, dtype));
-    OPS_TRY(check_work(work, work_bytes, 0));
     const LinearFwd p{dtype, act, x, ldx, W, ldw, b, r, ldr, M, N, K, y, ldy, z, ldz};
-    return launched(launch_linear_ffma(p, (cudaStream_t)stream));
+    if (!use_tc(M, N, K)) return launched(launch_linear_ffma(p, (cudaStream_t)stream));
+    OPS_TRY(check_work(work, work_bytes, linear_tc_workspace(dtype, M, N, K, false)));
+    return launched(launch_linear_tc(p, work, (cudaStream_t)stream));
 }
 
 int vf_linear_grad(int dtype, int act, const void* dy, long long lddy, const void* z, long long ldz, const void* x,
@@ -167,14 +170,18 @@ int vf_linear_grad(int dtype, int act, const void* dy, long long lddy, const voi
     }
     OPS_TRY(check_vector("db", db, dtype));
     if (dr != nullptr) OPS_TRY(check_matrix("dr", dr, M, N, lddr, dtype));
-    OPS_TRY(check_work(work, work_bytes, 0));
     const LinearGrad p{dtype, act, dy, lddy, z, ldz, x, ldx, W, ldw, M, N, K, dx, lddx, dW, lddw, db, dr, lddr};
-    return launched(launch_linear_grad_ffma(p, (cudaStream_t)stream));
+    if (!use_tc(M, N, K)) return launched(launch_linear_grad_ffma(p, (cudaStream_t)stream));
+    OPS_TRY(check_work(work, work_bytes, linear_tc_workspace(dtype, M, N, K, true)));
+    return launched(launch_linear_grad_tc(p, work, (cudaStream_t)stream));
 }
 
 int vf_ops_check(void) {
-    const cudaError_t e = cudaDeviceSynchronize();
+    int timeout = 0;
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = ops_take_timeout(&timeout);
     if (e != cudaSuccess) return ops_fail(VF_ERR_CUDA, "asynchronous CUDA error: %s", cudaGetErrorString(e));
+    if (timeout) return ops_fail(VF_ERR_TIMEOUT, "a kernel gave up a bounded wait; its outputs are not valid");
     return VF_OK;
 }
 
