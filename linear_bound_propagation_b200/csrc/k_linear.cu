@@ -56,7 +56,7 @@ __device__ __forceinline__ void load_slice(const Operand<T>& o, long long r0, lo
         float v = 0.f;
         if (r0 + r < o.rows && t0 + t < Tn) {
             v = to_f32(o.p[(r0 + r) * o.sr + (t0 + t) * o.st]);
-            if (o.z != nullptr) v = act_grad(v, to_f32(o.z[(r0 + r) * o.zr + (t0 + t) * o.zt]), act);
+            if (o.z != nullptr) v = act_grad<sizeof(T) == 2>(v, to_f32(o.z[(r0 + r) * o.zr + (t0 + t) * o.zt]), act);
         }
         s[t][r] = v;
     }
@@ -94,7 +94,7 @@ __device__ void product_tile(const Product<T>& p, long long tile, int act_in, in
             float z = acc[u][v] + bias;
             if (p.res != nullptr) z += to_f32(p.res[j * p.ldr + i]);
             if (p.zout != nullptr) p.zout[j * p.ldz + i] = from_f32<T>(z);
-            p.out[j * p.ldo + i] = from_f32<T>(act_value(z, act_out));
+            p.out[j * p.ldo + i] = from_f32<T>(act_value<sizeof(T) == 2>(z, act_out));
         }
     }
 }
@@ -115,7 +115,7 @@ __device__ void column_tile(const Operand<T>& g, long long N, long long M, long 
     if (n < N)
         for (long long m = q; m < M; m += THREADS / 32) {
             float v = to_f32(g.p[m * g.st + n]);
-            if (g.z != nullptr) v = act_grad(v, to_f32(g.z[m * g.zt + n]), act);
+            if (g.z != nullptr) v = act_grad<sizeof(T) == 2>(v, to_f32(g.z[m * g.zt + n]), act);
             if (dr != nullptr) dr[m * lddr + n] = from_f32<T>(v);
             s += v;
         }

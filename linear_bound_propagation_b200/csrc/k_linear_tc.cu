@@ -95,6 +95,19 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a, uint64_t
         : "memory");
 }
 
+// Position in the ring of stages: slot and how often the ring has been passed. Kept as counters: the roles below are
+// single threads, for which a division per block would cost more than the block's MMAs.
+struct Ring {
+    int slot = 0;
+    uint32_t lap = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++slot == stages) {
+            slot = 0;
+            ++lap;
+        }
+    }
+};
+
 // Operand of rows x BK elements in shared memory. Contiguous along t: rows of BK elements (128 or 64 bytes, swizzled
 // over as many bytes), 8-row groups one after the other. Contiguous along i or j: atoms of 64 elements x BK steps of t,
 // 128-byte rows swizzled over 128 bytes, 8-step groups 1024 bytes apart, atoms BK * 128 bytes apart.
@@ -121,6 +134,19 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
                  : "memory");
 }
 
+// One lane of a converged warp. tcgen05 and TMA instructions take their operands from uniform registers: behind
+// elect.sync the compiler knows that a single lane runs and issues them back to back; behind `lane == 0` every MMA took
+// about 110 cycles to issue.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t on;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(on));
+    return on != 0;
+}
+
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -137,72 +163,117 @@ __device__ __forceinline__ float ld_cluster(uint32_t saddr, uint32_t rank) {
     return v;
 }
 
+__device__ __forceinline__ float4 ld_cluster4(uint32_t saddr, uint32_t rank) {
+    uint32_t a;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
 template <typename T>
 struct alignas(16) Pack8 {
     T v[8];
 };
 
-// Eight consecutive outputs i .. i + 7 of row j.
-template <typename T>
-__device__ __forceinline__ void finish8(const TcProduct& p, long long i, long long j, float (&v)[8], const float (&bias)[8]) {
-    const bool full = p.vec && i + 8 <= p.I;
-    if (p.res != nullptr) {
-        const T* r = (const T*)p.res + j * p.ldr + i;
-        if (full) {
-            const Pack8<T> w = *reinterpret_cast<const Pack8<T>*>(r);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] += to_f32(w.v[u]) + bias[u];
-        } else {
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (i + u < p.I) v[u] += to_f32(r[u]) + bias[u];
-        }
-    } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] += bias[u];
-    }
-    Pack8<T> w;
-    if (p.zout != nullptr) {
-        T* zp = (T*)p.zout + j * p.ldz + i;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) w.v[u] = from_f32<T>(v[u]);
-        if (full) {
-            *reinterpret_cast<Pack8<T>*>(zp) = w;
-        } else {
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (i + u < p.I) zp[u] = w.v[u];
-        }
-    }
-    switch (p.act) {
+template <typename T, int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
+    constexpr bool FAST = sizeof(T) == 2;
+    switch (act) {
         case VF_ACT_RELU:
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = act_value(v[u], VF_ACT_RELU);
+            for (int u = 0; u < N; ++u) v[u] = act_value<FAST>(v[u], VF_ACT_RELU);
             break;
         case VF_ACT_GELU:
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = act_value(v[u], VF_ACT_GELU);
+            for (int u = 0; u < N; ++u) v[u] = act_value<FAST>(v[u], VF_ACT_GELU);
             break;
         case VF_ACT_SILU:
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = act_value(v[u], VF_ACT_SILU);
+            for (int u = 0; u < N; ++u) v[u] = act_value<FAST>(v[u], VF_ACT_SILU);
             break;
         default: break;
     }
-    T* o = (T*)p.out + j * p.ldo + i;
+}
+
+// Rows that allow 16-byte accesses: eight consecutive outputs i .. i + 7 of row j per thread. The residual is loaded
+// ahead (res8) so that several rows' loads are in flight.
+template <typename T>
+__device__ __forceinline__ void res8(const TcProduct& p, long long i, long long j, Pack8<T>& w) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) w.v[u] = from_f32<T>(0.f);
+    if (p.res == nullptr || j >= p.J) return;
+    const T* r = (const T*)p.res + j * p.ldr + i;
+    if (i + 8 <= p.I) {
+        w = *reinterpret_cast<const Pack8<T>*>(r);
+    } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (i + u < p.I) w.v[u] = r[u];
+    }
+}
+template <typename T>
+__device__ __forceinline__ void put8(T* o, int n, const float (&v)[8]) {
+    Pack8<T> w;
 #pragma unroll
     for (int u = 0; u < 8; ++u) w.v[u] = from_f32<T>(v[u]);
-    if (full) {
+    if (n >= 8) {
         *reinterpret_cast<Pack8<T>*>(o) = w;
     } else {
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-            if (i + u < p.I) o[u] = w.v[u];
+            if (u < n) o[u] = w.v[u];
     }
 }
+template <typename T>
+__device__ __forceinline__ void finish8(const TcProduct& p, long long i, long long j, float (&v)[8], const float (&bias)[8],
+                                        const Pack8<T>& r) {
+    const int n = (int)min(8LL, p.I - i);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] += bias[u] + to_f32(r.v[u]);
+    if (p.zout != nullptr) put8<T>((T*)p.zout + j * p.ldz + i, n, v);
+    activate<T>(v, p.act);
+    put8<T>((T*)p.out + j * p.ldo + i, n, v);
+}
 
-constexpr int STG_LD = 36;                             // floats per staged column: 16-byte rows, conflict-free reads
-constexpr int STG_BYTES = 8 * 8 * STG_LD * 4;          // eight warps x eight columns
+// Any other rows: one element i of N rows j .. j + N - 1 per thread, a warp's lanes on consecutive elements.
+template <typename T, int N>
+__device__ __forceinline__ void finish_lane(const TcProduct& p, long long i, long long j, float (&v)[N], float bias) {
+    if (i >= p.I) return;
+    if (p.res != nullptr) {
+        float r[N];
+#pragma unroll
+        for (int u = 0; u < N; ++u) r[u] = j + u < p.J ? to_f32(((const T*)p.res)[(j + u) * p.ldr + i]) : 0.f;
+#pragma unroll
+        for (int u = 0; u < N; ++u) v[u] += bias + r[u];
+    } else {
+#pragma unroll
+        for (int u = 0; u < N; ++u) v[u] += bias;
+    }
+    if (p.zout != nullptr)
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            if (j + u < p.J) ((T*)p.zout)[(j + u) * p.ldz + i] = from_f32<T>(v[u]);
+    activate<T>(v, p.act);
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+        if (j + u < p.J) ((T*)p.out)[(j + u) * p.ldo + i] = from_f32<T>(v[u]);
+}
+
+// Staging of the epilogue: a warp's 32 lanes x COLS columns, so that a thread gets eight lanes of one column. 36 floats
+// per column: 16-byte rows whose reads meet no bank twice. The 256-column fp32 tile leaves room for eight columns only.
+constexpr int STG_LD = 36;
+template <int PL, int BN>
+constexpr int stg_cols() {
+    return BN <= 64 ? BN / 2 : (PL == 3 && BN == 256 ? 8 : 16);
+}
+template <int PL, int BN>
+constexpr int stg_bytes() {
+    return 8 * stg_cols<PL, BN>() * STG_LD * 4;
+}
 
 template <int PL, int BN>
 constexpr int stage_bytes() {
@@ -222,6 +293,7 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
     constexpr int USED_COLS = PL == 3 ? 2 * ACC_COLS : ACC_COLS;
     constexpr int TMEM_COLS = USED_COLS < 32 ? 32 : USED_COLS;
     constexpr int HALF = BN / 2;
+    constexpr int COLS = stg_cols<PL, BN>();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], cor_empty[2], done_bar;
@@ -261,104 +333,104 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
     volatile int* abort_flag = &abort_sh;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             // ------------------------------------------------------------------------------- TMA producer
-            long long g = 0;
+            Ring g;
             for (long long t = tile0; t < P.tiles && !*abort_flag; t += tile_step) {
                 const int w = t >= P.p[0].tiles;
                 const TcProduct& p = P.p[w];
-                const long long u = w ? t - P.p[0].tiles : t;
-                const int i0 = (int)(u % p.tiles_i) * BM, j0 = (int)(u / p.tiles_i) * BN;
+                const int u = (int)(w ? t - P.p[0].tiles : t);
+                const int i0 = u % p.tiles_i * BM, j0 = u / p.tiles_i * BN;
                 const CUtensorMap* ma = w ? &tmA1 : &tmA0;
                 const CUtensorMap* mb = w ? &tmB1 : &tmB0;
-                const int kb1 = (int)((long long)p.nk * (rank + 1) / S);
-                for (int kb = (int)((long long)p.nk * rank / S); kb < kb1; ++kb, ++g) {
-                    const int s = (int)(g % NS);
-                    if (g >= NS && !mbar_wait(&empty[s], (uint32_t)((g / NS) - 1) & 1, abort_flag)) break;
-                    uint8_t* st = base + (size_t)s * STAGE;
-                    mbar_expect_tx(&full[s], STAGE);
+                const int kb0 = (int)((long long)p.nk * rank / S), kb1 = (int)((long long)p.nk * (rank + 1) / S);
+                const bool a_mn = p.a_mn, b_mn = p.b_mn;
+                for (int kb = kb0; kb < kb1; ++kb, g.next(NS)) {
+                    if (g.lap > 0 && !mbar_wait(&empty[g.slot], (g.lap - 1) & 1, abort_flag)) break;
+                    uint8_t* st = base + (size_t)g.slot * STAGE;
+                    uint64_t* bar = &full[g.slot];
+                    mbar_expect_tx(bar, STAGE);
 #pragma unroll
                     for (int q = 0; q < PL; ++q) {
                         uint8_t* a = st + q * A_PLANE;
                         uint8_t* b = st + PL * A_PLANE + q * B_PLANE;
-                        if (p.a_mn) {
+                        if (a_mn) {
 #pragma unroll
                             for (int c = 0; c < BM / 64; ++c)
-                                tma_load_3d(a + c * BK * 128, ma, &full[s], i0 + c * 64, kb * BK, q);
+                                tma_load_3d(a + c * BK * 128, ma, bar, i0 + c * 64, kb * BK, q);
                         } else {
-                            tma_load_3d(a, ma, &full[s], kb * BK, i0, q);
+                            tma_load_3d(a, ma, bar, kb * BK, i0, q);
                         }
-                        if (BN >= 64 && p.b_mn) {
+                        if (BN >= 64 && b_mn) {
 #pragma unroll
                             for (int c = 0; c < BN / 64; ++c)
-                                tma_load_3d(b + c * BK * 128, mb, &full[s], j0 + c * 64, kb * BK, q);
+                                tma_load_3d(b + c * BK * 128, mb, bar, j0 + c * 64, kb * BK, q);
                         } else {
-                            tma_load_3d(b, mb, &full[s], kb * BK, j0, q);
+                            tma_load_3d(b, mb, bar, kb * BK, j0, q);
                         }
                     }
                 }
             }
-            if (*abort_flag)  // wait (bounded) for copies that nobody will consume
-                for (long long h = (g > NS ? g - NS : 0); h < g; ++h) {
+            if (*abort_flag) {  // wait (bounded) for copies that nobody will consume: the last lap's
+                for (int h = 0; h < NS; ++h) {
+                    const uint32_t laps = g.lap + (h < g.slot ? 1 : 0);  // copies issued into slot h
                     const long long t0 = clock64();
-                    while (!mbar_test(&full[h % NS], (uint32_t)(h / NS) & 1) && clock64() - t0 < WAIT_CYCLES) {
+                    while (laps > 0 && !mbar_test(&full[h], (laps - 1) & 1) && clock64() - t0 < WAIT_CYCLES) {
                     }
                 }
+            }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             // --------------------------------------------------------------------------------- MMA issuer
-            long long g = 0, chunks = 0, tiles = 0;
+            Ring g, chunk, tile;  // stages; accumulator sets (one chunk each); small-product sets (one tile each)
             bool ok = true;
-            for (long long t = tile0; ok && t < P.tiles && !*abort_flag; t += tile_step, ++tiles) {
+            for (long long t = tile0; ok && t < P.tiles && !*abort_flag; t += tile_step, tile.next(NB)) {
                 const TcProduct& p = P.p[t >= P.p[0].tiles];
                 const int kb0 = (int)((long long)p.nk * rank / S), kb1 = (int)((long long)p.nk * (rank + 1) / S);
-                const uint32_t fmt = (PL == 3 || sizeof(T) == 4 || std::is_same<T, __nv_bfloat16>::value) ? 1u : 0u;
-                const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)p.a_mn << 15) |
-                                       ((uint32_t)p.b_mn << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
-                // bytes between the K = 16 steps of a stage
-                const uint32_t step_a = p.a_mn ? 2048 : 32, step_b = p.b_mn ? 2048 : 32;
-                const uint32_t cor = tmem + ACC_COLS + (uint32_t)(tiles % NB) * BN;
-                for (int kb = kb0; kb < kb1; ++kb, ++g) {
-                    const int s = (int)(g % NS);
-                    if (!(ok = mbar_wait(&full[s], (uint32_t)(g / NS) & 1, abort_flag))) break;
-                    const bool first = PL == 3 ? (kb - kb0) % CHUNK == 0 : kb == kb0;
-                    const bool last = kb + 1 == kb1 || (PL == 3 && (kb - kb0) % CHUNK == CHUNK - 1);
-                    const uint32_t d = tmem + (uint32_t)(chunks % NB) * BN;
-                    const uint32_t sa = smem_u32(base + (size_t)s * STAGE), sb = sa + PL * A_PLANE;
-                    tc_fence_after();
+                const int a_mn = p.a_mn, b_mn = p.b_mn;
+                const uint32_t fmt = (PL == 3 || std::is_same<T, __nv_bfloat16>::value) ? 1u : 0u;
+                const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)a_mn << 15) |
+                                       ((uint32_t)b_mn << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+                // descriptors of the ring's first slot, and their steps (16-byte units) per K = 16, plane and slot
+                const uint64_t a0 = operand_desc<BK>(smem_u32(base), a_mn);
+                const uint64_t b0 = operand_desc<BK>(smem_u32(base) + PL * A_PLANE, b_mn);
+                const uint32_t step_a = (a_mn ? 2048 : 32) / 16, step_b = (b_mn ? 2048 : 32) / 16;
+                const uint32_t cor = tmem + ACC_COLS + (uint32_t)tile.slot * BN;
+                int in_chunk = 0;
+                for (int kb = kb0; kb < kb1; ++kb, g.next(NS)) {
+                    if (!(ok = mbar_wait(&full[g.slot], g.lap & 1, abort_flag))) break;
+                    const uint32_t d = tmem + (uint32_t)chunk.slot * BN;
+                    const uint64_t ah = a0 + (uint32_t)(g.slot * (STAGE / 16)), bh = b0 + (uint32_t)(g.slot * (STAGE / 16));
                     if (PL == 3) {
-                        if (kb == kb0 && tiles >= NB &&
-                            !(ok = mbar_wait(&cor_empty[tiles % NB], (uint32_t)(tiles / NB - 1) & 1, abort_flag)))
+                        if (kb == kb0 && tile.lap > 0 &&
+                            !(ok = mbar_wait(&cor_empty[tile.slot], (tile.lap - 1) & 1, abort_flag)))
                             break;
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk) {
-                            const uint32_t oa = sa + kk * step_a, ob = sb + kk * step_b;
-                            const uint64_t ah = operand_desc<BK>(oa, p.a_mn), bh = operand_desc<BK>(ob, p.b_mn);
-                            const uint64_t am = operand_desc<BK>(oa + A_PLANE, p.a_mn);
-                            const uint64_t bm = operand_desc<BK>(ob + B_PLANE, p.b_mn);
-                            const uint64_t al = operand_desc<BK>(oa + 2 * A_PLANE, p.a_mn);
-                            const uint64_t bl = operand_desc<BK>(ob + 2 * B_PLANE, p.b_mn);
-                            mma_f16_ss(cor, al, bh, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
-                            mma_f16_ss(cor, ah, bl, idesc, 1u);
-                            mma_f16_ss(cor, am, bm, idesc, 1u);
-                            mma_f16_ss(cor, am, bh, idesc, 1u);
-                            mma_f16_ss(cor, ah, bm, idesc, 1u);
+                            const uint64_t h = ah + kk * step_a, m = h + A_PLANE / 16, l = m + A_PLANE / 16;
+                            const uint64_t H = bh + kk * step_b, M = H + B_PLANE / 16, L = M + B_PLANE / 16;
+                            mma_f16_ss(cor, l, H, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+                            mma_f16_ss(cor, h, L, idesc, 1u);
+                            mma_f16_ss(cor, m, M, idesc, 1u);
+                            mma_f16_ss(cor, m, H, idesc, 1u);
+                            mma_f16_ss(cor, h, M, idesc, 1u);
                         }
                     }
-                    if (first && chunks >= NB &&
-                        !(ok = mbar_wait(&acc_empty[chunks % NB], (uint32_t)(chunks / NB - 1) & 1, abort_flag)))
+                    if (in_chunk == 0 && chunk.lap > 0 &&
+                        !(ok = mbar_wait(&acc_empty[chunk.slot], (chunk.lap - 1) & 1, abort_flag)))
                         break;
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk)
-                        mma_f16_ss(d, operand_desc<BK>(sa + kk * step_a, p.a_mn), operand_desc<BK>(sb + kk * step_b, p.b_mn),
-                                   idesc, (!first || kk > 0) ? 1u : 0u);
-                    mma_commit(&empty[s]);
-                    if (last) {
-                        mma_commit(&acc_full[chunks % NB]);
-                        ++chunks;
+                        mma_f16_ss(d, ah + kk * step_a, bh + kk * step_b, idesc, (in_chunk > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit(&empty[g.slot]);
+                    ++in_chunk;
+                    if (kb + 1 == kb1 || (PL == 3 && in_chunk == CHUNK)) {
+                        mma_commit(&acc_full[chunk.slot]);
+                        chunk.next(NB);
+                        in_chunk = 0;
                     }
                 }
             }
@@ -372,7 +444,7 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
         // ------------------------------------------------------------------------------------- epilogue
         const int q = warp & 3, half = warp >= 6;
         const uint32_t lane_base = ((uint32_t)(q * 32) << 16) + half * HALF;
-        float* stg = reinterpret_cast<float*>(base + (size_t)NS * STAGE) + (warp - 2) * 8 * STG_LD;
+        float* stg = reinterpret_cast<float*>(base + (size_t)NS * STAGE) + (warp - 2) * COLS * STG_LD;
         if (P.db != nullptr)
             for (long long n = (long long)blockIdx.x * EPI_THREADS + threadIdx.x - 64; n < P.N;
                  n += (long long)gridDim.x * EPI_THREADS) {
@@ -381,14 +453,14 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
                 for (int k = 0; k < P.nparts; ++k) s += P.part[(long long)k * P.N + n];
                 ((T*)P.db)[n] = from_f32<T>(s);
             }
-        long long chunks = 0, tiles = 0;
+        Ring chunk, tile;  // as the MMA issuer counts them
         const int tj = lane >> 2, ti = (lane & 3) * 8;  // this thread's part of an 8-column, 32-lane block
-        for (long long t = tile0; t < P.tiles; t += tile_step, ++tiles) {
+        for (long long t = tile0; t < P.tiles; t += tile_step, tile.next(NB)) {
             const int w = t >= P.p[0].tiles;
             const TcProduct& p = P.p[w];
-            const long long u = w ? t - P.p[0].tiles : t;
-            const long long i0 = (u % p.tiles_i) * BM, j0 = (u / p.tiles_i) * BN + half * HALF;
-            const long long i = i0 + q * 32 + ti;
+            const int u = (int)(w ? t - P.p[0].tiles : t);
+            const int i0 = u % p.tiles_i * BM, j0 = u / p.tiles_i * BN + half * HALF;
+            const long long i = (long long)i0 + q * 32 + ti;
             float bias[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -401,14 +473,13 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
                 for (int c = 0; c < HALF; ++c) acc[c] = 0.f;
                 const int nc = (kb1 - kb0 + CHUNK - 1) / CHUNK;
                 bool alive = true;
-                for (int ch = 0; ch < nc; ++ch, ++chunks) {
-                    const int b = (int)(chunks % NB);
-                    if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[b], (uint32_t)(chunks / NB) & 1, abort_flag))) {
+                for (int ch = 0; ch < nc; ++ch) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[chunk.slot], chunk.lap & 1, abort_flag))) {
                         alive = false;
                         break;
                     }
                     tc_fence_after();
-                    acc_t = tmem + lane_base + b * BN;
+                    acc_t = tmem + lane_base + chunk.slot * BN;
 #pragma unroll
                     for (int c = 0; c < HALF; c += 8) {
                         uint32_t v[8];
@@ -417,14 +488,14 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
 #pragma unroll
                         for (int k = 0; k < 8; ++k) acc[c + k] += __uint_as_float(v[k]);
                     }
-                    if (ch + 1 < nc) {
+                    if (ch + 1 < nc) {  // the last chunk's columns are released after the epilogue
                         tc_fence_before();
-                        mbar_arrive(&acc_empty[b]);
+                        mbar_arrive(&acc_empty[chunk.slot]);
+                        chunk.next(NB);
                     }
                 }
                 if (!alive) break;
-                --chunks;  // the last chunk's columns are released after the epilogue
-                const uint32_t cor_t = tmem + lane_base + ACC_COLS + (uint32_t)(tiles % NB) * BN;
+                const uint32_t cor_t = tmem + lane_base + ACC_COLS + tile.slot * BN;
 #pragma unroll
                 for (int c = 0; c < HALF; c += 8) {  // the finished sums go back to TMEM for the rolled loop below
                     uint32_t v[8];
@@ -436,27 +507,55 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
-                mbar_arrive(&cor_empty[tiles % NB]);
+                mbar_arrive(&cor_empty[tile.slot]);
             } else {
-                const int b = (int)(chunks % NB);
-                if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[b], (uint32_t)(chunks / NB) & 1, abort_flag))) break;
+                if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[chunk.slot], chunk.lap & 1, abort_flag))) break;
                 tc_fence_after();
-                acc_t = tmem + lane_base + b * BN;
+                acc_t = tmem + lane_base + chunk.slot * BN;
             }
             if (S == 1) {
-                for (int c = 0; c < HALF; c += 8) {
-                    uint32_t v[8];
-                    tmem_ld<8>(acc_t + c, v);
-                    tmem_wait_ld();
+                if (p.vec) {
+                    // 32 columns (or all) per round: their residual rows and accumulators are loaded together
+                    constexpr int ROUND = HALF < 32 ? HALF : 32;
+#pragma unroll 1
+                    for (int c = 0; c < HALF; c += ROUND) {
+                        Pack8<T> r[ROUND / 8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) stg[k * STG_LD + lane] = __uint_as_float(v[k]);
-                    __syncwarp();
-                    const float4 lo = *reinterpret_cast<const float4*>(stg + tj * STG_LD + ti);
-                    const float4 hi = *reinterpret_cast<const float4*>(stg + tj * STG_LD + ti + 4);
-                    float o[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                    __syncwarp();
-                    const long long j = j0 + c + tj;
-                    if (i < p.I && j < p.J) finish8<T>(p, i, j, o, bias);
+                        for (int k = 0; k < ROUND / 8; ++k) res8<T>(p, i, (long long)j0 + c + k * 8 + tj, r[k]);
+#pragma unroll
+                        for (int d = 0; d < ROUND; d += COLS) {
+                            uint32_t v[COLS / 8][8];
+#pragma unroll
+                            for (int k = 0; k < COLS / 8; ++k) tmem_ld<8>(acc_t + c + d + k * 8, v[k]);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < COLS; ++k) stg[k * STG_LD + lane] = __uint_as_float(v[k / 8][k % 8]);
+                            __syncwarp();
+#pragma unroll
+                            for (int k = 0; k < COLS / 8; ++k) {
+                                const float* q8 = stg + (k * 8 + tj) * STG_LD + ti;
+                                const float4 lo = *reinterpret_cast<const float4*>(q8);
+                                const float4 hi = *reinterpret_cast<const float4*>(q8 + 4);
+                                float o[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                                const long long j = (long long)j0 + c + d + k * 8 + tj;
+                                if (i < p.I && j < p.J) finish8<T>(p, i, j, o, bias, r[d / 8 + k]);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                } else {
+                    const long long il = (long long)i0 + q * 32 + lane;
+                    const float bl = (p.bias != nullptr && il < p.I) ? to_f32(((const T*)p.bias)[il]) : 0.f;
+#pragma unroll 1
+                    for (int c = 0; c < HALF; c += 8) {
+                        uint32_t v[8];
+                        tmem_ld<8>(acc_t + c, v);
+                        tmem_wait_ld();
+                        float o[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[k] = __uint_as_float(v[k]);
+                        finish_lane<T, 8>(p, il, (long long)j0 + c, o, bl);
+                    }
                 }
             } else {
                 // every stage of this tile has been consumed: its shared memory takes the partial tile
@@ -470,8 +569,8 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
                 }
             }
             tc_fence_before();
-            mbar_arrive(&acc_empty[chunks % NB]);
-            ++chunks;
+            mbar_arrive(&acc_empty[chunk.slot]);
+            chunk.next(NB);
         }
     }
 
@@ -482,26 +581,57 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
         if (warp >= 2 && tile0 < P.tiles) {
             const int w = tile0 >= P.p[0].tiles;
             const TcProduct& p = P.p[w];
-            const long long u = w ? tile0 - P.p[0].tiles : tile0;
-            const long long i0 = (u % p.tiles_i) * BM, j0 = (u / p.tiles_i) * BN;
+            const int u = (int)(w ? tile0 - P.p[0].tiles : tile0);
+            const int i0 = u % p.tiles_i * BM, j0 = u / p.tiles_i * BN;
             const uint32_t part = smem_u32(base);
             const int c0 = BN * (int)rank / S, c1 = BN * ((int)rank + 1) / S;
-            // a thread takes eight lanes of a column: 16 threads per column, 16 columns at a time
-            const int e = threadIdx.x - 64;
-            const long long i = i0 + (e & 15) * 8;
-            for (int c = c0 + (e >> 4); c < c1; c += EPI_THREADS / 16) {
-                const long long j = j0 + c;
-                if (i >= p.I || j >= p.J) continue;
-                float o[8], bias[8];
+            // all ranks' loads of a thread's share are issued before the first is used
+            if (p.vec) {  // eight lanes of a column per thread
+                const int e = threadIdx.x - 64;
+                const long long i = (long long)i0 + (e & 15) * 8;
+                float bias[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    o[k] = 0.f;
+                for (int k = 0; k < 8; ++k)
                     bias[k] = (p.bias != nullptr && i + k < p.I) ? to_f32(((const T*)p.bias)[i + k]) : 0.f;
-                }
-                for (int r = 0; r < S; ++r)
+                for (int c = c0 + (e >> 4); c < c1; c += EPI_THREADS / 16) {
+                    const long long j = (long long)j0 + c;
+                    if (i >= p.I || j >= p.J) continue;
+                    Pack8<T> r;
+                    res8<T>(p, i, j, r);
+                    float4 x[8][2];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] += ld_cluster(part + (c * BM + (e & 15) * 8 + k) * 4, r);
-                finish8<T>(p, i, j, o, bias);
+                    for (int k = 0; k < 8; ++k)
+                        if (k < S) {
+                            x[k][0] = ld_cluster4(part + (c * BM + (e & 15) * 8) * 4, k);
+                            x[k][1] = ld_cluster4(part + (c * BM + (e & 15) * 8 + 4) * 4, k);
+                        }
+                    float o[8] = {};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < S) {
+                            o[0] += x[k][0].x, o[1] += x[k][0].y, o[2] += x[k][0].z, o[3] += x[k][0].w;
+                            o[4] += x[k][1].x, o[5] += x[k][1].y, o[6] += x[k][1].z, o[7] += x[k][1].w;
+                        }
+                    finish8<T>(p, i, j, o, bias, r);
+                }
+            } else {  // four lanes, 32 apart, of a column per thread
+                for (int c = c0 + warp - 2; c < c1; c += EPI_THREADS / 32) {
+                    const long long j = (long long)j0 + c;
+                    if (j >= p.J) continue;
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        const long long i = (long long)i0 + k * 32 + lane;
+                        float x[8], o[1] = {0.f};
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            if (r < S) x[r] = ld_cluster(part + (c * BM + k * 32 + lane) * 4, r);
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            if (r < S) o[0] += x[r];
+                        const float bl = (p.bias != nullptr && i < p.I) ? to_f32(((const T*)p.bias)[i]) : 0.f;
+                        finish_lane<T, 1>(p, i, j, o, bl);
+                    }
+                }
             }
         }
         __syncwarp();
@@ -573,19 +703,19 @@ struct PackJob {
     int cols, vec;
     uint16_t* dst;
     long long ldp;
-    long long blocks;  // of PACK_ROWS rows x PACK_COLS columns
-    int blocks_c;
+    long long blocks;  // of 8 * steps rows x PACK_COLS columns
+    int blocks_c, steps;
 };
-constexpr int PACK_ROWS = 64, PACK_COLS = 256, PACK_THREADS = 256;
+constexpr int PACK_COLS = 256, PACK_THREADS = 256;
 
 template <typename T>
 __device__ void pack_block(const PackJob& j, long long blk) {
-    const long long r0 = blk / j.blocks_c * PACK_ROWS + (threadIdx.x >> 5);
+    const long long r0 = blk / j.blocks_c * (8 * j.steps) + (threadIdx.x >> 5);
     const int c = (int)(blk % j.blocks_c) * PACK_COLS + (threadIdx.x & 31) * 8;
     if (c >= j.cols) return;
     const long long plane = j.rows * j.ldp;
 #pragma unroll 4
-    for (int k = 0; k < PACK_ROWS / 8; ++k) {
+    for (int k = 0; k < j.steps; ++k) {
         const long long r = r0 + k * 8;
         if (r >= j.rows) break;
         float v[8];
@@ -594,7 +724,7 @@ __device__ void pack_block(const PackJob& j, long long blk) {
     }
 }
 
-// g = dy act'(z) of PACK_ROWS rows x PACK_COLS columns: to the operand (dst, unless g is dy itself), to dr, and its column sums
+// g = dy act'(z) of 8 * steps rows x PACK_COLS columns: to the operand (dst, unless g is dy itself), to dr, and its column sums
 // over the rows, in fp32, to part[row block][N].
 struct GradJob {
     const void* dy;
@@ -609,7 +739,7 @@ struct GradJob {
     long long lddr;
     float* part;  // or nullptr
     long long blocks;
-    int blocks_c;
+    int blocks_c, steps;
 };
 
 template <typename T>
@@ -622,8 +752,8 @@ __device__ void grad_block(const GradJob& j, long long blk) {
     if (c < j.N) {
         const int n = j.N - c;
 #pragma unroll 2
-        for (int k = 0; k < PACK_ROWS / 8; ++k) {
-            const long long r = rb * PACK_ROWS + w + k * 8;
+        for (int k = 0; k < j.steps; ++k) {
+            const long long r = rb * (8 * j.steps) + w + k * 8;
             if (r >= j.M) break;
             float v[8];
             load8((const T*)j.dy + r * j.lddy + c, n, j.vec, v);
@@ -633,15 +763,15 @@ __device__ void grad_block(const GradJob& j, long long blk) {
                 switch (j.act) {
                     case VF_ACT_RELU:
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) v[u] = act_grad(v[u], z[u], VF_ACT_RELU);
+                        for (int u = 0; u < 8; ++u) v[u] = act_grad<sizeof(T) == 2>(v[u], z[u], VF_ACT_RELU);
                         break;
                     case VF_ACT_GELU:
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) v[u] = act_grad(v[u], z[u], VF_ACT_GELU);
+                        for (int u = 0; u < 8; ++u) v[u] = act_grad<sizeof(T) == 2>(v[u], z[u], VF_ACT_GELU);
                         break;
                     default:
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) v[u] = act_grad(v[u], z[u], VF_ACT_SILU);
+                        for (int u = 0; u < 8; ++u) v[u] = act_grad<sizeof(T) == 2>(v[u], z[u], VF_ACT_SILU);
                 }
             }
             if (j.dst != nullptr) store_operand<T>(j.dst + r * j.ldp + c, j.M * j.ldp, v);
@@ -732,6 +862,14 @@ bool aligned16(const void* p, long long ld, int e) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * e) % 16 == 0;
 }
 
+// Rows of a block are 8 * steps: 64, or fewer (down to 8) until the blocks fill the SMs. Depends on the sizes alone, so
+// that column sums are added in the same order on every device.
+int pack_steps(long long rows, int blocks_c) {
+    int steps = 8;
+    while (steps > 1 && (rows + 8 * steps - 1) / (8 * steps) * blocks_c < 592) steps /= 2;
+    return steps;
+}
+
 long long round_up(long long v, long long m) { return (v + m - 1) / m * m; }
 
 // Bytes of the laid-out form of a rows x cols matrix.
@@ -763,7 +901,8 @@ Operand16 operand(int dtype, const void* src, long long ld, long long rows, int 
     job->ldp = round_up(cols, 64);
     job->dst = (uint16_t*)w.take(operand_bytes(dtype, rows, cols));
     job->blocks_c = (cols + PACK_COLS - 1) / PACK_COLS;
-    job->blocks = (rows + PACK_ROWS - 1) / PACK_ROWS * job->blocks_c;
+    job->steps = pack_steps(rows, job->blocks_c);
+    job->blocks = (rows + 8 * job->steps - 1) / (8 * job->steps) * job->blocks_c;
     return Operand16{job->dst, rows, job->ldp, cols};
 }
 
@@ -806,6 +945,7 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
         p.tiles = (long long)p.tiles_i * ((p.J + BN - 1) / BN);
         P.tiles += p.tiles;
         min_nk = std::min(min_nk, p.nk);
+        if (P.tiles > 0x7fffffffLL) return cudaErrorInvalidValue;  // tile numbers of a product are ints
         if (!make_map(&ma[k], A[k].o, PL, A[k].mn, BK, BM, bf16) || !make_map(&mb[k], B[k].o, PL, B[k].mn, BK, BN, bf16))
             return cudaErrorInvalidValue;
     }
@@ -819,8 +959,8 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
     P.split = 1;
     while (count > 0 && P.split < 8 && P.tiles * P.split * 2 <= sms && min_nk >= P.split * 4) P.split *= 2;
     const int need = stage_bytes<PL, BN>();
-    P.stages = std::min(MAX_STAGES, (SMEM_LIMIT - 1024 - 1024 - STG_BYTES) / need);
-    size_t smem = 1024 + (size_t)P.stages * need + STG_BYTES;
+    P.stages = std::min(MAX_STAGES, (SMEM_LIMIT - 1024 - 1024 - stg_bytes<PL, BN>()) / need);
+    size_t smem = 1024 + (size_t)P.stages * need + stg_bytes<PL, BN>();
     auto kern = linear_tc_k<T, PL, BN>;
     cudaError_t e = allow_dyn_smem((const void*)kern, SMEM_LIMIT - 1024);
     if (e != cudaSuccess) return e;
@@ -878,7 +1018,11 @@ int blocks_of(int dtype, long long t) {
     return (int)((t + bk - 1) / bk);
 }
 
-long long row_blocks(long long M) { return (M + PACK_ROWS - 1) / PACK_ROWS; }
+int col_blocks(int N) { return (N + PACK_COLS - 1) / PACK_COLS; }
+long long row_blocks(long long M, int N) {
+    const int rows = 8 * pack_steps(M, col_blocks(N));
+    return (M + rows - 1) / rows;
+}
 
 }  // namespace
 
@@ -886,7 +1030,7 @@ bool linear_tc_supported(long long M, int N, int K) { return M > 0 && N > 0 && K
 
 size_t linear_tc_workspace(int dtype, long long M, int N, int K, bool grad) {
     size_t n = operand_bytes(dtype, M, K) + operand_bytes(dtype, N, K);
-    if (grad) n += operand_bytes(dtype, M, N) + (size_t)round_up(row_blocks(M) * N * 4, 256);
+    if (grad) n += operand_bytes(dtype, M, N) + (size_t)round_up(row_blocks(M, N) * N * 4, 256);
     return n;
 }
 
@@ -945,10 +1089,11 @@ cudaError_t launch_linear_grad_tc(const LinearGrad& f, void* work, cudaStream_t 
             g = Operand16{gj.dst, f.M, gj.ldp, f.N};
         }
     }
-    if (f.db != nullptr) gj.part = (float*)w.take((size_t)row_blocks(f.M) * f.N * 4);
+    if (f.db != nullptr) gj.part = (float*)w.take((size_t)row_blocks(f.M, f.N) * f.N * 4);
     if (gj.dst != nullptr || gj.dr != nullptr || gj.part != nullptr) {
-        gj.blocks_c = (f.N + PACK_COLS - 1) / PACK_COLS;
-        gj.blocks = row_blocks(f.M) * gj.blocks_c;
+        gj.blocks_c = col_blocks(f.N);
+        gj.steps = pack_steps(f.M, gj.blocks_c);
+        gj.blocks = row_blocks(f.M, f.N) * gj.blocks_c;
     }
     PackJob jw{}, jx{};
     Side A[2] = {}, B[2] = {};
@@ -980,7 +1125,7 @@ cudaError_t launch_linear_grad_tc(const LinearGrad& f, void* work, cudaStream_t 
     if (err != cudaSuccess) return err;
     if (count == 0 && f.db == nullptr) return cudaSuccess;
     P.part = gj.part;
-    P.nparts = (int)row_blocks(f.M);
+    P.nparts = (int)row_blocks(f.M, f.N);
     P.N = f.N;
     P.db = f.db;
     return launch_products(f.dtype, P, A, B, count, s);
