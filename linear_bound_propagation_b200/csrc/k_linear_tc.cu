@@ -15,8 +15,8 @@
 // a sum of positive terms over 512 MMAs comes out 1e-5 low), so the five small products go to an accumulator of their own, and
 // the h h accumulator is added to registers, rounding to nearest, every CHUNK of the reduction.
 //
-// Roles (10 warps, one CTA per SM, persistent over the tiles): warp 0 TMA producer and TMEM owner, warp 1 MMA issuer,
-// warps 2-9 epilogue (TMEM lane quarter warp % 4; 2-5 the first half of the tile's columns, 6-9 the second).
+// Roles (10 warps, one CTA per SM, persistent over the tiles): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9
+// epilogue (warp 2 owns the TMEM allocation; TMEM lane quarter warp % 4; 2-5 the first half of the tile's columns, 6-9 the second).
 // When the tiles are too few to fill the SMs, the reduction is split over a cluster of 2, 4 or 8 CTAs, which
 // join their partial tiles through distributed shared memory in rank order. All waits are bounded: on expiry an abort
 // flag stops every role, copies and MMAs in flight are waited for (also bounded), TMEM is freed and a device flag set.
@@ -24,6 +24,9 @@
 
 #include <algorithm>
 #include <cstring>
+#include <map>
+#include <mutex>
+#include <tuple>
 #include <type_traits>
 
 #include "tc_ptx.cuh"
@@ -42,7 +45,6 @@ constexpr int BM = 128;
 constexpr int NUM_THREADS = 320;
 constexpr int EPI_THREADS = 256;
 constexpr int MAX_STAGES = 8;
-constexpr int SMEM_LIMIT = 232448;  // 227 KB, static shared memory included
 constexpr int CHUNK = 8;            // k-blocks of 32 between two additions of the h h accumulator (PL = 3)
 
 template <int PL>
@@ -146,6 +148,15 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(on));
     return on != 0;
 }
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+// Programmatic dependent launch: grid_wait returns when the launches before have completed and their writes are seen;
+// grid_trigger lets the next launch begin its prologue.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -275,13 +286,24 @@ constexpr int stg_bytes() {
     return 8 * stg_cols<PL, BN>() * STG_LD * 4;
 }
 
+// Calls of few rows stream the weights: two CTAs per SM keep more loads in flight, and clusters of eight find room.
+template <int BN>
+constexpr int ctas_per_sm() {
+    return BN <= 32 ? 2 : 1;
+}
+// Shared memory of a CTA, static included: 227 KB, or half an SM's 228 KB less the 1 KB that each CTA costs.
+template <int BN>
+constexpr int smem_limit() {
+    return BN <= 32 ? 115712 : 232448;
+}
+
 template <int PL, int BN>
 constexpr int stage_bytes() {
     return PL * (BM + BN) * block_k<PL>() * 2;
 }
 
 template <typename T, int PL, int BN>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(NUM_THREADS, ctas_per_sm<BN>())
 linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
             const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
             const __grid_constant__ TcParams P) {
@@ -306,6 +328,7 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
     const uint32_t rank = S > 1 ? cluster_rank() : 0;
     const long long tile0 = blockIdx.x / S, tile_step = gridDim.x / S;
 
+    // The producer needs the barriers only; TMEM is allocated beside its first loads.
     if (threadIdx.x == 0) {
         abort_sh = 0;
         for (int s = 0; s < NS; ++s) {
@@ -320,16 +343,28 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
         mbar_init(&done_bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_sh)),
-                     "r"(TMEM_COLS)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if (warp == 1 && elect_one()) {
+        prefetch_map(&tmA0);
+        prefetch_map(&tmB0);
+        prefetch_map(&tmA1);
+        prefetch_map(&tmB1);
     }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_base_sh;
+    grid_wait();  // what the launch before wrote may be read from here on
+    uint32_t tmem = 0;
+    if (warp > 0) {
+        if (warp == 2) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(&tmem_base_sh)),
+                         "r"(TMEM_COLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+        tc_fence_before();
+        asm volatile("bar.sync 1, %0;" ::"r"(NUM_THREADS - 32) : "memory");
+        tc_fence_after();
+        tmem = tmem_base_sh;
+    }
     volatile int* abort_flag = &abort_sh;
 
     if (warp == 0) {
@@ -461,6 +496,10 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
             const int u = (int)(w ? t - P.p[0].tiles : t);
             const int i0 = u % p.tiles_i * BM, j0 = u / p.tiles_i * BN + half * HALF;
             const long long i = (long long)i0 + q * 32 + ti;
+            if (p.res != nullptr && S == 1)  // this warp's part of the residual comes to L2 while the products run
+                for (int c = lane; c < HALF; c += 32)
+                    if ((long long)j0 + c < p.J && i0 + q * 32 < p.I)
+                        prefetch_l2((const T*)p.res + ((long long)j0 + c) * p.ldr + i0 + q * 32);
             float bias[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -639,7 +678,7 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 2) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
     }
@@ -808,6 +847,8 @@ __device__ void grad_block(const GradJob& j, long long blk) {
 template <typename T>
 __global__ void __launch_bounds__(PACK_THREADS)
 linear_operands_k(const __grid_constant__ GradJob g, const __grid_constant__ PackJob a, const __grid_constant__ PackJob b) {
+    grid_trigger();
+    grid_wait();
     const long long t = blockIdx.x;
     if (t < g.blocks)
         grad_block<T>(g, t);
@@ -910,12 +951,20 @@ cudaError_t launch_operands(int dtype, const GradJob& g, const PackJob& a, const
     const long long blocks = g.blocks + a.blocks + b.blocks;
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(PACK_THREADS);
+    cfg.stream = s;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
     switch (dtype) {
-        case VF_F32: linear_operands_k<float><<<(unsigned)blocks, PACK_THREADS, 0, s>>>(g, a, b); break;
-        case VF_BF16: linear_operands_k<__nv_bfloat16><<<(unsigned)blocks, PACK_THREADS, 0, s>>>(g, a, b); break;
-        default: linear_operands_k<__half><<<(unsigned)blocks, PACK_THREADS, 0, s>>>(g, a, b);
+        case VF_F32: return cudaLaunchKernelEx(&cfg, linear_operands_k<float>, g, a, b);
+        case VF_BF16: return cudaLaunchKernelEx(&cfg, linear_operands_k<__nv_bfloat16>, g, a, b);
+        default: return cudaLaunchKernelEx(&cfg, linear_operands_k<__half>, g, a, b);
     }
-    return cudaGetLastError();
 }
 
 struct Side {
@@ -928,6 +977,25 @@ int sm_count_() {
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return 0;
     return n;
+}
+
+// Clusters of cfg's size that run at once on the current device (asked once per kernel, size and device).
+cudaError_t cluster_limit(const void* kern, const cudaLaunchConfig_t* cfg, int* fit) {
+    static std::mutex mu;
+    static std::map<std::tuple<const void*, unsigned, int>, int> known;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const auto key = std::make_tuple(kern, cfg->attrs[0].val.clusterDim.x, dev);
+    std::lock_guard<std::mutex> lock(mu);
+    const auto it = known.find(key);
+    if (it != known.end()) {
+        *fit = it->second;
+        return cudaSuccess;
+    }
+    e = cudaOccupancyMaxActiveClusters(fit, kern, cfg);
+    if (e == cudaSuccess) known[key] = *fit;
+    return e;
 }
 
 template <typename T, int PL, int BN>
@@ -955,30 +1023,40 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
         mb[1] = mb[0];
         if (count == 1) P.p[1].tiles = 0;
     }
-    // few tiles: split the reduction over a cluster, each CTA keeping at least two blocks of it
-    P.split = 1;
-    while (count > 0 && P.split < 8 && P.tiles * P.split * 2 <= sms && min_nk >= P.split * 4) P.split *= 2;
-    const int need = stage_bytes<PL, BN>();
-    P.stages = std::min(MAX_STAGES, (SMEM_LIMIT - 1024 - 1024 - stg_bytes<PL, BN>()) / need);
-    size_t smem = 1024 + (size_t)P.stages * need + stg_bytes<PL, BN>();
     auto kern = linear_tc_k<T, PL, BN>;
-    cudaError_t e = allow_dyn_smem((const void*)kern, SMEM_LIMIT - 1024);
+    cudaError_t e = allow_dyn_smem((const void*)kern, smem_limit<BN>() - 1024);
     if (e != cudaSuccess) return e;
-    long long grid = P.split > 1 ? P.tiles * P.split : std::min<long long>(P.tiles, sms);
-    if (P.tiles == 0) grid = std::min<long long>((P.N + EPI_THREADS - 1) / EPI_THREADS, sms);
+    const int need = stage_bytes<PL, BN>();
+    P.stages = std::min(MAX_STAGES, (smem_limit<BN>() - 1024 - 1024 - stg_bytes<PL, BN>()) / need);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(NUM_THREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = 1024 + (size_t)P.stages * need + stg_bytes<PL, BN>();
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = P.split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[0].val.clusterDim.x = at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, ma[0], mb[0], ma[1], mb[1], P);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    // Few tiles: split the reduction over a cluster, each CTA keeping at least two blocks of it, as long as all clusters
+    // run at once (a cluster's CTAs share a GPC, so fewer may fit than the SMs suggest).
+    P.split = 1;
+    const int slots = sms * ctas_per_sm<BN>();
+    while (count > 0 && P.split < 8 && P.tiles * P.split * 2 <= slots && min_nk >= P.split * 4) {
+        at[0].val.clusterDim.x = P.split * 2;
+        cfg.numAttrs = 1;
+        cfg.gridDim = dim3((unsigned)(P.tiles * P.split * 2));
+        int fit = 0;
+        if ((e = cluster_limit((const void*)kern, &cfg, &fit)) != cudaSuccess) return e;
+        if (fit < P.tiles) break;
+        P.split *= 2;
+    }
+    long long grid = P.split > 1 ? P.tiles * P.split : std::min<long long>(P.tiles, slots);
+    if (P.tiles == 0) grid = std::min<long long>((P.N + EPI_THREADS - 1) / EPI_THREADS, sms);
+    cfg.gridDim = dim3((unsigned)grid);
+    at[0].val.clusterDim.x = P.split;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, ma[0], mb[0], ma[1], mb[1], P);
 }
 
 template <typename T, int PL>

@@ -35,6 +35,22 @@ __device__ __forceinline__ float exp2f_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Clamps that keep NaN.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
 
 // Evaluated in fp32. FAST serves the 16-bit types, whose rounding (2^-9, 2^-12) lies far above its error; float32 takes
 // CUDA's erfcf and expf.
@@ -52,7 +68,7 @@ __device__ __forceinline__ float phi(float z, float& e) {
     }
     const float a = fabsf(z);
     e = exp2f_approx(z * z * -0.72134752044448170f);
-    const float t = __fdividef(1.f, fmaf(0.3f, a, 1.f));
+    const float t = rcp_approx(fmaf(0.3f, a, 1.f));
     float q = 0.035423859484090325f;
     q = fmaf(q, t, -0.15615893604759168f);
     q = fmaf(q, t, 0.204557570019329f);
@@ -67,8 +83,8 @@ __device__ __forceinline__ float phi(float z, float& e) {
 // 1 / (1 + exp(-z)) and e = exp(-z).
 template <bool FAST>
 __device__ __forceinline__ float sigmoid(float z, float& e) {
-    e = FAST ? __expf(-z) : expf(-z);
-    return FAST ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e);
+    e = FAST ? exp2f_approx(z * -1.4426950408889634f) : expf(-z);
+    return FAST ? rcp_approx(1.f + e) : 1.f / (1.f + e);
 }
 
 // relu passes NaN on (z < 0 is false for it); gelu and silu take their limit 0 at -inf.
@@ -97,9 +113,9 @@ __device__ __forceinline__ float act_grad(float dy, float z, int act) {
     float e;
     if (act == VF_ACT_NONE) return dy;
     if (act == VF_ACT_RELU) return z <= 0.f ? 0.f : dy;
-    if (z > 80.f) z = 80.f;
+    z = min_nan(z, 80.f);
     if (act == VF_ACT_GELU) {
-        if (z < -80.f) z = -80.f;
+        z = max_nan(z, -80.f);
         const float f = phi<FAST>(z, e);
         return dy * fmaf(z * 0.39894228040143268f, e, f);
     }

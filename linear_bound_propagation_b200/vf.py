@@ -8,6 +8,7 @@ there is no other implementation behind these names.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, Optional, Sequence
 
@@ -478,10 +479,8 @@ def concretize_dense_noalloc(lam: torch.Tensor, W: torch.Tensor, b: torch.Tensor
 class _On:
     """The device and stream of one operator call: allocations inside belong to the stream the kernels run on."""
 
-    def __init__(self, device, stream):
-        self.guards = []
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
+    def __init__(self, dev, stream):
+        self.guards = [torch.cuda.device(dev)]
         if stream is not None:
             self.guards.append(torch.cuda.stream(stream))
 
@@ -494,43 +493,52 @@ class _On:
             g.__exit__(*exc)
 
 
-def _matrix(name, t, rows, cols, dtype, device):
-    """(pointer, row stride) of a [rows, cols] argument with unit column stride; (None, 0) for None."""
-    if t is None:
-        return None, 0
-    if t.dtype != dtype or t.device != device or t.shape != (rows, cols):
-        raise ValueError(f"{name} must be {dtype} [{rows}, {cols}] on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+def _matrix(name, t, shape, dtype, dev):
+    """(pointer, row stride) of a matrix argument with unit column stride."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on CUDA device {dev}, got {t.dtype} {list(t.shape)} on {t.device}")
     ld, one = t.stride()
-    if rows <= 1:
+    cols = shape[1]
+    if shape[0] <= 1:
         ld = cols
-    if (one != 1 and cols > 1) or ld < cols:
+    if ld < cols or (one != 1 and cols > 1):
         raise ValueError(f"{name} must have rows of unit stride that do not overlap, got strides {t.stride()}")
     return t.data_ptr(), ld
 
 
-def _vector(name, t, n, dtype, device):
-    if t is None:
-        return None
-    if t.dtype != dtype or t.device != device or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {dtype} [{n}] on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+def _vector(name, t, n, dtype, dev):
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} [{n}] on CUDA device {dev}, got {t.dtype} {list(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _layer(x, W, act):
-    """Common checks of a layer's arguments: (dtype, activation, device, M, N, K)."""
-    if x.dtype not in VF_DTYPES:
+    """Common checks of a layer's arguments: (torch type, vf_dtype, vf_act, device, M, N, K)."""
+    dtype, a, dev = VF_DTYPES.get(x.dtype), VF_ACTS.get(act), x.get_device()
+    if dtype is None:
         raise ValueError(f"float32, bfloat16 or float16 expected, got {x.dtype}")
-    if act not in VF_ACTS:
+    if a is None:
         raise ValueError(f"act must be one of {sorted(VF_ACTS)}, got {act!r}")
-    if not x.is_cuda or x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1]:
+    if dev < 0 or x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1]:
         raise ValueError(f"x [M, K] and W [N, K] on a CUDA device expected, got {list(x.shape)} and {list(W.shape)}")
-    return x.dtype, VF_ACTS[act], x.device, x.shape[0], W.shape[0], x.shape[1]
+    M, K = x.shape
+    return x.dtype, dtype, a, dev, M, W.shape[0], K
 
 
-def _linear_work(dtype, M, N, K, grad, device):
+@functools.lru_cache(maxsize=4096)
+def _linear_work(dtype, M, N, K, grad):
+    """Bytes of workspace for these sizes (a function of the sizes alone)."""
     n = ctypes.c_size_t()
     _check(lib().vf_linear_workspace(dtype, M, N, K, grad, ctypes.byref(n)))
-    return (torch.empty(n.value, device=device, dtype=torch.uint8) if n.value else None), n.value
+    return n.value
+
+
+@functools.lru_cache(maxsize=None)
+def _clip_work(n, dev):
+    """Bytes of workspace for n gradients on device dev (the current one)."""
+    b = ctypes.c_size_t()
+    _check(lib().vf_clip_workspace(n, ctypes.byref(b)))
+    return b.value
 
 
 def linear(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tensor] = None,
@@ -540,19 +548,27 @@ def linear(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tensor] = None,
     bfloat16 or float16); rows may be any distance apart. act: "none", "relu", "gelu" (normal distribution) or
     "silu". Returns dict(y=[M, N], z=the pre-activation for linear_grad or None). out: y's buffer; it may be
     `residual` itself. Runs on the current stream of x's device unless `stream` is given."""
-    dtype, a, dev, M, N, K = _layer(x, W, act)
-    xp, ldx = _matrix("x", x, M, K, dtype, dev)
-    wp, ldw = _matrix("W", W, N, K, dtype, dev)
-    bp = _vector("b", b, N, dtype, dev)
-    rp, ldr = _matrix("residual", residual, M, N, dtype, dev)
-    with _On(dev, stream):
-        y = torch.empty(M, N, device=dev, dtype=dtype) if out is None else out
-        z = torch.empty(M, N, device=dev, dtype=dtype) if want_z else None
-        yp, ldy = _matrix("out", y, M, N, dtype, dev)
-        work, nbytes = _linear_work(VF_DTYPES[dtype], M, N, K, 0, dev)
-        _check(lib().vf_linear(VF_DTYPES[dtype], a, xp, ldx, wp, ldw, bp, rp, ldr, M, N, K, yp, ldy,
-                               None if z is None else z.data_ptr(), N, None if work is None else work.data_ptr(),
-                               nbytes, _stream_ptr()))
+    tt, dtype, a, dev, M, N, K = _layer(x, W, act)
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        with _On(dev, stream):
+            return linear(x, W, b, residual, act, want_z, out)
+    xp, ldx = _matrix("x", x, (M, K), tt, dev)
+    wp, ldw = _matrix("W", W, (N, K), tt, dev)
+    shape = (M, N)
+    bp = None if b is None else _vector("b", b, N, tt, dev)
+    rp, ldr = (None, 0) if residual is None else _matrix("residual", residual, shape, tt, dev)
+    if out is None:
+        y = torch.empty(shape, device=x.device, dtype=tt)
+        yp, ldy = y.data_ptr(), N
+    else:
+        y = out
+        yp, ldy = _matrix("out", y, shape, tt, dev)
+    z = torch.empty(shape, device=x.device, dtype=tt) if want_z else None
+    nbytes = _linear_work(dtype, M, N, K, 0)
+    work = torch.empty(nbytes, device=x.device, dtype=torch.uint8) if nbytes else None
+    _check(lib().vf_linear(dtype, a, xp, ldx, wp, ldw, bp, rp, ldr, M, N, K, yp, ldy, None if z is None else z.data_ptr(),
+                           N, None if work is None else work.data_ptr(), nbytes,
+                           torch._C._cuda_getCurrentRawStream(dev)))
     return {"y": y, "z": z}
 
 
@@ -561,24 +577,32 @@ def linear_grad(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, act: str = "
     """vf_linear_grad: the backward pass of linear for dy [M, N], the gradient of y, and the z that linear returned
     (not needed for act="none"). Returns dict(dx=[M, K], dW=[N, K], db=[N], dr=[M, N], the gradient of the
     residual), None for those not in `need`."""
-    dtype, a, dev, M, N, K = _layer(x, W, act)
+    tt, dtype, a, dev, M, N, K = _layer(x, W, act)
     if not set(need) <= {"dx", "dW", "db", "dr"}:
         raise ValueError(f"need names dx, dW, db and dr, got {list(need)}")
     if a != 0 and z is None:
         raise ValueError(f"act={act!r} needs the pre-activation z")
-    dyp, lddy = _matrix("dy", dy, M, N, dtype, dev)
-    zp, ldz = _matrix("z", z, M, N, dtype, dev)
-    xp, ldx = _matrix("x", x, M, K, dtype, dev)
-    wp, ldw = _matrix("W", W, N, K, dtype, dev)
-    with _On(dev, stream):
-        shapes = {"dx": (M, K), "dW": (N, K), "db": (N,), "dr": (M, N)}
-        o = {k: torch.empty(shape, device=dev, dtype=dtype) if k in need else None for k, shape in shapes.items()}
-        p = {k: None if t is None else t.data_ptr() for k, t in o.items()}
-        work, nbytes = _linear_work(VF_DTYPES[dtype], M, N, K, 1, dev)
-        _check(lib().vf_linear_grad(VF_DTYPES[dtype], a, dyp, lddy, zp, ldz, xp, ldx, wp, ldw, M, N, K, p["dx"], K,
-                                    p["dW"], K, p["db"], p["dr"], N, None if work is None else work.data_ptr(), nbytes,
-                                    _stream_ptr()))
-    return o
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        with _On(dev, stream):
+            return linear_grad(dy, x, W, act, z, need)
+    shape = (M, N)
+    dyp, lddy = _matrix("dy", dy, shape, tt, dev)
+    zp, ldz = (None, 0) if z is None else _matrix("z", z, shape, tt, dev)
+    xp, ldx = _matrix("x", x, (M, K), tt, dev)
+    wp, ldw = _matrix("W", W, (N, K), tt, dev)
+    device = x.device
+    dx = torch.empty((M, K), device=device, dtype=tt) if "dx" in need else None
+    dW = torch.empty((N, K), device=device, dtype=tt) if "dW" in need else None
+    db = torch.empty((N,), device=device, dtype=tt) if "db" in need else None
+    dr = torch.empty(shape, device=device, dtype=tt) if "dr" in need else None
+    nbytes = _linear_work(dtype, M, N, K, 1)
+    work = torch.empty(nbytes, device=device, dtype=torch.uint8) if nbytes else None
+    _check(lib().vf_linear_grad(dtype, a, dyp, lddy, zp, ldz, xp, ldx, wp, ldw, M, N, K,
+                                None if dx is None else dx.data_ptr(), K, None if dW is None else dW.data_ptr(), K,
+                                None if db is None else db.data_ptr(), None if dr is None else dr.data_ptr(), N,
+                                None if work is None else work.data_ptr(), nbytes,
+                                torch._C._cuda_getCurrentRawStream(dev)))
+    return {"dx": dx, "dW": dW, "db": db, "dr": dr}
 
 
 def ops_check():
@@ -595,25 +619,33 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, scale: float 
     is not finite clips nothing and is left for the caller to look at."""
     grads = list(grads)
     outs = grads if out is None else list(out)
-    if len(outs) != len(grads):
-        raise ValueError(f"{len(grads)} gradients and {len(outs)} outputs")
-    dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
     n = len(grads)
-    gp, op = (ctypes.c_void_p * n)(), (ctypes.c_void_p * n)()
-    sizes, dtypes = (ctypes.c_longlong * n)(), (ctypes.c_int * n)()
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        if g.dtype not in VF_DTYPES or not g.is_cuda or g.device != dev or not g.is_contiguous():
-            raise ValueError(f"gradient {i} must be contiguous float32, bfloat16 or float16 on {dev}, got {g.dtype} on {g.device}")
-        if o is not g and (o.dtype != g.dtype or o.device != dev or o.shape != g.shape or not o.is_contiguous()):
-            raise ValueError(f"out {i} must be contiguous {g.dtype} {list(g.shape)} on {dev}, got {o.dtype} {list(o.shape)}")
-        gp[i], op[i], sizes[i], dtypes[i] = g.data_ptr(), o.data_ptr(), g.numel(), VF_DTYPES[g.dtype]
-    with _On(dev, stream):
-        norm = torch.empty((), device=dev, dtype=torch.float32)
-        nbytes = ctypes.c_size_t()
-        _check(lib().vf_clip_workspace(n, ctypes.byref(nbytes)))
-        work = torch.empty(nbytes.value, device=dev, dtype=torch.uint8)
-        _check(lib().vf_clip_grad_norm(n, gp, op, sizes, dtypes, float(scale), float(max_norm), norm.data_ptr(),
-                                       work.data_ptr(), nbytes.value, _stream_ptr()))
+    if len(outs) != n:
+        raise ValueError(f"{n} gradients and {len(outs)} outputs")
+    dev = grads[0].get_device() if n else torch.cuda.current_device()
+    if stream is not None or (dev >= 0 and dev != torch._C._cuda_getDevice()):
+        with _On(dev, stream):
+            return clip_grad_norm(grads, max_norm, scale, out)
+    dtypes = [VF_DTYPES.get(g.dtype) for g in grads]
+    for i, g in enumerate(grads):
+        if dtypes[i] is None or dev < 0 or g.get_device() != dev or not g.is_contiguous():
+            raise ValueError(f"gradient {i} must be contiguous float32, bfloat16 or float16 on CUDA device {dev}, got "
+                             f"{g.dtype} on {g.device}")
+    gp = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+    op = gp
+    if out is not None:
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if o.dtype is not g.dtype or o.get_device() != dev or o.shape != g.shape or not o.is_contiguous():
+                raise ValueError(f"out {i} must be contiguous {g.dtype} {list(g.shape)} on CUDA device {dev}, got "
+                                 f"{o.dtype} {list(o.shape)} on {o.device}")
+        op = (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs])
+    sizes = (ctypes.c_longlong * n)(*[g.numel() for g in grads])
+    nbytes = _clip_work(n, dev)
+    # the norm and the workspace in one allocation: the workspace first, for its alignment
+    buf = torch.empty(nbytes // 4 + 1, device=f"cuda:{dev}", dtype=torch.float32)
+    norm = buf[-1]
+    _check(lib().vf_clip_grad_norm(n, gp, op, sizes, (ctypes.c_int * n)(*dtypes), float(scale), float(max_norm),
+                                   norm.data_ptr(), buf.data_ptr(), nbytes, torch._C._cuda_getCurrentRawStream(dev)))
     return norm, outs
 
 
