@@ -15,7 +15,7 @@
 // a sum of positive terms over 512 MMAs comes out 1e-5 low), so the five small products go to an accumulator of their own, and
 // the h h accumulator is added to registers, rounding to nearest, every CHUNK of the reduction.
 //
-// Roles (10 warps, one CTA per SM, persistent over the tiles): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9
+// Roles (10 warps; one CTA per SM, or a pair of CTAs on two SMs for 256 x 256 tiles; persistent over the tiles): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9
 // epilogue (warp 2 owns the TMEM allocation; TMEM lane quarter warp % 4; 2-5 the first half of the tile's columns, 6-9 the second).
 // When the tiles are too few to fill the SMs, the reduction is split over a cluster of 2, 4 or 8 CTAs, which
 // join their partial tiles through distributed shared memory in rank order. All waits are bounded: on expiry an abort
@@ -57,7 +57,7 @@ struct TcProduct {
     int nk;              // blocks of the reduction
     int a_mn, b_mn;      // operand contiguous along i (j) instead of t
     int tiles_i;
-    long long tiles;
+    int tiles;
     void* out;
     long long ldo;
     const void* bias;
@@ -65,12 +65,14 @@ struct TcProduct {
     long long ldr;
     void* zout;
     long long ldz;
-    int act, vec;        // vec: output, residual and z rows all allow 16-byte accesses
+    int act;
+    int vec;             // output, residual and z rows all allow 16-byte accesses (and TMA)
 };
 
 struct TcParams {
-    TcProduct p[2];
-    long long tiles;     // of both products
+    TcProduct p[2];      // the longer reduction first
+    int gap;             // tiles of p[1] that take about as long as one of p[0]
+    int workers;         // CTAs, pairs or clusters that walk the tiles
     int split;           // CTAs per tile (cluster size)
     int stages;
     // column sums of g, joined here: db[n] = sum_q part[q * N + n]
@@ -79,22 +81,76 @@ struct TcParams {
     void* db;
 };
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-            smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-        : "memory");
+// Tensor maps of a launch: operands, and where rows allow TMA the outputs, the residual and z of p[0].
+struct Maps {
+    CUtensorMap a[2], b[2], out[2], res, z;
+};
+
+// The tiles of worker w, the same for every role: its turns through p[0], then through p[1], where the workers that the
+// last, partial turn through p[0] left out begin with `gap` tiles of p[1] each.
+struct Walk {
+    int w, workers, n0, n1, gap, rem, t, phase;
+    __device__ __forceinline__ Walk(const TcParams& P, int worker)
+        : w(worker), workers(P.workers), n0(P.p[0].tiles), n1(P.p[1].tiles), gap(P.gap), t(worker), phase(0) {
+        rem = n0 % workers;
+    }
+    // false: no more tiles
+    __device__ __forceinline__ bool next(int& prod, int& tile) {
+        if (phase == 0) {
+            if (t < n0) {
+                prod = 0;
+                tile = t;
+                t += workers;
+                return true;
+            }
+            phase = rem > 0 && w >= rem ? 1 : 2;
+            t = phase == 1 ? (w - rem) * gap : w + (rem > 0 ? (workers - rem) * gap : 0);
+        }
+        prod = 1;
+        tile = t;
+        if (t >= n1 && phase == 2) return false;
+        if (phase == 1) {
+            if (t >= n1) return false;  // later turns begin further on still
+            if (++t == (w - rem + 1) * gap) {
+                phase = 2;
+                t = w + (workers - rem) * gap;
+            }
+        } else {
+            t += workers;
+        }
+        return true;
+    }
+};
+
+// Tile of an output, a residual or z between shared memory and a 2-D map. Stores belong to the issuing thread's groups.
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, const void* src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(x), "r"(y)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+// At most one store of this thread has its shared memory still to read.
+__device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // D (tmem) (+)= A (smem) x B (smem), kind::f16.
+template <int CG>
 __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
+    if (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
 }
 
 // Position in the ring of stages: slot and how often the ring has been passed. Kept as counters: the roles below are
@@ -109,6 +165,47 @@ struct Ring {
         }
     }
 };
+
+// Two CTAs of a pair (CG = 2) compute one tile: the first issues the MMAs for both, so barriers that its issuer waits on
+// live in its shared memory, and commits arrive in both.
+__device__ __forceinline__ uint32_t leader_addr(const void* p) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+    return a;
+}
+template <int CG>
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+    if (CG == 1)
+        mbar_arrive(bar);
+    else
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar)) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    if (CG == 1)
+        mma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void load_operand(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+            "[%2];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+            "%4, %5}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+            : "memory");
+}
 
 // Operand of rows x BK elements in shared memory. Contiguous along t: rows of BK elements (128 or 64 bytes, swizzled
 // over as many bytes), 8-row groups one after the other. Contiguous along i or j: atoms of 64 elements x BK steps of t,
@@ -127,6 +224,15 @@ __device__ __forceinline__ void tmem_ld<8>(uint32_t taddr, uint32_t (&r)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
+}
+template <>
+__device__ __forceinline__ void tmem_ld<16>(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
@@ -152,7 +258,6 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // Programmatic dependent launch: grid_wait returns when the launches before have completed and their writes are seen;
 // grid_trigger lets the next launch begin its prologue.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -250,42 +355,49 @@ __device__ __forceinline__ void finish8(const TcProduct& p, long long i, long lo
     put8<T>((T*)p.out + j * p.ldo + i, n, v);
 }
 
-// Any other rows: one element i of N rows j .. j + N - 1 per thread, a warp's lanes on consecutive elements.
+// One element i of N rows j .. j + N - 1 per thread, a warp's lanes on consecutive elements: fp32 rows (a warp's access
+// is a whole 128-byte line) and rows that do not allow 16-byte accesses.
 template <typename T, int N>
-__device__ __forceinline__ void finish_lane(const TcProduct& p, long long i, long long j, float (&v)[N], float bias) {
-    if (i >= p.I) return;
-    if (p.res != nullptr) {
-        float r[N];
-#pragma unroll
-        for (int u = 0; u < N; ++u) r[u] = j + u < p.J ? to_f32(((const T*)p.res)[(j + u) * p.ldr + i]) : 0.f;
-#pragma unroll
-        for (int u = 0; u < N; ++u) v[u] += bias + r[u];
-    } else {
-#pragma unroll
-        for (int u = 0; u < N; ++u) v[u] += bias;
-    }
-    if (p.zout != nullptr)
-#pragma unroll
-        for (int u = 0; u < N; ++u)
-            if (j + u < p.J) ((T*)p.zout)[(j + u) * p.ldz + i] = from_f32<T>(v[u]);
-    activate<T>(v, p.act);
+__device__ __forceinline__ void res_lane(const TcProduct& p, long long i, long long j, float (&r)[N]) {
 #pragma unroll
     for (int u = 0; u < N; ++u)
-        if (j + u < p.J) ((T*)p.out)[(j + u) * p.ldo + i] = from_f32<T>(v[u]);
+        r[u] = (p.res != nullptr && i < p.I && j + u < p.J) ? to_f32(((const T*)p.res)[(j + u) * p.ldr + i]) : 0.f;
+}
+template <typename T, int N>
+__device__ __forceinline__ void finish_lane(const TcProduct& p, long long i, long long j, float (&v)[N], float bias,
+                                            const float (&r)[N]) {
+    if (i >= p.I) return;
+    const int n = (int)min((long long)N, p.J - j);
+#pragma unroll
+    for (int u = 0; u < N; ++u) v[u] += bias + r[u];
+    if (p.zout != nullptr) {
+        T* z = (T*)p.zout + j * p.ldz + i;
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            if (u < n) z[u * p.ldz] = from_f32<T>(v[u]);
+    }
+    activate<T>(v, p.act);
+    T* o = (T*)p.out + j * p.ldo + i;
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+        if (u < n) o[u * p.ldo] = from_f32<T>(v[u]);
 }
 
-// Staging of the epilogue: a warp's 32 lanes x COLS columns, so that a thread gets eight lanes of one column. 36 floats
-// per column: 16-byte rows whose reads meet no bank twice. The 256-column fp32 tile leaves room for eight columns only.
-constexpr int STG_LD = 36;
-template <int PL, int BN>
-constexpr int stg_cols() {
-    return BN <= 64 ? BN / 2 : (PL == 3 && BN == 256 ? 8 : 16);
+// Epilogue through TMA (tiles of 64 columns and more whose rows allow it): a warp handles its 32 lanes in rounds of
+// ROUND columns, with two 2 KB buffers for the residual on its way in and two for z and y on their way out.
+template <typename T, int BN>
+constexpr int epi_round() {
+    return sizeof(T) == 4 ? 16 : 32;
 }
-template <int PL, int BN>
-constexpr int stg_bytes() {
-    return 8 * stg_cols<PL, BN>() * STG_LD * 4;
+template <int BN>
+constexpr int epi_bytes() {
+    return BN >= 64 ? 8 * 4 * 2048 : 0;
 }
-
+// A pair of CTAs takes the 256-column tiles: each loads half of both operands, which halves what a CTA reads per MMA.
+template <int BN>
+constexpr int pair_of() {
+    return BN == 256 ? 2 : 1;
+}
 // Calls of few rows stream the weights: two CTAs per SM keep more loads in flight, and clusters of eight find room.
 template <int BN>
 constexpr int ctas_per_sm() {
@@ -299,34 +411,51 @@ constexpr int smem_limit() {
 
 template <int PL, int BN>
 constexpr int stage_bytes() {
-    return PL * (BM + BN) * block_k<PL>() * 2;
+    return PL * (BM + BN / pair_of<BN>()) * block_k<PL>() * 2;
+}
+
+// One round of a warp: 32 lanes x N columns to shared memory, a column's 32 elements together, and on to rows
+// y .. y + N - 1 of the map. Two buffers take turns: the store before last has read the one written here.
+template <typename T, int N>
+__device__ __forceinline__ void put_round(T* buf, const float (&v)[N], const CUtensorMap* map, int x, int y, int lane) {
+    if (lane == 0) store_wait_read();
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < N; ++c) buf[c * 32 + lane] = from_f32<T>(v[c]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) store_tile(map, buf, x, y);
 }
 
 template <typename T, int PL, int BN>
 __global__ void __launch_bounds__(NUM_THREADS, ctas_per_sm<BN>())
-linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
-            const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
-            const __grid_constant__ TcParams P) {
+linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams P) {
     constexpr int BK = block_k<PL>();
-    constexpr int A_PLANE = BM * BK * 2, B_PLANE = BN * BK * 2;
+    constexpr int CG = pair_of<BN>();
+    constexpr int BL = BN / CG;                              // rows of B that a CTA loads
+    constexpr int A_PLANE = BM * BK * 2, B_PLANE = BL * BK * 2;
     constexpr int STAGE = stage_bytes<PL, BN>();
     constexpr int NB = (PL == 1 || BN <= 128) ? 2 : 1;       // accumulator sets in TMEM
     constexpr int ACC_COLS = NB * BN;
     constexpr int USED_COLS = PL == 3 ? 2 * ACC_COLS : ACC_COLS;
     constexpr int TMEM_COLS = USED_COLS < 32 ? 32 : USED_COLS;
     constexpr int HALF = BN / 2;
-    constexpr int COLS = stg_cols<PL, BN>();
+    constexpr int LD = HALF < 16 ? 8 : 16;                   // columns per TMEM load
+    constexpr bool EPI_TMA = BN >= 64;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], cor_empty[2], done_bar;
+    __shared__ uint64_t res_full[8][2];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int NS = P.stages;
-    const int S = P.split;
-    const uint32_t rank = S > 1 ? cluster_rank() : 0;
-    const long long tile0 = blockIdx.x / S, tile_step = gridDim.x / S;
+    const int S = CG == 1 ? P.split : 1;
+    const int crank = (CG > 1 || S > 1) ? (int)cluster_rank() : 0;
+    const int rank = CG == 1 ? crank : 0;   // share of a split reduction
+    const int pr = CG == 2 ? crank : 0;     // place in a pair
+    const int worker = blockIdx.x / (CG * S);
 
     // The producer needs the barriers only; TMEM is allocated beside its first loads.
     if (threadIdx.x == 0) {
@@ -337,28 +466,43 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&acc_full[s], 1);
-            mbar_init(&acc_empty[s], EPI_THREADS);
-            mbar_init(&cor_empty[s], EPI_THREADS);
+            mbar_init(&acc_empty[s], 8 * CG);  // one arrival per epilogue warp
+            mbar_init(&cor_empty[s], 8 * CG);
         }
+        for (int s = 0; s < 16; ++s) mbar_init(&res_full[s >> 1][s & 1], 1);
         mbar_init(&done_bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1 && elect_one()) {
-        prefetch_map(&tmA0);
-        prefetch_map(&tmB0);
-        prefetch_map(&tmA1);
-        prefetch_map(&tmB1);
+        for (int w = 0; w < 2; ++w)
+            if (P.p[w].tiles > 0) {
+                prefetch_map(&maps.a[w]);
+                prefetch_map(&maps.b[w]);
+            }
     }
-    __syncthreads();
+    if (CG == 2) {
+        __syncwarp();
+        cluster_sync_all();  // the other CTA's barriers exist
+    } else {
+        __syncthreads();
+    }
     grid_wait();  // what the launch before wrote may be read from here on
     uint32_t tmem = 0;
     if (warp > 0) {
         if (warp == 2) {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                             smem_u32(&tmem_base_sh)),
-                         "r"(TMEM_COLS)
-                         : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+            if (CG == 2) {
+                asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                                 smem_u32(&tmem_base_sh)),
+                             "r"(TMEM_COLS)
+                             : "memory");
+                asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+            } else {
+                asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                                 smem_u32(&tmem_base_sh)),
+                             "r"(TMEM_COLS)
+                             : "memory");
+                asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+            }
         }
         tc_fence_before();
         asm volatile("bar.sync 1, %0;" ::"r"(NUM_THREADS - 32) : "memory");
@@ -371,20 +515,21 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
         if (elect_one()) {
             // ------------------------------------------------------------------------------- TMA producer
             Ring g;
-            for (long long t = tile0; t < P.tiles && !*abort_flag; t += tile_step) {
-                const int w = t >= P.p[0].tiles;
+            Walk walk(P, worker);
+            int w, u;
+            while (!*abort_flag && walk.next(w, u)) {
                 const TcProduct& p = P.p[w];
-                const int u = (int)(w ? t - P.p[0].tiles : t);
-                const int i0 = u % p.tiles_i * BM, j0 = u / p.tiles_i * BN;
-                const CUtensorMap* ma = w ? &tmA1 : &tmA0;
-                const CUtensorMap* mb = w ? &tmB1 : &tmB0;
+                const int i0 = u % p.tiles_i * (BM * CG) + pr * BM, j0 = u / p.tiles_i * BN + pr * BL;
+                const CUtensorMap* ma = &maps.a[w];
+                const CUtensorMap* mb = &maps.b[w];
                 const int kb0 = (int)((long long)p.nk * rank / S), kb1 = (int)((long long)p.nk * (rank + 1) / S);
                 const bool a_mn = p.a_mn, b_mn = p.b_mn;
                 for (int kb = kb0; kb < kb1; ++kb, g.next(NS)) {
                     if (g.lap > 0 && !mbar_wait(&empty[g.slot], (g.lap - 1) & 1, abort_flag)) break;
                     uint8_t* st = base + (size_t)g.slot * STAGE;
-                    uint64_t* bar = &full[g.slot];
-                    mbar_expect_tx(bar, STAGE);
+                    uint32_t bar = smem_u32(&full[g.slot]);
+                    if (CG == 1 || pr == 0) mbar_expect_tx(&full[g.slot], STAGE * CG);
+                    if (CG == 2) bar = leader_addr(&full[g.slot]);
 #pragma unroll
                     for (int q = 0; q < PL; ++q) {
                         uint8_t* a = st + q * A_PLANE;
@@ -392,22 +537,27 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
                         if (a_mn) {
 #pragma unroll
                             for (int c = 0; c < BM / 64; ++c)
-                                tma_load_3d(a + c * BK * 128, ma, bar, i0 + c * 64, kb * BK, q);
+                                load_operand<CG>(a + c * BK * 128, ma, bar, i0 + c * 64, kb * BK, q);
                         } else {
-                            tma_load_3d(a, ma, bar, kb * BK, i0, q);
+                            load_operand<CG>(a, ma, bar, kb * BK, i0, q);
                         }
-                        if (BN >= 64 && b_mn) {
+                        if (BL >= 64 && b_mn) {
 #pragma unroll
-                            for (int c = 0; c < BN / 64; ++c)
-                                tma_load_3d(b + c * BK * 128, mb, bar, j0 + c * 64, kb * BK, q);
+                            for (int c = 0; c < BL / 64; ++c)
+                                load_operand<CG>(b + c * BK * 128, mb, bar, j0 + c * 64, kb * BK, q);
                         } else {
-                            tma_load_3d(b, mb, bar, kb * BK, j0, q);
+                            load_operand<CG>(b, mb, bar, kb * BK, j0, q);
                         }
                     }
                 }
             }
             if (*abort_flag) {  // wait (bounded) for copies that nobody will consume: the last lap's
-                for (int h = 0; h < NS; ++h) {
+                if (CG == 2) {  // their barriers may be the other CTA's: a millisecond is enough for any of them
+                    const long long t0 = clock64();
+                    while (clock64() - t0 < 2000000) {
+                    }
+                }
+                for (int h = 0; h < NS && CG == 1; ++h) {
                     const uint32_t laps = g.lap + (h < g.slot ? 1 : 0);  // copies issued into slot h
                     const long long t0 = clock64();
                     while (laps > 0 && !mbar_test(&full[h], (laps - 1) & 1) && clock64() - t0 < WAIT_CYCLES) {
@@ -416,17 +566,20 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
             }
         }
     } else if (warp == 1) {
-        if (elect_one()) {
+        if (pr == 0 && elect_one()) {
             // --------------------------------------------------------------------------------- MMA issuer
             Ring g, chunk, tile;  // stages; accumulator sets (one chunk each); small-product sets (one tile each)
             bool ok = true;
-            for (long long t = tile0; ok && t < P.tiles && !*abort_flag; t += tile_step, tile.next(NB)) {
-                const TcProduct& p = P.p[t >= P.p[0].tiles];
+            Walk walk(P, worker);
+            int w, u;
+            while (ok && !*abort_flag && walk.next(w, u)) {
+                const TcProduct& p = P.p[w];
                 const int kb0 = (int)((long long)p.nk * rank / S), kb1 = (int)((long long)p.nk * (rank + 1) / S);
                 const int a_mn = p.a_mn, b_mn = p.b_mn;
                 const uint32_t fmt = (PL == 3 || std::is_same<T, __nv_bfloat16>::value) ? 1u : 0u;
                 const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)a_mn << 15) |
-                                       ((uint32_t)b_mn << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+                                       ((uint32_t)b_mn << 16) | ((uint32_t)(BN >> 3) << 17) |
+                                       ((uint32_t)(BM * CG >> 4) << 24);
                 // descriptors of the ring's first slot, and their steps (16-byte units) per K = 16, plane and slot
                 const uint64_t a0 = operand_desc<BK>(smem_u32(base), a_mn);
                 const uint64_t b0 = operand_desc<BK>(smem_u32(base) + PL * A_PLANE, b_mn);
@@ -446,11 +599,11 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
                         for (int kk = 0; kk < BK / 16; ++kk) {
                             const uint64_t h = ah + kk * step_a, m = h + A_PLANE / 16, l = m + A_PLANE / 16;
                             const uint64_t H = bh + kk * step_b, M = H + B_PLANE / 16, L = M + B_PLANE / 16;
-                            mma_f16_ss(cor, l, H, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
-                            mma_f16_ss(cor, h, L, idesc, 1u);
-                            mma_f16_ss(cor, m, M, idesc, 1u);
-                            mma_f16_ss(cor, m, H, idesc, 1u);
-                            mma_f16_ss(cor, h, M, idesc, 1u);
+                            mma_f16_ss<CG>(cor, l, H, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+                            mma_f16_ss<CG>(cor, h, L, idesc, 1u);
+                            mma_f16_ss<CG>(cor, m, M, idesc, 1u);
+                            mma_f16_ss<CG>(cor, m, H, idesc, 1u);
+                            mma_f16_ss<CG>(cor, h, M, idesc, 1u);
                         }
                     }
                     if (in_chunk == 0 && chunk.lap > 0 &&
@@ -459,27 +612,32 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk)
-                        mma_f16_ss(d, ah + kk * step_a, bh + kk * step_b, idesc, (in_chunk > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(&empty[g.slot]);
+                        mma_f16_ss<CG>(d, ah + kk * step_a, bh + kk * step_b, idesc, (in_chunk > 0 || kk > 0) ? 1u : 0u);
+                    commit<CG>(&empty[g.slot]);
                     ++in_chunk;
                     if (kb + 1 == kb1 || (PL == 3 && in_chunk == CHUNK)) {
-                        mma_commit(&acc_full[chunk.slot]);
+                        commit<CG>(&acc_full[chunk.slot]);
                         chunk.next(NB);
                         in_chunk = 0;
                     }
                 }
+                tile.next(NB);
             }
             // TMEM is never freed, nor the stages reused, under MMAs in flight: one last commit tracks them all
-            mma_commit(&done_bar);
+            if (CG == 1)
+                mma_commit(&done_bar);
+            else
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                 smem_u32(&done_bar))
+                             : "memory");
             const long long t0 = clock64();
             while (!mbar_test(&done_bar, 0) && clock64() - t0 < WAIT_CYCLES) {
             }
         }
     } else {
         // ------------------------------------------------------------------------------------- epilogue
-        const int q = warp & 3, half = warp >= 6;
+        const int e = warp - 2, q = warp & 3, half = e >> 2;
         const uint32_t lane_base = ((uint32_t)(q * 32) << 16) + half * HALF;
-        float* stg = reinterpret_cast<float*>(base + (size_t)NS * STAGE) + (warp - 2) * COLS * STG_LD;
         if (P.db != nullptr)
             for (long long n = (long long)blockIdx.x * EPI_THREADS + threadIdx.x - 64; n < P.N;
                  n += (long long)gridDim.x * EPI_THREADS) {
@@ -488,30 +646,40 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
                 for (int k = 0; k < P.nparts; ++k) s += P.part[(long long)k * P.N + n];
                 ((T*)P.db)[n] = from_f32<T>(s);
             }
-        Ring chunk, tile;  // as the MMA issuer counts them
-        const int tj = lane >> 2, ti = (lane & 3) * 8;  // this thread's part of an 8-column, 32-lane block
-        for (long long t = tile0; t < P.tiles; t += tile_step, tile.next(NB)) {
-            const int w = t >= P.p[0].tiles;
+        constexpr int ROUND = epi_round<T, BN>();
+        T* buf = reinterpret_cast<T*>(base + (size_t)NS * STAGE + (EPI_TMA ? e * 8192 : 0));  // 4 x 32 x ROUND
+        Ring chunk, tile;     // as the MMA issuer counts them
+        Ring rin;             // residual rounds consumed
+        int pending = 0;      // residual rounds loaded and not yet consumed
+        int ob = 0;           // output buffer in turn
+        Walk walk(P, worker);
+        int w, u;
+        while (walk.next(w, u)) {
             const TcProduct& p = P.p[w];
-            const int u = (int)(w ? t - P.p[0].tiles : t);
-            const int i0 = u % p.tiles_i * BM, j0 = u / p.tiles_i * BN + half * HALF;
-            const long long i = (long long)i0 + q * 32 + ti;
-            if (p.res != nullptr && S == 1)  // this warp's part of the residual comes to L2 while the products run
-                for (int c = lane; c < HALF; c += 32)
-                    if ((long long)j0 + c < p.J && i0 + q * 32 < p.I)
-                        prefetch_l2((const T*)p.res + ((long long)j0 + c) * p.ldr + i0 + q * 32);
-            float bias[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                bias[k] = (p.bias != nullptr && i + k < p.I) ? to_f32(((const T*)p.bias)[i + k]) : 0.f;
+            const int i0 = u % p.tiles_i * (BM * CG) + pr * BM + q * 32, j0 = u / p.tiles_i * BN + half * HALF;
+            const long long i = (long long)i0 + lane;
+            const bool by_tma = EPI_TMA && S == 1 && p.vec;
+            const int rounds = by_tma && i0 < p.I && j0 < p.J ? (int)min((long long)HALF / ROUND, (p.J - j0 + ROUND - 1) / ROUND) : 0;
+            // the residual comes in while the products run
+            if (by_tma && p.res != nullptr) {
+                for (int k = 0; k < 2 && k < rounds; ++k, ++pending)
+                    if (lane == 0) {
+                        uint64_t* bar = &res_full[e][(rin.slot + k) & 1];
+                        mbar_expect_tx(bar, 32 * ROUND * sizeof(T));
+                        tma_load_2d(buf + ((rin.slot + k) & 1) * 32 * ROUND, &maps.res, bar, i0, j0 + k * ROUND);
+                    }
+            }
+            const float bias = (p.bias != nullptr && i < p.I) ? to_f32(((const T*)p.bias)[i]) : 0.f;
+            float r[LD];
+            if (S == 1 && !by_tma) res_lane<T>(p, i, j0, r);
             const int kb0 = (int)((long long)p.nk * rank / S), kb1 = (int)((long long)p.nk * (rank + 1) / S);
             uint32_t acc_t = 0;  // TMEM columns that hold this warp's part of the finished tile
+            bool alive = true;
             if (PL == 3) {
                 float acc[HALF];
 #pragma unroll
                 for (int c = 0; c < HALF; ++c) acc[c] = 0.f;
                 const int nc = (kb1 - kb0 + CHUNK - 1) / CHUNK;
-                bool alive = true;
                 for (int ch = 0; ch < nc; ++ch) {
                     if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[chunk.slot], chunk.lap & 1, abort_flag))) {
                         alive = false;
@@ -520,83 +688,42 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
                     tc_fence_after();
                     acc_t = tmem + lane_base + chunk.slot * BN;
 #pragma unroll
-                    for (int c = 0; c < HALF; c += 8) {
-                        uint32_t v[8];
-                        tmem_ld<8>(acc_t + c, v);
+                    for (int c = 0; c < HALF; c += LD) {
+                        uint32_t v[LD];
+                        tmem_ld<LD>(acc_t + c, v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) acc[c + k] += __uint_as_float(v[k]);
+                        for (int k = 0; k < LD; ++k) acc[c + k] += __uint_as_float(v[k]);
                     }
                     if (ch + 1 < nc) {  // the last chunk's columns are released after the epilogue
                         tc_fence_before();
-                        mbar_arrive(&acc_empty[chunk.slot]);
+                        __syncwarp();
+                        if (lane == 0) arrive_leader<CG>(&acc_empty[chunk.slot]);
                         chunk.next(NB);
                     }
                 }
                 if (!alive) break;
                 const uint32_t cor_t = tmem + lane_base + ACC_COLS + tile.slot * BN;
 #pragma unroll
-                for (int c = 0; c < HALF; c += 8) {  // the finished sums go back to TMEM for the rolled loop below
-                    uint32_t v[8];
-                    tmem_ld<8>(cor_t + c, v);
+                for (int c = 0; c < HALF; c += LD) {  // the finished sums go back to TMEM for the rolled loops below
+                    uint32_t v[LD];
+                    tmem_ld<LD>(cor_t + c, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) acc[c + k] += __uint_as_float(v[k]);
-                    tmem_st8(acc_t + c, acc + c);
+                    for (int k = 0; k < LD; ++k) acc[c + k] += __uint_as_float(v[k]);
+#pragma unroll
+                    for (int k = 0; k < LD; k += 8) tmem_st8(acc_t + c + k, acc + c + k);
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
-                mbar_arrive(&cor_empty[tile.slot]);
+                __syncwarp();
+                if (lane == 0) arrive_leader<CG>(&cor_empty[tile.slot]);
             } else {
                 if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[chunk.slot], chunk.lap & 1, abort_flag))) break;
                 tc_fence_after();
                 acc_t = tmem + lane_base + chunk.slot * BN;
             }
-            if (S == 1) {
-                if (p.vec) {
-                    // 32 columns (or all) per round: their residual rows and accumulators are loaded together
-                    constexpr int ROUND = HALF < 32 ? HALF : 32;
-#pragma unroll 1
-                    for (int c = 0; c < HALF; c += ROUND) {
-                        Pack8<T> r[ROUND / 8];
-#pragma unroll
-                        for (int k = 0; k < ROUND / 8; ++k) res8<T>(p, i, (long long)j0 + c + k * 8 + tj, r[k]);
-#pragma unroll
-                        for (int d = 0; d < ROUND; d += COLS) {
-                            uint32_t v[COLS / 8][8];
-#pragma unroll
-                            for (int k = 0; k < COLS / 8; ++k) tmem_ld<8>(acc_t + c + d + k * 8, v[k]);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < COLS; ++k) stg[k * STG_LD + lane] = __uint_as_float(v[k / 8][k % 8]);
-                            __syncwarp();
-#pragma unroll
-                            for (int k = 0; k < COLS / 8; ++k) {
-                                const float* q8 = stg + (k * 8 + tj) * STG_LD + ti;
-                                const float4 lo = *reinterpret_cast<const float4*>(q8);
-                                const float4 hi = *reinterpret_cast<const float4*>(q8 + 4);
-                                float o[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                                const long long j = (long long)j0 + c + d + k * 8 + tj;
-                                if (i < p.I && j < p.J) finish8<T>(p, i, j, o, bias, r[d / 8 + k]);
-                            }
-                            __syncwarp();
-                        }
-                    }
-                } else {
-                    const long long il = (long long)i0 + q * 32 + lane;
-                    const float bl = (p.bias != nullptr && il < p.I) ? to_f32(((const T*)p.bias)[il]) : 0.f;
-#pragma unroll 1
-                    for (int c = 0; c < HALF; c += 8) {
-                        uint32_t v[8];
-                        tmem_ld<8>(acc_t + c, v);
-                        tmem_wait_ld();
-                        float o[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) o[k] = __uint_as_float(v[k]);
-                        finish_lane<T, 8>(p, il, (long long)j0 + c, o, bl);
-                    }
-                }
-            } else {
+            if (S > 1) {
                 // every stage of this tile has been consumed: its shared memory takes the partial tile
                 float* part = reinterpret_cast<float*>(base);
                 for (int c = 0; c < HALF; c += 8) {
@@ -606,32 +733,101 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
 #pragma unroll
                     for (int k = 0; k < 8; ++k) part[(half * HALF + c + k) * BM + q * 32 + lane] = __uint_as_float(v[k]);
                 }
+            } else if (by_tma) {
+#pragma unroll 1
+                for (int k = 0; k < rounds; ++k) {
+                    uint32_t v[ROUND];
+#pragma unroll
+                    for (int c = 0; c < ROUND; c += 16)
+                        tmem_ld<16>(acc_t + k * ROUND + c, reinterpret_cast<uint32_t(&)[16]>(v[c]));
+                    tmem_wait_ld();
+                    float o[ROUND];
+#pragma unroll
+                    for (int c = 0; c < ROUND; ++c) o[c] = __uint_as_float(v[c]) + bias;
+                    if (p.res != nullptr) {
+                        alive = __all_sync(0xffffffffu, mbar_wait(&res_full[e][rin.slot], rin.lap & 1, abort_flag));
+                        if (!alive) break;
+                        const T* rb = buf + rin.slot * 32 * ROUND + lane;
+#pragma unroll
+                        for (int c = 0; c < ROUND; ++c) o[c] += to_f32(rb[c * 32]);
+                        __syncwarp();
+                        --pending;
+                        if (k + 2 < rounds) {
+                            if (lane == 0) {
+                                fence_proxy_async_smem();
+                                mbar_expect_tx(&res_full[e][rin.slot], 32 * ROUND * sizeof(T));
+                                tma_load_2d(buf + rin.slot * 32 * ROUND, &maps.res, &res_full[e][rin.slot], i0,
+                                            j0 + (k + 2) * ROUND);
+                            }
+                            ++pending;
+                        }
+                        rin.next(2);
+                    }
+                    if (p.zout != nullptr) {
+                        put_round<T, ROUND>(buf + (2 + ob) * 32 * ROUND, o, &maps.z, i0, j0 + k * ROUND, lane);
+                        ob ^= 1;
+                    }
+                    activate<T>(o, p.act);
+                    put_round<T, ROUND>(buf + (2 + ob) * 32 * ROUND, o, &maps.out[w], i0, j0 + k * ROUND, lane);
+                    ob ^= 1;
+                }
+                if (!alive) break;
+            } else {
+                float rn[LD];
+#pragma unroll 1
+                for (int c = 0; c < HALF; c += LD) {
+                    uint32_t v[LD];
+                    tmem_ld<LD>(acc_t + c, v);
+                    if (c + LD < HALF) res_lane<T>(p, i, (long long)j0 + c + LD, rn);
+                    tmem_wait_ld();
+                    float o[LD];
+#pragma unroll
+                    for (int k = 0; k < LD; ++k) o[k] = __uint_as_float(v[k]);
+                    if ((long long)j0 + c < p.J) finish_lane<T>(p, i, (long long)j0 + c, o, bias, r);
+#pragma unroll
+                    for (int k = 0; k < LD; ++k) r[k] = rn[k];
+                }
             }
             tc_fence_before();
-            mbar_arrive(&acc_empty[chunk.slot]);
+            __syncwarp();
+            if (lane == 0) arrive_leader<CG>(&acc_empty[chunk.slot]);
             chunk.next(NB);
+            tile.next(NB);
+        }
+        // stores have read their buffers and reached memory, and no load into them is left behind
+        if (lane == 0) {
+            store_wait_all();
+            for (; pending > 0; --pending, rin.next(2)) {
+                const long long t0 = clock64();
+                while (!mbar_test(&res_full[e][rin.slot], rin.lap & 1) && clock64() - t0 < WAIT_CYCLES) {
+                }
+            }
         }
     }
 
     if (S > 1) {
         // one tile per cluster: join the partial tiles, each CTA its share of the columns
+        Walk walk(P, worker);
+        int w, u;
+        walk.next(w, u);
+        const TcProduct& p = P.p[w];
+        const int i0 = u % p.tiles_i * BM, j0 = u / p.tiles_i * BN;
+        const uint32_t part = smem_u32(base);
+        const int c0 = BN * rank / S, c1 = BN * (rank + 1) / S;
+        float bias[8];
+        {
+            const long long i = (long long)i0 + ((threadIdx.x - 64) & 15) * 8;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                bias[k] = (p.vec && p.bias != nullptr && i + k < p.I) ? to_f32(((const T*)p.bias)[i + k]) : 0.f;
+        }
         __syncwarp();
         cluster_sync_all();
-        if (warp >= 2 && tile0 < P.tiles) {
-            const int w = tile0 >= P.p[0].tiles;
-            const TcProduct& p = P.p[w];
-            const int u = (int)(w ? tile0 - P.p[0].tiles : tile0);
-            const int i0 = u % p.tiles_i * BM, j0 = u / p.tiles_i * BN;
-            const uint32_t part = smem_u32(base);
-            const int c0 = BN * (int)rank / S, c1 = BN * ((int)rank + 1) / S;
+        if (warp >= 2) {
             // all ranks' loads of a thread's share are issued before the first is used
             if (p.vec) {  // eight lanes of a column per thread
                 const int e = threadIdx.x - 64;
                 const long long i = (long long)i0 + (e & 15) * 8;
-                float bias[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    bias[k] = (p.bias != nullptr && i + k < p.I) ? to_f32(((const T*)p.bias)[i + k]) : 0.f;
                 for (int c = c0 + (e >> 4); c < c1; c += EPI_THREADS / 16) {
                     const long long j = (long long)j0 + c;
                     if (i >= p.I || j >= p.J) continue;
@@ -668,19 +864,27 @@ linear_tc_k(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
                         for (int r = 0; r < 8; ++r)
                             if (r < S) o[0] += x[r];
                         const float bl = (p.bias != nullptr && i < p.I) ? to_f32(((const T*)p.bias)[i]) : 0.f;
-                        finish_lane<T, 1>(p, i, j, o, bl);
+                        float res[1];
+                        res_lane<T>(p, i, j, res);
+                        finish_lane<T>(p, i, j, o, bl, res);
                     }
                 }
             }
         }
-        __syncwarp();
-        cluster_sync_all();  // no CTA leaves while another reads its partial tile
     }
     tc_fence_before();
-    __syncthreads();
+    if (CG > 1 || S > 1) {
+        __syncwarp();
+        cluster_sync_all();  // no CTA leaves while another reads its shared memory or arrives on its barriers
+    } else {
+        __syncthreads();
+    }
     if (warp == 2) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+        if (CG == 2)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
     }
     if (threadIdx.x == 0 && abort_sh) atomicExch(&g_ops_timeout, 1);
 }
@@ -899,8 +1103,25 @@ bool make_map(CUtensorMap* map, const Operand16& o, int planes, bool mn, int bk,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of an output, a residual or z for the epilogue's rounds: boxes of 32 columns x `rows` rows.
+template <typename T>
+bool make_rows(CUtensorMap* map, const void* ptr, long long cols, long long rows, long long ld, int box) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld * sizeof(T)};
+    cuuint32_t boxes[2] = {32, (cuuint32_t)box}, estr[2] = {1, 1};
+    const CUtensorMapDataType t = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                  : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return fn(map, t, 2, const_cast<void*>(ptr), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 16-byte rows that TMA can address too (its strides end at 2^40 bytes).
 bool aligned16(const void* p, long long ld, int e) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * e) % 16 == 0;
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * e) % 16 == 0 && ld < (1LL << 37);
 }
 
 // Rows of a block are 8 * steps: 64, or fewer (down to 8) until the blocks fill the SMs. Depends on the sizes alone, so
@@ -933,7 +1154,7 @@ struct Carver {
 Operand16 operand(int dtype, const void* src, long long ld, long long rows, int cols, Carver& w, PackJob* job) {
     const int e = dtype == VF_F32 ? 4 : 2;
     *job = PackJob{};
-    if (e == 2 && aligned16(src, ld, e) && ld < (1LL << 38)) return Operand16{src, rows, ld, cols};
+    if (e == 2 && aligned16(src, ld, e)) return Operand16{src, rows, ld, cols};
     job->src = src;
     job->ld = ld;
     job->rows = rows;
@@ -1000,37 +1221,39 @@ cudaError_t cluster_limit(const void* kern, const cudaLaunchConfig_t* cfg, int* 
 
 template <typename T, int PL, int BN>
 cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int count, int sms, cudaStream_t s) {
-    constexpr int BK = block_k<PL>();
+    constexpr int BK = block_k<PL>(), CG = pair_of<BN>();
     const bool bf16 = PL == 3 || std::is_same<T, __nv_bfloat16>::value;
-    CUtensorMap ma[2], mb[2];
+    Maps m;
+    memset(&m, 0, sizeof(m));
     int min_nk = 1 << 30;
-    P.tiles = 0;
+    long long tiles = 0;
     for (int k = 0; k < count; ++k) {
         TcProduct& p = P.p[k];
         p.a_mn = A[k].mn;
         p.b_mn = B[k].mn;
-        p.tiles_i = (int)((p.I + BM - 1) / BM);
-        p.tiles = (long long)p.tiles_i * ((p.J + BN - 1) / BN);
-        P.tiles += p.tiles;
+        p.tiles_i = (int)((p.I + BM * CG - 1) / (BM * CG));
+        const long long n = (long long)p.tiles_i * ((p.J + BN - 1) / BN);
+        if (n > 0x3fffffffLL) return cudaErrorInvalidValue;  // tile numbers are ints
+        p.tiles = (int)n;
+        tiles += n;
         min_nk = std::min(min_nk, p.nk);
-        if (P.tiles > 0x7fffffffLL) return cudaErrorInvalidValue;  // tile numbers of a product are ints
-        if (!make_map(&ma[k], A[k].o, PL, A[k].mn, BK, BM, bf16) || !make_map(&mb[k], B[k].o, PL, B[k].mn, BK, BN, bf16))
+        if (!make_map(&m.a[k], A[k].o, PL, A[k].mn, BK, BM, bf16) || !make_map(&m.b[k], B[k].o, PL, B[k].mn, BK, BN / CG, bf16))
             return cudaErrorInvalidValue;
-    }
-    if (count == 0) memset(ma, 0, sizeof(ma)), memset(mb, 0, sizeof(mb));
-    if (count < 2) {
-        ma[1] = ma[0];
-        mb[1] = mb[0];
-        if (count == 1) P.p[1].tiles = 0;
+        constexpr int R = epi_round<T, BN>();
+        if (BN >= 64 && p.vec &&
+            (!make_rows<T>(&m.out[k], p.out, p.I, p.J, p.ldo, R) ||
+             (p.res != nullptr && !make_rows<T>(&m.res, p.res, p.I, p.J, p.ldr, R)) ||
+             (p.zout != nullptr && !make_rows<T>(&m.z, p.zout, p.I, p.J, p.ldz, R))))
+            return cudaErrorInvalidValue;
     }
     auto kern = linear_tc_k<T, PL, BN>;
     cudaError_t e = allow_dyn_smem((const void*)kern, smem_limit<BN>() - 1024);
     if (e != cudaSuccess) return e;
     const int need = stage_bytes<PL, BN>();
-    P.stages = std::min(MAX_STAGES, (smem_limit<BN>() - 1024 - 1024 - stg_bytes<PL, BN>()) / need);
+    P.stages = std::min(MAX_STAGES, (smem_limit<BN>() - 1024 - 1024 - epi_bytes<BN>()) / need);
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(NUM_THREADS);
-    cfg.dynamicSmemBytes = 1024 + (size_t)P.stages * need + stg_bytes<PL, BN>();
+    cfg.dynamicSmemBytes = 1024 + (size_t)P.stages * need + epi_bytes<BN>();
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1042,21 +1265,22 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
     // run at once (a cluster's CTAs share a GPC, so fewer may fit than the SMs suggest).
     P.split = 1;
     const int slots = sms * ctas_per_sm<BN>();
-    while (count > 0 && P.split < 8 && P.tiles * P.split * 2 <= slots && min_nk >= P.split * 4) {
+    while (CG == 1 && count > 0 && P.split < 8 && tiles * P.split * 2 <= slots && min_nk >= P.split * 4) {
         at[0].val.clusterDim.x = P.split * 2;
         cfg.numAttrs = 1;
-        cfg.gridDim = dim3((unsigned)(P.tiles * P.split * 2));
+        cfg.gridDim = dim3((unsigned)(tiles * P.split * 2));
         int fit = 0;
         if ((e = cluster_limit((const void*)kern, &cfg, &fit)) != cudaSuccess) return e;
-        if (fit < P.tiles) break;
+        if (fit < tiles) break;
         P.split *= 2;
     }
-    long long grid = P.split > 1 ? P.tiles * P.split : std::min<long long>(P.tiles, slots);
-    if (P.tiles == 0) grid = std::min<long long>((P.N + EPI_THREADS - 1) / EPI_THREADS, sms);
-    cfg.gridDim = dim3((unsigned)grid);
-    at[0].val.clusterDim.x = P.split;
+    P.workers = (int)std::min<long long>(tiles, P.split > 1 ? tiles : slots / CG);
+    if (tiles == 0) P.workers = std::min((P.N + EPI_THREADS - 1) / EPI_THREADS, sms);
+    P.gap = P.split > 1 || count < 2 ? 1 : std::max(1, (P.p[0].nk + P.p[1].nk / 2) / P.p[1].nk);
+    cfg.gridDim = dim3((unsigned)(P.workers * CG * P.split));
+    at[0].val.clusterDim.x = CG * P.split;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, ma[0], mb[0], ma[1], mb[1], P);
+    return cudaLaunchKernelEx(&cfg, kern, m, P);
 }
 
 template <typename T, int PL>
@@ -1078,7 +1302,10 @@ cudaError_t launch_pl(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
         return n;
     };
     auto cost = [&](int bn) { return (tiles(bn) + sms - 1) / sms * (bn + 48); };
-    if (J > 128 && cost(256) <= cost(128) && cost(256) <= cost(64)) return launch_bn<T, PL, 256>(P, A, B, count, sms, s);
+    long long I = 1;
+    for (int k = 0; k < count; ++k) I = std::max(I, P.p[k].I);
+    if (J > 128 && I > BM && cost(256) <= cost(128) && cost(256) <= cost(64))
+        return launch_bn<T, PL, 256>(P, A, B, count, sms, s);
     if (J > 64 && cost(128) <= cost(64)) return launch_bn<T, PL, 128>(P, A, B, count, sms, s);
     return launch_bn<T, PL, 64>(P, A, B, count, sms, s);
 }
@@ -1112,13 +1339,15 @@ size_t linear_tc_workspace(int dtype, long long M, int N, int K, bool grad) {
     return n;
 }
 
-cudaError_t launch_linear_tc(const LinearFwd& f, void* work, cudaStream_t s) {
+cudaError_t launch_linear_tc(const LinearFwd& f, void* work, size_t have, size_t* need, cudaStream_t s) {
     const int e = f.dtype == VF_F32 ? 4 : 2;
     Carver w{(uint8_t*)work};
     PackJob jx, jw;
     Side A[2] = {}, B[2] = {};
     A[0] = Side{operand(f.dtype, f.W, f.ldw, f.N, f.K, w, &jw), false};
     B[0] = Side{operand(f.dtype, f.x, f.ldx, f.M, f.K, w, &jx), false};
+    *need = w.used;
+    if (w.used > have) return cudaSuccess;  // the caller reports it
     cudaError_t err = launch_operands(f.dtype, GradJob{}, jw, jx, s);
     if (err != cudaSuccess) return err;
     TcParams P{};
@@ -1139,7 +1368,7 @@ cudaError_t launch_linear_tc(const LinearFwd& f, void* work, cudaStream_t s) {
     return launch_products(f.dtype, P, A, B, 1, s);
 }
 
-cudaError_t launch_linear_grad_tc(const LinearGrad& f, void* work, cudaStream_t s) {
+cudaError_t launch_linear_grad_tc(const LinearGrad& f, void* work, size_t have, size_t* need, cudaStream_t s) {
     const int e = f.dtype == VF_F32 ? 4 : 2;
     Carver w{(uint8_t*)work};
     const bool products = f.dx != nullptr || f.dW != nullptr;
@@ -1157,9 +1386,9 @@ cudaError_t launch_linear_grad_tc(const LinearGrad& f, void* work, cudaStream_t 
     gj.vec_r = f.dr != nullptr && aligned16(f.dr, f.lddr, e);
     Operand16 g{};
     if (products) {
-        if (e == 2 && f.act == VF_ACT_NONE && aligned16(f.dy, f.lddy, e) && f.lddy < (1LL << 38)) {
+        if (e == 2 && f.act == VF_ACT_NONE && aligned16(f.dy, f.lddy, e)) {
             g = Operand16{f.dy, f.M, f.lddy, f.N};  // dy is g, and TMA can read it
-        } else if (e == 2 && gj.vec_r && f.lddr < (1LL << 38)) {
+        } else if (e == 2 && gj.vec_r) {
             g = Operand16{f.dr, f.M, f.lddr, f.N};  // dr is g
         } else {
             gj.ldp = round_up(f.N, 64);
@@ -1198,6 +1427,13 @@ cudaError_t launch_linear_grad_tc(const LinearGrad& f, void* work, cudaStream_t 
         p.out = f.dW;
         p.ldo = f.lddw;
         p.vec = aligned16(f.dW, f.lddw, e);
+    }
+    *need = w.used;
+    if (w.used > have) return cudaSuccess;  // the caller reports it
+    if (count == 2 && P.p[1].nk > P.p[0].nk) {
+        std::swap(P.p[0], P.p[1]);
+        std::swap(A[0], A[1]);
+        std::swap(B[0], B[1]);
     }
     cudaError_t err = launch_operands(f.dtype, gj, jw, jx, s);
     if (err != cudaSuccess) return err;

@@ -66,11 +66,13 @@ int check_vector(const char* name, const void* p, int dtype) {
     return VF_OK;
 }
 
-int check_work(const void* work, size_t have, size_t need) {
-    if (need == 0) return VF_OK;
-    if (work == nullptr || have < need)
-        return ops_fail(VF_ERR_WORKSPACE, "workspace of %zu bytes, this call needs %zu", work == nullptr ? 0 : have, need);
+int check_aligned(const void* work) {
     if (reinterpret_cast<uintptr_t>(work) % 256 != 0) return ops_fail(VF_ERR_ARG, "workspace is not 256-byte aligned");
+    return VF_OK;
+}
+
+int check_work(size_t have, size_t need) {
+    if (have < need) return ops_fail(VF_ERR_WORKSPACE, "workspace of %zu bytes, this call needs %zu", have, need);
     return VF_OK;
 }
 
@@ -148,8 +150,11 @@ int vf_linear(int dtype, int act, const void* x, long long ldx, const void* W, l
     if (z != nullptr) OPS_TRY(check_matrix("z", z, M, N, ldz, dtype));
     const LinearFwd p{dtype, act, x, ldx, W, ldw, b, r, ldr, M, N, K, y, ldy, z, ldz};
     if (!use_tc(M, N, K)) return launched(launch_linear_ffma(p, (cudaStream_t)stream));
-    OPS_TRY(check_work(work, work_bytes, linear_tc_workspace(dtype, M, N, K, false)));
-    return launched(launch_linear_tc(p, work, (cudaStream_t)stream));
+    OPS_TRY(check_aligned(work));
+    size_t need = 0;
+    const size_t have = work == nullptr ? 0 : work_bytes;
+    OPS_TRY(launched(launch_linear_tc(p, work, have, &need, (cudaStream_t)stream)));
+    return check_work(have, need);
 }
 
 int vf_linear_grad(int dtype, int act, const void* dy, long long lddy, const void* z, long long ldz, const void* x,
@@ -172,8 +177,11 @@ int vf_linear_grad(int dtype, int act, const void* dy, long long lddy, const voi
     if (dr != nullptr) OPS_TRY(check_matrix("dr", dr, M, N, lddr, dtype));
     const LinearGrad p{dtype, act, dy, lddy, z, ldz, x, ldx, W, ldw, M, N, K, dx, lddx, dW, lddw, db, dr, lddr};
     if (!use_tc(M, N, K)) return launched(launch_linear_grad_ffma(p, (cudaStream_t)stream));
-    OPS_TRY(check_work(work, work_bytes, linear_tc_workspace(dtype, M, N, K, true)));
-    return launched(launch_linear_grad_tc(p, work, (cudaStream_t)stream));
+    OPS_TRY(check_aligned(work));
+    size_t need = 0;
+    const size_t have = work == nullptr ? 0 : work_bytes;
+    OPS_TRY(launched(launch_linear_grad_tc(p, work, have, &need, (cudaStream_t)stream)));
+    return check_work(have, need);
 }
 
 int vf_ops_check(void) {
@@ -213,7 +221,8 @@ int vf_clip_grad_norm(int n, const void* const* grads, void* const* outs, const 
     OPS_TRY(check_overlaps(l));
     size_t need = 0;
     OPS_TRY(vf_clip_workspace(n, &need));
-    OPS_TRY(check_work(work, work_bytes, need));
+    OPS_TRY(check_aligned(work));
+    OPS_TRY(check_work(work == nullptr ? 0 : work_bytes, need));
     return launched(launch_clip(l, scale, max_norm, norm, (double*)work, (cudaStream_t)stream));
 }
 

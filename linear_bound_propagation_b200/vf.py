@@ -558,14 +558,15 @@ def linear(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tensor] = None,
     bp = None if b is None else _vector("b", b, N, tt, dev)
     rp, ldr = (None, 0) if residual is None else _matrix("residual", residual, shape, tt, dev)
     if out is None:
-        y = torch.empty(shape, device=x.device, dtype=tt)
+        y = torch.empty_strided(shape, (N, 1), device=x.device, dtype=tt)
         yp, ldy = y.data_ptr(), N
     else:
         y = out
         yp, ldy = _matrix("out", y, shape, tt, dev)
-    z = torch.empty(shape, device=x.device, dtype=tt) if want_z else None
-    nbytes = _linear_work(dtype, M, N, K, 0)
-    work = torch.empty(nbytes, device=x.device, dtype=torch.uint8) if nbytes else None
+    z = torch.empty_strided(shape, (N, 1), device=x.device, dtype=tt) if want_z else None
+    # 16-bit operands with 16-byte rows are read in place
+    nbytes = 0 if dtype and (xp | wp) & 15 == 0 and (ldx | ldw) & 7 == 0 else _linear_work(dtype, M, N, K, 0)
+    work = torch.empty_strided((nbytes,), (1,), device=x.device, dtype=torch.uint8) if nbytes else None
     _check(lib().vf_linear(dtype, a, xp, ldx, wp, ldw, bp, rp, ldr, M, N, K, yp, ldy, None if z is None else z.data_ptr(),
                            N, None if work is None else work.data_ptr(), nbytes,
                            torch._C._cuda_getCurrentRawStream(dev)))
@@ -591,12 +592,12 @@ def linear_grad(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, act: str = "
     xp, ldx = _matrix("x", x, (M, K), tt, dev)
     wp, ldw = _matrix("W", W, (N, K), tt, dev)
     device = x.device
-    dx = torch.empty((M, K), device=device, dtype=tt) if "dx" in need else None
-    dW = torch.empty((N, K), device=device, dtype=tt) if "dW" in need else None
-    db = torch.empty((N,), device=device, dtype=tt) if "db" in need else None
-    dr = torch.empty(shape, device=device, dtype=tt) if "dr" in need else None
+    dx = torch.empty_strided((M, K), (K, 1), device=device, dtype=tt) if "dx" in need else None
+    dW = torch.empty_strided((N, K), (K, 1), device=device, dtype=tt) if "dW" in need else None
+    db = torch.empty_strided((N,), (1,), device=device, dtype=tt) if "db" in need else None
+    dr = torch.empty_strided(shape, (N, 1), device=device, dtype=tt) if "dr" in need else None
     nbytes = _linear_work(dtype, M, N, K, 1)
-    work = torch.empty(nbytes, device=device, dtype=torch.uint8) if nbytes else None
+    work = torch.empty_strided((nbytes,), (1,), device=device, dtype=torch.uint8) if nbytes else None
     _check(lib().vf_linear_grad(dtype, a, dyp, lddy, zp, ldz, xp, ldx, wp, ldw, M, N, K,
                                 None if dx is None else dx.data_ptr(), K, None if dW is None else dW.data_ptr(), K,
                                 None if db is None else db.data_ptr(), None if dr is None else dr.data_ptr(), N,

@@ -160,6 +160,22 @@ def test_small_whole_numbers_are_exact(dtype, M, N, K):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K", [(4090, 1016, 72), (4096, 1020, 200), (2050, 2048, 2040), (8200, 520, 264)])
+def test_many_large_tiles(dtype, M, N, K):
+    """Sizes whose tiles are 256 x 256 and shared by a pair of CTAs, several per pair, ragged in every direction."""
+    check_forward(dtype, M, N, K, "relu", True, True, 0, 0, 1)
+    check_forward(dtype, M, N, K, "gelu", True, False, 3, 1, 2)
+    check_grad(dtype, M, N, K, "silu", 0, 0, 3)
+    check_grad(dtype, M, N, K, "relu", 8, 8, 4, ("dx", "dW"))
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    x, W, r = (torch.randint(-2, 3, s, generator=gen, device="cuda").to(dtype) for s in ((M, K), (N, K), (M, N)))
+    assert torch.equal(vf.linear(x, W, residual=r)["y"], (x.double() @ W.double().t() + r.double()).to(dtype))
+    got = vf.linear_grad(r, x, W)
+    assert torch.equal(got["dx"], (r.double() @ W.double()).to(dtype))
+    assert torch.equal(got["dW"], (r.double().t() @ x.double()).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_empty_sizes(dtype):
     e = lambda *s: torch.zeros(*s, device="cuda", dtype=dtype)  # noqa: E731
     assert vf.linear(e(0, 4), e(3, 4), e(3))["y"].shape == (0, 3)
