@@ -15,8 +15,9 @@
 // a sum of positive terms over 512 MMAs comes out 1e-5 low), so the five small products go to an accumulator of their own, and
 // the h h accumulator is added to registers, rounding to nearest, every CHUNK of the reduction.
 //
-// Roles (10 warps; one CTA per SM, or a pair of CTAs on two SMs for 256 x 256 tiles; persistent over the tiles): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9
-// epilogue (warp 2 owns the TMEM allocation; TMEM lane quarter warp % 4; 2-5 the first half of the tile's columns, 6-9 the second).
+// Roles (one CTA per SM, or a pair of CTAs on two SMs for 256 x 256 tiles; persistent over the tiles): warp 0 TMA
+// producer, warp 1 MMA issuer, warps 2 and up epilogue (lane quarter warp % 4 of TMEM, four warps to a share of the
+// tile's columns; warp 2 owns the TMEM allocation).
 // When the tiles are too few to fill the SMs, the reduction is split over a cluster of 2, 4 or 8 CTAs, which
 // join their partial tiles through distributed shared memory in rank order. All waits are bounded: on expiry an abort
 // flag stops every role, copies and MMAs in flight are waited for (also bounded), TMEM is freed and a device flag set.
@@ -29,7 +30,7 @@
 #include <tuple>
 #include <type_traits>
 
-#include "tc_ptx.cuh"
+#include "linear_tc.cuh"
 #include "vf_internal.cuh"
 #include "vf_ops.cuh"
 
@@ -38,42 +39,32 @@ namespace vf {
 namespace {
 
 using namespace tc;
+using namespace lin;
 
 __device__ int g_ops_timeout;
 
-constexpr int BM = 128;
-constexpr int NUM_THREADS = 320;
-constexpr int EPI_THREADS = 256;
+// Epilogue warps: 16 behind the 256-column tiles, each with a quarter of the columns of its 32 lanes, else 8 with half.
+template <int BN>
+constexpr int epi_warps() {
+    return BN == 256 ? 16 : 8;
+}
+template <int BN>
+constexpr int threads_of() {
+    return 64 + 32 * epi_warps<BN>();
+}
 constexpr int MAX_STAGES = 8;
-constexpr int CHUNK = 8;            // k-blocks of 32 between two additions of the h h accumulator (PL = 3)
+constexpr int CHUNK = 16;           // k-blocks of 32 between two additions of the h h accumulator (PL = 3)
 
 template <int PL>
 constexpr int block_k() {
     return PL == 3 ? 32 : 64;
 }
 
-struct TcProduct {
-    long long I, J;      // output columns (contiguous) and rows
-    int nk;              // blocks of the reduction
-    int a_mn, b_mn;      // operand contiguous along i (j) instead of t
-    int tiles_i;
-    int tiles;
-    void* out;
-    long long ldo;
-    const void* bias;
-    const void* res;
-    long long ldr;
-    void* zout;
-    long long ldz;
-    int act;
-    int vec;             // output, residual and z rows all allow 16-byte accesses (and TMA)
-};
-
 struct TcParams {
     TcProduct p[2];      // the longer reduction first
     int gap;             // tiles of p[1] that take about as long as one of p[0]
     int workers;         // CTAs, pairs or clusters that walk the tiles
-    int split;           // CTAs per tile (cluster size)
+    int split, split_log;  // CTAs per tile (cluster size), a power of two
     int stages;
     // column sums of g, joined here: db[n] = sum_q part[q * N + n]
     const float* part;
@@ -134,38 +125,6 @@ __device__ __forceinline__ void store_tile(const CUtensorMap* map, const void* s
 __device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// D (tmem) (+)= A (smem) x B (smem), kind::f16.
-template <int CG>
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    if (CG == 1)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "l"(a), "l"(b), "r"(idesc), "r"(acc)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "l"(a), "l"(b), "r"(idesc), "r"(acc)
-            : "memory");
-}
-
-// Position in the ring of stages: slot and how often the ring has been passed. Kept as counters: the roles below are
-// single threads, for which a division per block would cost more than the block's MMAs.
-struct Ring {
-    int slot = 0;
-    uint32_t lap = 0;
-    __device__ __forceinline__ void next(int stages) {
-        if (++slot == stages) {
-            slot = 0;
-            ++lap;
-        }
-    }
-};
-
 // Two CTAs of a pair (CG = 2) compute one tile: the first issues the MMAs for both, so barriers that its issuer waits on
 // live in its shared memory, and commits arrive in both.
 __device__ __forceinline__ uint32_t leader_addr(const void* p) {
@@ -207,191 +166,18 @@ __device__ __forceinline__ void load_operand(void* dst, const CUtensorMap* map, 
             : "memory");
 }
 
-// Operand of rows x BK elements in shared memory. Contiguous along t: rows of BK elements (128 or 64 bytes, swizzled
-// over as many bytes), 8-row groups one after the other. Contiguous along i or j: atoms of 64 elements x BK steps of t,
-// 128-byte rows swizzled over 128 bytes, 8-step groups 1024 bytes apart, atoms BK * 128 bytes apart.
-template <int BK>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, int mn) {
-    const uint64_t base = (uint64_t)((saddr >> 4) & 0x3FFF) | (1ull << 46);
-    if (mn) return base | ((uint64_t)(BK * 128 / 16) << 16) | (64ull << 32) | (2ull << 61);
-    return base | (1ull << 16) | ((uint64_t)(8 * BK * 2 / 16) << 32) | ((BK == 64 ? 2ull : 4ull) << 61);
-}
-
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]);
-template <>
-__device__ __forceinline__ void tmem_ld<8>(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
-template <>
-__device__ __forceinline__ void tmem_ld<16>(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-                 "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-                 "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
-                 : "memory");
-}
-
-// One lane of a converged warp. tcgen05 and TMA instructions take their operands from uniform registers: behind
-// elect.sync the compiler knows that a single lane runs and issues them back to back; behind `lane == 0` every MMA took
-// about 110 cycles to issue.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t on;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(on));
-    return on != 0;
-}
-
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
-// Programmatic dependent launch: grid_wait returns when the launches before have completed and their writes are seen;
-// grid_trigger lets the next launch begin its prologue.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ float ld_cluster(uint32_t saddr, uint32_t rank) {
-    uint32_t a;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ float4 ld_cluster4(uint32_t saddr, uint32_t rank) {
-    uint32_t a;
-    float4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
-}
-
-template <typename T>
-struct alignas(16) Pack8 {
-    T v[8];
-};
-
-template <typename T, int N>
-__device__ __forceinline__ void activate(float (&v)[N], int act) {
-    constexpr bool FAST = sizeof(T) == 2;
-    switch (act) {
-        case VF_ACT_RELU:
-#pragma unroll
-            for (int u = 0; u < N; ++u) v[u] = act_value<FAST>(v[u], VF_ACT_RELU);
-            break;
-        case VF_ACT_GELU:
-#pragma unroll
-            for (int u = 0; u < N; ++u) v[u] = act_value<FAST>(v[u], VF_ACT_GELU);
-            break;
-        case VF_ACT_SILU:
-#pragma unroll
-            for (int u = 0; u < N; ++u) v[u] = act_value<FAST>(v[u], VF_ACT_SILU);
-            break;
-        default: break;
-    }
-}
-
-// Rows that allow 16-byte accesses: eight consecutive outputs i .. i + 7 of row j per thread. The residual is loaded
-// ahead (res8) so that several rows' loads are in flight.
-template <typename T>
-__device__ __forceinline__ void res8(const TcProduct& p, long long i, long long j, Pack8<T>& w) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u) w.v[u] = from_f32<T>(0.f);
-    if (p.res == nullptr || j >= p.J) return;
-    const T* r = (const T*)p.res + j * p.ldr + i;
-    if (i + 8 <= p.I) {
-        w = *reinterpret_cast<const Pack8<T>*>(r);
-    } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (i + u < p.I) w.v[u] = r[u];
-    }
-}
-template <typename T>
-__device__ __forceinline__ void put8(T* o, int n, const float (&v)[8]) {
-    Pack8<T> w;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) w.v[u] = from_f32<T>(v[u]);
-    if (n >= 8) {
-        *reinterpret_cast<Pack8<T>*>(o) = w;
-    } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (u < n) o[u] = w.v[u];
-    }
-}
-template <typename T>
-__device__ __forceinline__ void finish8(const TcProduct& p, long long i, long long j, float (&v)[8], const float (&bias)[8],
-                                        const Pack8<T>& r) {
-    const int n = (int)min(8LL, p.I - i);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] += bias[u] + to_f32(r.v[u]);
-    if (p.zout != nullptr) put8<T>((T*)p.zout + j * p.ldz + i, n, v);
-    activate<T>(v, p.act);
-    put8<T>((T*)p.out + j * p.ldo + i, n, v);
-}
-
-// One element i of N rows j .. j + N - 1 per thread, a warp's lanes on consecutive elements: fp32 rows (a warp's access
-// is a whole 128-byte line) and rows that do not allow 16-byte accesses.
-template <typename T, int N>
-__device__ __forceinline__ void res_lane(const TcProduct& p, long long i, long long j, float (&r)[N]) {
-#pragma unroll
-    for (int u = 0; u < N; ++u)
-        r[u] = (p.res != nullptr && i < p.I && j + u < p.J) ? to_f32(((const T*)p.res)[(j + u) * p.ldr + i]) : 0.f;
-}
-template <typename T, int N>
-__device__ __forceinline__ void finish_lane(const TcProduct& p, long long i, long long j, float (&v)[N], float bias,
-                                            const float (&r)[N]) {
-    if (i >= p.I) return;
-    const int n = (int)min((long long)N, p.J - j);
-#pragma unroll
-    for (int u = 0; u < N; ++u) v[u] += bias + r[u];
-    if (p.zout != nullptr) {
-        T* z = (T*)p.zout + j * p.ldz + i;
-#pragma unroll
-        for (int u = 0; u < N; ++u)
-            if (u < n) z[u * p.ldz] = from_f32<T>(v[u]);
-    }
-    activate<T>(v, p.act);
-    T* o = (T*)p.out + j * p.ldo + i;
-#pragma unroll
-    for (int u = 0; u < N; ++u)
-        if (u < n) o[u * p.ldo] = from_f32<T>(v[u]);
-}
-
 // Epilogue through TMA (tiles of 64 columns and more whose rows allow it): a warp handles its 32 lanes in rounds of
-// ROUND columns, with two 2 KB buffers for the residual on its way in and two for z and y on their way out.
-template <typename T, int BN>
-constexpr int epi_round() {
-    return sizeof(T) == 4 ? 16 : 32;
-}
+// ROUND columns, with two buffers for the residual on its way in and two for z and y on their way out, 64 KB in all.
 template <int BN>
 constexpr int epi_bytes() {
-    return BN >= 64 ? 8 * 4 * 2048 : 0;
+    return BN >= 64 ? 65536 : 0;
+}
+template <typename T, int BN>
+constexpr int epi_round() {
+    return 65536 / epi_warps<BN>() / 4 / 32 / (int)sizeof(T);
 }
 // A pair of CTAs takes the 256-column tiles: each loads half of both operands, which halves what a CTA reads per MMA.
 template <int BN>
@@ -414,21 +200,45 @@ constexpr int stage_bytes() {
     return PL * (BM + BN / pair_of<BN>()) * block_k<PL>() * 2;
 }
 
+// N columns of this lane, 32 elements apart. The 16-bit conversions work on pairs.
+template <int N>
+__device__ __forceinline__ void put_lane(float* o, const float (&v)[N]) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) o[c * 32] = v[c];
+}
+template <int N>
+__device__ __forceinline__ void put_lane(__nv_bfloat16* o, const float (&v)[N]) {
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        const __nv_bfloat162 w = __floats2bfloat162_rn(v[c], v[c + 1]);
+        o[c * 32] = w.x;
+        o[c * 32 + 32] = w.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void put_lane(__half* o, const float (&v)[N]) {
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        const __half2 w = __floats2half2_rn(v[c], v[c + 1]);
+        o[c * 32] = w.x;
+        o[c * 32 + 32] = w.y;
+    }
+}
+
 // One round of a warp: 32 lanes x N columns to shared memory, a column's 32 elements together, and on to rows
 // y .. y + N - 1 of the map. Two buffers take turns: the store before last has read the one written here.
 template <typename T, int N>
 __device__ __forceinline__ void put_round(T* buf, const float (&v)[N], const CUtensorMap* map, int x, int y, int lane) {
     if (lane == 0) store_wait_read();
     __syncwarp();
-#pragma unroll
-    for (int c = 0; c < N; ++c) buf[c * 32 + lane] = from_f32<T>(v[c]);
+    put_lane<N>(buf + lane, v);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) store_tile(map, buf, x, y);
 }
 
 template <typename T, int PL, int BN>
-__global__ void __launch_bounds__(NUM_THREADS, ctas_per_sm<BN>())
+__global__ void __launch_bounds__(threads_of<BN>(), ctas_per_sm<BN>())
 linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams P) {
     constexpr int BK = block_k<PL>();
     constexpr int CG = pair_of<BN>();
@@ -439,13 +249,14 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
     constexpr int ACC_COLS = NB * BN;
     constexpr int USED_COLS = PL == 3 ? 2 * ACC_COLS : ACC_COLS;
     constexpr int TMEM_COLS = USED_COLS < 32 ? 32 : USED_COLS;
-    constexpr int HALF = BN / 2;
-    constexpr int LD = HALF < 16 ? 8 : 16;                   // columns per TMEM load
+    constexpr int EW = epi_warps<BN>(), EPI_THREADS = 32 * EW;
+    constexpr int PART = BN / (EW / 4);                      // columns of an epilogue warp
+    constexpr int LD = PART < 16 ? 8 : 16;                   // columns per TMEM load
     constexpr bool EPI_TMA = BN >= 64;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], cor_empty[2], done_bar;
-    __shared__ uint64_t res_full[8][2];
+    __shared__ uint64_t res_full[EW][2];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
 
@@ -455,7 +266,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
     const int crank = (CG > 1 || S > 1) ? (int)cluster_rank() : 0;
     const int rank = CG == 1 ? crank : 0;   // share of a split reduction
     const int pr = CG == 2 ? crank : 0;     // place in a pair
-    const int worker = blockIdx.x / (CG * S);
+    const int worker = CG == 2 ? blockIdx.x >> 1 : blockIdx.x >> P.split_log;
 
     // The producer needs the barriers only; TMEM is allocated beside its first loads.
     if (threadIdx.x == 0) {
@@ -466,10 +277,10 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&acc_full[s], 1);
-            mbar_init(&acc_empty[s], 8 * CG);  // one arrival per epilogue warp
-            mbar_init(&cor_empty[s], 8 * CG);
+            mbar_init(&acc_empty[s], EW * CG);  // one arrival per epilogue warp
+            mbar_init(&cor_empty[s], EW * CG);
         }
-        for (int s = 0; s < 16; ++s) mbar_init(&res_full[s >> 1][s & 1], 1);
+        for (int s = 0; s < 2 * EW; ++s) mbar_init(&res_full[s >> 1][s & 1], 1);
         mbar_init(&done_bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -505,7 +316,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
             }
         }
         tc_fence_before();
-        asm volatile("bar.sync 1, %0;" ::"r"(NUM_THREADS - 32) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"r"(32 + EPI_THREADS) : "memory");
         tc_fence_after();
         tmem = tmem_base_sh;
     }
@@ -522,10 +333,10 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                 const int i0 = u % p.tiles_i * (BM * CG) + pr * BM, j0 = u / p.tiles_i * BN + pr * BL;
                 const CUtensorMap* ma = &maps.a[w];
                 const CUtensorMap* mb = &maps.b[w];
-                const int kb0 = (int)((long long)p.nk * rank / S), kb1 = (int)((long long)p.nk * (rank + 1) / S);
+                const int kb0 = share(p.nk, rank, P.split_log), kb1 = share(p.nk, rank + 1, P.split_log);
                 const bool a_mn = p.a_mn, b_mn = p.b_mn;
                 for (int kb = kb0; kb < kb1; ++kb, g.next(NS)) {
-                    if (g.lap > 0 && !mbar_wait(&empty[g.slot], (g.lap - 1) & 1, abort_flag)) break;
+                    if (g.lap > 0 && !wait_phase(&empty[g.slot], (g.lap - 1) & 1, abort_flag)) break;
                     uint8_t* st = base + (size_t)g.slot * STAGE;
                     uint32_t bar = smem_u32(&full[g.slot]);
                     if (CG == 1 || pr == 0) mbar_expect_tx(&full[g.slot], STAGE * CG);
@@ -574,7 +385,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
             int w, u;
             while (ok && !*abort_flag && walk.next(w, u)) {
                 const TcProduct& p = P.p[w];
-                const int kb0 = (int)((long long)p.nk * rank / S), kb1 = (int)((long long)p.nk * (rank + 1) / S);
+                const int kb0 = share(p.nk, rank, P.split_log), kb1 = share(p.nk, rank + 1, P.split_log);
                 const int a_mn = p.a_mn, b_mn = p.b_mn;
                 const uint32_t fmt = (PL == 3 || std::is_same<T, __nv_bfloat16>::value) ? 1u : 0u;
                 const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)a_mn << 15) |
@@ -587,12 +398,12 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                 const uint32_t cor = tmem + ACC_COLS + (uint32_t)tile.slot * BN;
                 int in_chunk = 0;
                 for (int kb = kb0; kb < kb1; ++kb, g.next(NS)) {
-                    if (!(ok = mbar_wait(&full[g.slot], g.lap & 1, abort_flag))) break;
+                    if (!(ok = wait_phase(&full[g.slot], g.lap & 1, abort_flag))) break;
                     const uint32_t d = tmem + (uint32_t)chunk.slot * BN;
                     const uint64_t ah = a0 + (uint32_t)(g.slot * (STAGE / 16)), bh = b0 + (uint32_t)(g.slot * (STAGE / 16));
                     if (PL == 3) {
                         if (kb == kb0 && tile.lap > 0 &&
-                            !(ok = mbar_wait(&cor_empty[tile.slot], (tile.lap - 1) & 1, abort_flag)))
+                            !(ok = wait_phase(&cor_empty[tile.slot], (tile.lap - 1) & 1, abort_flag)))
                             break;
                         tc_fence_after();
 #pragma unroll
@@ -607,7 +418,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                         }
                     }
                     if (in_chunk == 0 && chunk.lap > 0 &&
-                        !(ok = mbar_wait(&acc_empty[chunk.slot], (chunk.lap - 1) & 1, abort_flag)))
+                        !(ok = wait_phase(&acc_empty[chunk.slot], (chunk.lap - 1) & 1, abort_flag)))
                         break;
                     tc_fence_after();
 #pragma unroll
@@ -636,8 +447,8 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
         }
     } else {
         // ------------------------------------------------------------------------------------- epilogue
-        const int e = warp - 2, q = warp & 3, half = e >> 2;
-        const uint32_t lane_base = ((uint32_t)(q * 32) << 16) + half * HALF;
+        const int e = warp - 2, q = warp & 3, part_no = e >> 2;
+        const uint32_t lane_base = ((uint32_t)(q * 32) << 16) + part_no * PART;
         if (P.db != nullptr)
             for (long long n = (long long)blockIdx.x * EPI_THREADS + threadIdx.x - 64; n < P.N;
                  n += (long long)gridDim.x * EPI_THREADS) {
@@ -646,8 +457,8 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                 for (int k = 0; k < P.nparts; ++k) s += P.part[(long long)k * P.N + n];
                 ((T*)P.db)[n] = from_f32<T>(s);
             }
-        constexpr int ROUND = epi_round<T, BN>();
-        T* buf = reinterpret_cast<T*>(base + (size_t)NS * STAGE + (EPI_TMA ? e * 8192 : 0));  // 4 x 32 x ROUND
+        constexpr int ROUND = epi_round<T, BN>(), RL = ROUND < 16 ? 8 : 16;
+        T* buf = reinterpret_cast<T*>(base + (size_t)NS * STAGE + (EPI_TMA ? e * (65536 / EW) : 0));  // 4 x 32 x ROUND
         Ring chunk, tile;     // as the MMA issuer counts them
         Ring rin;             // residual rounds consumed
         int pending = 0;      // residual rounds loaded and not yet consumed
@@ -656,10 +467,10 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
         int w, u;
         while (walk.next(w, u)) {
             const TcProduct& p = P.p[w];
-            const int i0 = u % p.tiles_i * (BM * CG) + pr * BM + q * 32, j0 = u / p.tiles_i * BN + half * HALF;
+            const int i0 = u % p.tiles_i * (BM * CG) + pr * BM + q * 32, j0 = u / p.tiles_i * BN + part_no * PART;
             const long long i = (long long)i0 + lane;
             const bool by_tma = EPI_TMA && S == 1 && p.vec;
-            const int rounds = by_tma && i0 < p.I && j0 < p.J ? (int)min((long long)HALF / ROUND, (p.J - j0 + ROUND - 1) / ROUND) : 0;
+            const int rounds = by_tma && i0 < p.I && j0 < p.J ? (int)min((long long)PART / ROUND, (p.J - j0 + ROUND - 1) / ROUND) : 0;
             // the residual comes in while the products run
             if (by_tma && p.res != nullptr) {
                 for (int k = 0; k < 2 && k < rounds; ++k, ++pending)
@@ -672,23 +483,23 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
             const float bias = (p.bias != nullptr && i < p.I) ? to_f32(((const T*)p.bias)[i]) : 0.f;
             float r[LD];
             if (S == 1 && !by_tma) res_lane<T>(p, i, j0, r);
-            const int kb0 = (int)((long long)p.nk * rank / S), kb1 = (int)((long long)p.nk * (rank + 1) / S);
+            const int kb0 = share(p.nk, rank, P.split_log), kb1 = share(p.nk, rank + 1, P.split_log);
             uint32_t acc_t = 0;  // TMEM columns that hold this warp's part of the finished tile
             bool alive = true;
             if (PL == 3) {
-                float acc[HALF];
+                float acc[PART];
 #pragma unroll
-                for (int c = 0; c < HALF; ++c) acc[c] = 0.f;
+                for (int c = 0; c < PART; ++c) acc[c] = 0.f;
                 const int nc = (kb1 - kb0 + CHUNK - 1) / CHUNK;
                 for (int ch = 0; ch < nc; ++ch) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[chunk.slot], chunk.lap & 1, abort_flag))) {
+                    if (!__all_sync(0xffffffffu, wait_phase(&acc_full[chunk.slot], chunk.lap & 1, abort_flag))) {
                         alive = false;
                         break;
                     }
                     tc_fence_after();
                     acc_t = tmem + lane_base + chunk.slot * BN;
 #pragma unroll
-                    for (int c = 0; c < HALF; c += LD) {
+                    for (int c = 0; c < PART; c += LD) {
                         uint32_t v[LD];
                         tmem_ld<LD>(acc_t + c, v);
                         tmem_wait_ld();
@@ -705,7 +516,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                 if (!alive) break;
                 const uint32_t cor_t = tmem + lane_base + ACC_COLS + tile.slot * BN;
 #pragma unroll
-                for (int c = 0; c < HALF; c += LD) {  // the finished sums go back to TMEM for the rolled loops below
+                for (int c = 0; c < PART; c += LD) {  // the finished sums go back to TMEM for the rolled loops below
                     uint32_t v[LD];
                     tmem_ld<LD>(cor_t + c, v);
                     tmem_wait_ld();
@@ -719,33 +530,33 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                 __syncwarp();
                 if (lane == 0) arrive_leader<CG>(&cor_empty[tile.slot]);
             } else {
-                if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[chunk.slot], chunk.lap & 1, abort_flag))) break;
+                if (!__all_sync(0xffffffffu, wait_phase(&acc_full[chunk.slot], chunk.lap & 1, abort_flag))) break;
                 tc_fence_after();
                 acc_t = tmem + lane_base + chunk.slot * BN;
             }
             if (S > 1) {
                 // every stage of this tile has been consumed: its shared memory takes the partial tile
                 float* part = reinterpret_cast<float*>(base);
-                for (int c = 0; c < HALF; c += 8) {
+                for (int c = 0; c < PART; c += 8) {
                     uint32_t v[8];
                     tmem_ld<8>(acc_t + c, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) part[(half * HALF + c + k) * BM + q * 32 + lane] = __uint_as_float(v[k]);
+                    for (int k = 0; k < 8; ++k) part[(part_no * PART + c + k) * BM + q * 32 + lane] = __uint_as_float(v[k]);
                 }
             } else if (by_tma) {
 #pragma unroll 1
                 for (int k = 0; k < rounds; ++k) {
                     uint32_t v[ROUND];
 #pragma unroll
-                    for (int c = 0; c < ROUND; c += 16)
-                        tmem_ld<16>(acc_t + k * ROUND + c, reinterpret_cast<uint32_t(&)[16]>(v[c]));
+                    for (int c = 0; c < ROUND; c += RL)
+                        tmem_ld<RL>(acc_t + k * ROUND + c, reinterpret_cast<uint32_t(&)[RL]>(v[c]));
                     tmem_wait_ld();
                     float o[ROUND];
 #pragma unroll
                     for (int c = 0; c < ROUND; ++c) o[c] = __uint_as_float(v[c]) + bias;
                     if (p.res != nullptr) {
-                        alive = __all_sync(0xffffffffu, mbar_wait(&res_full[e][rin.slot], rin.lap & 1, abort_flag));
+                        alive = __all_sync(0xffffffffu, wait_phase(&res_full[e][rin.slot], rin.lap & 1, abort_flag));
                         if (!alive) break;
                         const T* rb = buf + rin.slot * 32 * ROUND + lane;
 #pragma unroll
@@ -775,10 +586,10 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
             } else {
                 float rn[LD];
 #pragma unroll 1
-                for (int c = 0; c < HALF; c += LD) {
+                for (int c = 0; c < PART; c += LD) {
                     uint32_t v[LD];
                     tmem_ld<LD>(acc_t + c, v);
-                    if (c + LD < HALF) res_lane<T>(p, i, (long long)j0 + c + LD, rn);
+                    if (c + LD < PART) res_lane<T>(p, i, (long long)j0 + c + LD, rn);
                     tmem_wait_ld();
                     float o[LD];
 #pragma unroll
@@ -806,71 +617,11 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
     }
 
     if (S > 1) {
-        // one tile per cluster: join the partial tiles, each CTA its share of the columns
         Walk walk(P, worker);
         int w, u;
         walk.next(w, u);
         const TcProduct& p = P.p[w];
-        const int i0 = u % p.tiles_i * BM, j0 = u / p.tiles_i * BN;
-        const uint32_t part = smem_u32(base);
-        const int c0 = BN * rank / S, c1 = BN * (rank + 1) / S;
-        float bias[8];
-        {
-            const long long i = (long long)i0 + ((threadIdx.x - 64) & 15) * 8;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                bias[k] = (p.vec && p.bias != nullptr && i + k < p.I) ? to_f32(((const T*)p.bias)[i + k]) : 0.f;
-        }
-        __syncwarp();
-        cluster_sync_all();
-        if (warp >= 2) {
-            // all ranks' loads of a thread's share are issued before the first is used
-            if (p.vec) {  // eight lanes of a column per thread
-                const int e = threadIdx.x - 64;
-                const long long i = (long long)i0 + (e & 15) * 8;
-                for (int c = c0 + (e >> 4); c < c1; c += EPI_THREADS / 16) {
-                    const long long j = (long long)j0 + c;
-                    if (i >= p.I || j >= p.J) continue;
-                    Pack8<T> r;
-                    res8<T>(p, i, j, r);
-                    float4 x[8][2];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (k < S) {
-                            x[k][0] = ld_cluster4(part + (c * BM + (e & 15) * 8) * 4, k);
-                            x[k][1] = ld_cluster4(part + (c * BM + (e & 15) * 8 + 4) * 4, k);
-                        }
-                    float o[8] = {};
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (k < S) {
-                            o[0] += x[k][0].x, o[1] += x[k][0].y, o[2] += x[k][0].z, o[3] += x[k][0].w;
-                            o[4] += x[k][1].x, o[5] += x[k][1].y, o[6] += x[k][1].z, o[7] += x[k][1].w;
-                        }
-                    finish8<T>(p, i, j, o, bias, r);
-                }
-            } else {  // four lanes, 32 apart, of a column per thread
-                for (int c = c0 + warp - 2; c < c1; c += EPI_THREADS / 32) {
-                    const long long j = (long long)j0 + c;
-                    if (j >= p.J) continue;
-#pragma unroll 1
-                    for (int k = 0; k < 4; ++k) {
-                        const long long i = (long long)i0 + k * 32 + lane;
-                        float x[8], o[1] = {0.f};
-#pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            if (r < S) x[r] = ld_cluster(part + (c * BM + k * 32 + lane) * 4, r);
-#pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            if (r < S) o[0] += x[r];
-                        const float bl = (p.bias != nullptr && i < p.I) ? to_f32(((const T*)p.bias)[i]) : 0.f;
-                        float res[1];
-                        res_lane<T>(p, i, j, res);
-                        finish_lane<T>(p, i, j, o, bl, res);
-                    }
-                }
-            }
-        }
+        join_cluster<T, BN, 8>(p, u % p.tiles_i * BM, u / p.tiles_i * BN, smem_u32(base), rank, P.split_log, warp - 2);
     }
     tc_fence_before();
     if (CG > 1 || S > 1) {
@@ -891,51 +642,20 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
 
 // ----------------------------------------------------------------------------------- operands in tensor-core form
 
-// x = h + m + l: three bf16 by truncation, 8 significand bits each. A value that is not finite has m = l = 0.
-__device__ __forceinline__ void split3(float x, uint16_t& h, uint16_t& m, uint16_t& l) {
-    const uint32_t hb = __float_as_uint(x) & 0xffff0000u;
-    h = (uint16_t)(hb >> 16);
-    if (isfinite(x)) {
-        const float r = x - __uint_as_float(hb);
-        const uint32_t mb = __float_as_uint(r) & 0xffff0000u;
-        m = (uint16_t)(mb >> 16);
-        l = (uint16_t)(__float_as_uint(r - __uint_as_float(mb)) >> 16);
-    } else {
-        if (isnan(x)) h = 0x7fff;  // the payload may sit in the bits cut off
-        m = l = 0;
-    }
-}
-
 // Eight values of a row to the planes of the operand at dst (planes `plane` elements apart; PL = 1: the type itself).
 template <typename T>
 __device__ __forceinline__ void store_operand(uint16_t* dst, long long plane, const float (&v)[8]) {
     if (sizeof(T) == 4) {
-        union {
-            uint16_t s[8];
-            uint4 q;
-        } h, m, l;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) split3(v[u], h.s[u], m.s[u], l.s[u]);
-        *reinterpret_cast<uint4*>(dst) = h.q;
-        *reinterpret_cast<uint4*>(dst + plane) = m.q;
-        *reinterpret_cast<uint4*>(dst + 2 * plane) = l.q;
+        uint4 h, m, l;
+        split3x8(v, h, m, l);
+        *reinterpret_cast<uint4*>(dst) = h;
+        *reinterpret_cast<uint4*>(dst + plane) = m;
+        *reinterpret_cast<uint4*>(dst + 2 * plane) = l;
     } else {
         Pack8<T> w;
 #pragma unroll
         for (int u = 0; u < 8; ++u) w.v[u] = from_f32<T>(v[u]);
         *reinterpret_cast<Pack8<T>*>(dst) = w;
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]) {
-    if (vec && n >= 8) {
-        const Pack8<T> w = *reinterpret_cast<const Pack8<T>*>(p);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = to_f32(w.v[u]);
-    } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = u < n ? to_f32(p[u]) : 0.f;
     }
 }
 
@@ -1193,13 +913,6 @@ struct Side {
     bool mn;
 };
 
-int sm_count_() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return n;
-}
-
 // Clusters of cfg's size that run at once on the current device (asked once per kernel, size and device).
 cudaError_t cluster_limit(const void* kern, const cudaLaunchConfig_t* cfg, int* fit) {
     static std::mutex mu;
@@ -1252,7 +965,7 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
     const int need = stage_bytes<PL, BN>();
     P.stages = std::min(MAX_STAGES, (smem_limit<BN>() - 1024 - 1024 - epi_bytes<BN>()) / need);
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(NUM_THREADS);
+    cfg.blockDim = dim3(threads_of<BN>());
     cfg.dynamicSmemBytes = 1024 + (size_t)P.stages * need + epi_bytes<BN>();
     cfg.stream = s;
     cudaLaunchAttribute at[2];
@@ -1264,6 +977,7 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
     // Few tiles: split the reduction over a cluster, each CTA keeping at least two blocks of it, as long as all clusters
     // run at once (a cluster's CTAs share a GPC, so fewer may fit than the SMs suggest).
     P.split = 1;
+    P.split_log = 0;
     const int slots = sms * ctas_per_sm<BN>();
     while (CG == 1 && count > 0 && P.split < 8 && tiles * P.split * 2 <= slots && min_nk >= P.split * 4) {
         at[0].val.clusterDim.x = P.split * 2;
@@ -1273,9 +987,10 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
         if ((e = cluster_limit((const void*)kern, &cfg, &fit)) != cudaSuccess) return e;
         if (fit < tiles) break;
         P.split *= 2;
+        ++P.split_log;
     }
     P.workers = (int)std::min<long long>(tiles, P.split > 1 ? tiles : slots / CG);
-    if (tiles == 0) P.workers = std::min((P.N + EPI_THREADS - 1) / EPI_THREADS, sms);
+    if (tiles == 0) P.workers = std::min((P.N + 255) / 256, sms);
     P.gap = P.split > 1 || count < 2 ? 1 : std::max(1, (P.p[0].nk + P.p[1].nk / 2) / P.p[1].nk);
     cfg.gridDim = dim3((unsigned)(P.workers * CG * P.split));
     at[0].val.clusterDim.x = CG * P.split;
@@ -1285,8 +1000,9 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
 
 template <typename T, int PL>
 cudaError_t launch_pl(TcParams& P, const Side (&A)[2], const Side (&B)[2], int count, cudaStream_t s) {
-    const int sms = sm_count_();
-    if (sms == 0) return cudaErrorInvalidDevice;
+    int sms = 0;
+    const cudaError_t e = device_sms(&sms);
+    if (e != cudaSuccess) return e;
     long long J = 1;
     bool mn = false;
     for (int k = 0; k < count; ++k) {
@@ -1332,6 +1048,10 @@ long long row_blocks(long long M, int N) {
 }  // namespace
 
 bool linear_tc_supported(long long M, int N, int K) { return M > 0 && N > 0 && K > 0; }
+
+bool linear_tc_in_place(const LinearFwd& f) {
+    return f.dtype != VF_F32 && aligned16(f.x, f.ldx, 2) && aligned16(f.W, f.ldw, 2);
+}
 
 size_t linear_tc_workspace(int dtype, long long M, int N, int K, bool grad) {
     size_t n = operand_bytes(dtype, M, K) + operand_bytes(dtype, N, K);
@@ -1445,12 +1165,21 @@ cudaError_t launch_linear_grad_tc(const LinearGrad& f, void* work, size_t have, 
     return launch_products(f.dtype, P, A, B, count, s);
 }
 
-// Reads and clears the flag of expired waits (the device is idle when this is called).
+cudaError_t device_sms(int* sms) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
+// Reads and clears the flags of expired waits (the device is idle when this is called).
 cudaError_t ops_take_timeout(int* flag) {
-    cudaError_t e = cudaMemcpyFromSymbol(flag, g_ops_timeout, sizeof(int));
-    if (e != cudaSuccess || *flag == 0) return e;
+    int direct = 0;
+    cudaError_t e = direct_take_timeout(&direct);
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(flag, g_ops_timeout, sizeof(int));
     const int zero = 0;
-    return cudaMemcpyToSymbol(g_ops_timeout, &zero, sizeof(int));
+    if (e == cudaSuccess && *flag != 0) e = cudaMemcpyToSymbol(g_ops_timeout, &zero, sizeof(int));
+    *flag |= direct;
+    return e;
 }
 
 }  // namespace vf

@@ -132,7 +132,9 @@ int vf_linear_workspace(int dtype, long long M, int N, int K, int grad, size_t* 
     if (bytes == nullptr) return ops_fail(VF_ERR_ARG, "NULL pointer");
     OPS_TRY(check_kind(dtype, VF_ACT_NONE));
     OPS_TRY(check_sizes(M, N, K));
-    *bytes = use_tc(M, N, K) ? linear_tc_workspace(dtype, M, N, K, grad != 0) : 0;
+    *bytes = use_tc(M, N, K) && (grad != 0 || !linear_direct_fits(dtype, M, N, K))
+                 ? linear_tc_workspace(dtype, M, N, K, grad != 0)
+                 : 0;
     return VF_OK;
 }
 
@@ -150,6 +152,8 @@ int vf_linear(int dtype, int act, const void* x, long long ldx, const void* W, l
     if (z != nullptr) OPS_TRY(check_matrix("z", z, M, N, ldz, dtype));
     const LinearFwd p{dtype, act, x, ldx, W, ldw, b, r, ldr, M, N, K, y, ldy, z, ldz};
     if (!use_tc(M, N, K)) return launched(launch_linear_ffma(p, (cudaStream_t)stream));
+    if (!linear_tc_in_place(p) && linear_direct_fits(dtype, M, N, K))
+        return launched(launch_linear_direct(p, (cudaStream_t)stream));
     OPS_TRY(check_aligned(work));
     size_t need = 0;
     const size_t have = work == nullptr ? 0 : work_bytes;

@@ -171,10 +171,19 @@ cudaError_t launch_linear_grad_ffma(const LinearGrad& p, cudaStream_t s);
 // Tensor-core kernels (k_linear_tc.cu). linear_tc_workspace: the most any strides and alignment take. The launches write
 // to *need what this call takes of `work` (256-byte aligned) and launch nothing if that is more than `have`.
 bool linear_tc_supported(long long M, int N, int K);
+// Whether TMA can read x and W in place.
+bool linear_tc_in_place(const LinearFwd& p);
 size_t linear_tc_workspace(int dtype, long long M, int N, int K, bool grad);
 cudaError_t launch_linear_tc(const LinearFwd& p, void* work, size_t have, size_t* need, cudaStream_t s);
 cudaError_t launch_linear_grad_tc(const LinearGrad& p, void* work, size_t have, size_t* need, cudaStream_t s);
 cudaError_t ops_take_timeout(int* flag);
+cudaError_t device_sms(int* sms);  // SMs of the current device
+
+// Forward product that lays its operands out itself (k_linear_direct.cu): any strides and alignment, no workspace, for the
+// sizes that `fits` accepts.
+bool linear_direct_fits(int dtype, long long M, int N, int K);
+cudaError_t launch_linear_direct(const LinearFwd& p, cudaStream_t s);
+cudaError_t direct_take_timeout(int* flag);
 
 // Gradient norm and clipping (k_clip.cu); ranges as in vf_clip_grad_norm. `work` holds clip_work_doubles(n, SMs) doubles.
 struct ClipList {
