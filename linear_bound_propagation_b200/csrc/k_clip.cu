@@ -61,6 +61,17 @@ __device__ __forceinline__ double squares(const T* v, int n) {
     return (double)s;
 }
 
+// Accesses that should not push out of L2 what is still to be read from it.
+template <typename V>
+__device__ __forceinline__ V load_once(const V* p) {
+    const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p));
+    return *reinterpret_cast<const V*>(&q);
+}
+template <typename V>
+__device__ __forceinline__ void store_out(V* p, const V& v) {
+    __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&v));
+}
+
 // One chunk of a tensor: elements [e0, e1). `head` elements come before the first 16-byte boundary.
 template <typename T>
 __device__ __forceinline__ double chunk_squares(const T* __restrict__ p, long long e0, long long e1) {
@@ -134,12 +145,12 @@ __device__ __forceinline__ void chunk_scale(const T* p, T* out, long long e0, lo
     if (nv == 4 * THREADS) {
         Vec<T, N> v[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = b[threadIdx.x + u * THREADS];
+        for (int u = 0; u < 4; ++u) v[u] = load_once(b + threadIdx.x + u * THREADS);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
 #pragma unroll
             for (int i = 0; i < N; ++i) v[u].v[i] = from_f32<T>(to_f32(v[u].v[i]) * f);
-            ob[threadIdx.x + u * THREADS] = v[u];
+            store_out(ob + threadIdx.x + u * THREADS, v[u]);
         }
     } else {
         for (int i = threadIdx.x; i < nv; i += THREADS) {
@@ -163,9 +174,10 @@ clip_scale_k(const __grid_constant__ Table tab, const double* part, int nparts, 
     if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
     const bool clip = n > (double)max_norm && !isinf(n);  // NaN compares false
     const float f = (float)(clip ? (double)scale * ((double)max_norm / n) : (double)scale);
-    int t = 0;
-    for (int c = blockIdx.x; c < tab.first[tab.n]; c += gridDim.x) {
-        while (c >= tab.first[t + 1]) ++t;
+    // backwards: what the norm's pass read last is still in L2
+    int t = tab.n - 1;
+    for (int c = tab.first[tab.n] - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
+        while (c < tab.first[t]) --t;
         if (tab.in[t] == tab.out[t] && f == 1.f) continue;
         const long long e = chunk_elems(tab.dtype[t]);
         const long long e0 = (c - tab.first[t]) * e, e1 = min(tab.size[t], e0 + e);

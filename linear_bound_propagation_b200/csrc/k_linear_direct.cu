@@ -45,6 +45,15 @@ struct DirectParams {
 // What a thread holds of a block of one operand: N times eight elements. A staged operand is made of 128-byte lines of
 // BK elements, one per row. VEC (rows of 16-byte alignment): eight elements that lie together, a line by eight neighbouring
 // threads, groups of 64 lines. Else single elements, a line by the lanes of a warp, half by half, groups of 16 lines.
+template <typename T, int N, bool VEC>
+struct Held {
+    Pack8<T> v[N];
+};
+template <typename T, int N>
+struct Held<T, N, false> {
+    T e[8 * N];  // a register each: nothing waits for a load before the block is laid out
+};
+
 template <typename T, int N, int LINES, bool VEC>
 struct Loader {
     static constexpr int STEP = VEC ? 64 : 16;
@@ -52,7 +61,7 @@ struct Loader {
     long long line_step;  // elements between its lines
     int left;             // rows from its first line to the operand's last
     int t;                // step of its first element in a block
-    Pack8<T> h[2][N];
+    Held<T, N, VEC> h[2];
     __device__ __forceinline__ Loader(const Source& s, int r0, int kb0) {
         const int line = VEC ? threadIdx.x >> 3 : threadIdx.x >> 5;
         t = VEC ? (threadIdx.x & 7) * 8 : threadIdx.x & 31;
@@ -67,16 +76,11 @@ struct Loader {
         for (int g = 0; g < (VEC ? N : 4 * N); ++g, q += line_step) {
             if (LINES < STEP * (g + 1) && (int)(VEC ? threadIdx.x >> 3 : threadIdx.x >> 5) + STEP * g >= LINES) break;
             const int n = left > STEP * g ? steps - t : 0;
-            if (VEC) {
-                if (n >= 8) {
-                    h[b][g] = *reinterpret_cast<const Pack8<T>*>(q);
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) h[b][g].v[u] = u < n ? q[u] : from_f32<T>(0.f);
-                }
+            if constexpr (VEC) {
+                load_raw8(q, n, true, h[b].v[g]);
             } else {
-                h[b][g >> 2].v[(g & 3) * 2] = n > 0 ? q[0] : from_f32<T>(0.f);
-                h[b][g >> 2].v[(g & 3) * 2 + 1] = n > 32 ? q[32] : from_f32<T>(0.f);
+                h[b].e[2 * g] = n > 0 ? q[0] : from_f32<T>(0.f);
+                h[b].e[2 * g + 1] = n > 32 ? q[32] : from_f32<T>(0.f);
             }
         }
         p += BK;
@@ -87,8 +91,8 @@ struct Loader {
 __device__ __forceinline__ int swizzled(int line, int c) { return line * 128 + ((c ^ (line & 7)) << 4); }
 
 template <typename T, int PL, int N, int LINES, bool VEC>
-__device__ __forceinline__ void store_block(uint8_t* dst, int plane, const Pack8<T> (&h)[N]) {
-    if (VEC) {
+__device__ __forceinline__ void store_block(uint8_t* dst, int plane, const Held<T, N, VEC>& h) {
+    if constexpr (VEC) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const int line = (int)(threadIdx.x >> 3) + 64 * k;
@@ -96,15 +100,14 @@ __device__ __forceinline__ void store_block(uint8_t* dst, int plane, const Pack8
             uint8_t* o = dst + swizzled(line, threadIdx.x & 7);
             if (PL == 3) {
                 float v[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) v[u] = to_f32(h[k].v[u]);
+                unpack8(h.v[k], v);
                 uint4 hi, mid, lo;
                 split3x8(v, hi, mid, lo);
                 *reinterpret_cast<uint4*>(o) = hi;
                 *reinterpret_cast<uint4*>(o + plane) = mid;
                 *reinterpret_cast<uint4*>(o + 2 * plane) = lo;
             } else {
-                *reinterpret_cast<Pack8<T>*>(o) = h[k];
+                *reinterpret_cast<Pack8<T>*>(o) = h.v[k];
             }
         }
     } else {
@@ -114,14 +117,14 @@ __device__ __forceinline__ void store_block(uint8_t* dst, int plane, const Pack8
             if (LINES < 16 * ((x >> 1) + 1) && line >= LINES) break;
             uint8_t* o = dst + swizzled(line, e >> 3) + (e & 7) * 2;
             if (PL == 3) {
-                const float v = to_f32(h[x >> 3].v[x & 7]);
+                const float v = to_f32(h.e[x]);
                 float r, l;
                 split3(v, r, l);
                 *reinterpret_cast<uint16_t*>(o) = (uint16_t)(__float_as_uint(v) >> 16);
                 *reinterpret_cast<uint16_t*>(o + plane) = (uint16_t)(__float_as_uint(r) >> 16);
                 *reinterpret_cast<uint16_t*>(o + 2 * plane) = (uint16_t)(__float_as_uint(l) >> 16);
             } else {
-                *reinterpret_cast<T*>(o) = h[x >> 3].v[x & 7];
+                *reinterpret_cast<T*>(o) = h.e[x];
             }
         }
     }
@@ -175,8 +178,11 @@ __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (S > 1) cluster_arrive();
     const uint32_t tmem = tmem_base_sh;
     volatile int* abort_flag = &abort_sh;
+    const uint32_t inbox = smem_u32(base) + NS * STAGE;
+    bool pushed = false;  // this warp has met the cluster's first barrier
 
     if (warp == WORKERS / 32) {
         if (elect_one()) {
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_const
             const uint64_t b0 = operand_desc<BK>(smem_u32(base) + PL * A_PLANE, 0);
             Ring g;
             for (int kb = kb0; kb < kb1; ++kb, g.next(NS)) {
-                if (!mbar_wait(&full[g.slot], g.lap & 1, abort_flag)) break;
+                if (!wait_phase(&full[g.slot], g.lap & 1, abort_flag)) break;
                 tc_fence_after();
                 const uint64_t ah = a0 + (uint32_t)(g.slot * (STAGE / 16)), bh = b0 + (uint32_t)(g.slot * (STAGE / 16));
 #pragma unroll
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_const
                 a.load(h ^ 1, P.Tn - (kb + 1) * BK);
                 b.load(h ^ 1, P.Tn - (kb + 1) * BK);
             }
-            if (g.lap > 0) ok = mbar_wait(&empty[g.slot], (g.lap - 1) & 1, abort_flag);
+            if (g.lap > 0) ok = wait_phase(&empty[g.slot], (g.lap - 1) & 1, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             uint8_t* st = base + (size_t)g.slot * STAGE;
@@ -248,10 +254,11 @@ __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_const
         const float bias = (S == 1 && p.bias != nullptr && i < p.I) ? to_f32(((const T*)p.bias)[i]) : 0.f;
         float r[LD], rn[LD];
         if (S == 1 && warp < FW) res_lane<T>(p, i, jw, r);
-        ok = mbar_wait(&acc_full, 0, abort_flag);
+        ok = wait_phase(&acc_full, 0, abort_flag);
         if (__all_sync(0xffffffffu, ok) && warp < FW) {
             tc_fence_after();
-            float* part = reinterpret_cast<float*>(base);
+            if (S > 1) cluster_wait();  // all of the cluster's CTAs have begun
+            pushed = true;
 #pragma unroll 1
             for (int c = 0; c < PART; c += LD) {
                 uint32_t v[LD], x[LD];
@@ -267,7 +274,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_const
                                      : __uint_as_float(v[k]);
                 if (S > 1) {
 #pragma unroll
-                    for (int k = 0; k < LD; ++k) part[(part_no * PART + c + k) * BM + q * 32 + lane] = o[k];
+                    for (int k = 0; k < LD; ++k)
+                        push_column<BN>(inbox, part_no * PART + c + k, q * 32 + lane, rank, P.split_log, o[k]);
                 } else {
                     if ((long long)jw + c < p.J) finish_lane<T>(p, i, (long long)jw + c, o, bias, r);
 #pragma unroll
@@ -278,14 +286,13 @@ __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_const
         }
     }
     __syncwarp();
-    if (S > 1) join_cluster<T, BN, WORKERS / 32>(p, i0, j0, smem_u32(base), rank, P.split_log, warp);
-    tc_fence_before();
     if (S > 1) {
-        __syncwarp();
-        cluster_sync_all();  // no CTA leaves while another reads its partial tile
-    } else {
-        __syncthreads();
+        if (!pushed) cluster_wait();
+        join_cluster<T, BN, WORKERS / 32>(p, i0, j0, reinterpret_cast<const float*>(base + NS * STAGE), rank, P.split_log,
+                                          warp);
     }
+    tc_fence_before();
+    __syncthreads();
     if (warp == WORKERS / 32) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
@@ -330,12 +337,12 @@ cudaError_t launch_bn(DirectParams& P, int sms, cudaStream_t s) {
     cudaError_t e = allow_dyn_smem((const void*)kern, SMEM_LIMIT);
     if (e != cudaSuccess) return e;
     const int need = direct_stage<PL, BN>();
-    P.stages = std::min(4, (SMEM_LIMIT - 1024) / need);
+    P.stages = std::min(4, (SMEM_LIMIT - 1024 - BN * 512) / need);
     P.split_log = split_log(p.tiles, p.nk, PL == 3, sms);
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(THREADS);
     cfg.gridDim = dim3((unsigned)(p.tiles << P.split_log));
-    cfg.dynamicSmemBytes = 1024 + (size_t)P.stages * need;
+    cfg.dynamicSmemBytes = 1024 + (size_t)P.stages * need + BN * 512;  // and the inbox
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;

@@ -171,9 +171,10 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
 }
 // Epilogue through TMA (tiles of 64 columns and more whose rows allow it): a warp handles its 32 lanes in rounds of
 // ROUND columns, with two buffers for the residual on its way in and two for z and y on their way out, 64 KB in all.
+// Split reductions have their inbox in the same place, and narrow tiles this alone.
 template <int BN>
 constexpr int epi_bytes() {
-    return BN >= 64 ? 65536 : 0;
+    return BN >= 64 ? 65536 : BN * 512;
 }
 template <typename T, int BN>
 constexpr int epi_round() {
@@ -296,6 +297,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
         cluster_sync_all();  // the other CTA's barriers exist
     } else {
         __syncthreads();
+        if (S > 1) cluster_arrive();
     }
     grid_wait();  // what the launch before wrote may be read from here on
     uint32_t tmem = 0;
@@ -321,6 +323,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
         tmem = tmem_base_sh;
     }
     volatile int* abort_flag = &abort_sh;
+    bool pushed = false;  // this warp has met the cluster's first barrier
 
     if (warp == 0) {
         if (elect_one()) {
@@ -453,7 +456,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
             for (long long n = (long long)blockIdx.x * EPI_THREADS + threadIdx.x - 64; n < P.N;
                  n += (long long)gridDim.x * EPI_THREADS) {
                 float s = 0.f;
-#pragma unroll 8
+#pragma unroll 16
                 for (int k = 0; k < P.nparts; ++k) s += P.part[(long long)k * P.N + n];
                 ((T*)P.db)[n] = from_f32<T>(s);
             }
@@ -535,15 +538,18 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                 acc_t = tmem + lane_base + chunk.slot * BN;
             }
             if (S > 1) {
-                // every stage of this tile has been consumed: its shared memory takes the partial tile
-                float* part = reinterpret_cast<float*>(base);
+                cluster_wait();  // all of the cluster's CTAs have begun
+#pragma unroll 1
                 for (int c = 0; c < PART; c += 8) {
                     uint32_t v[8];
                     tmem_ld<8>(acc_t + c, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) part[(part_no * PART + c + k) * BM + q * 32 + lane] = __uint_as_float(v[k]);
+                    for (int k = 0; k < 8; ++k)
+                        push_column<BN>(smem_u32(base + (size_t)NS * STAGE), part_no * PART + c + k, q * 32 + lane, rank,
+                                        P.split_log, __uint_as_float(v[k]));
                 }
+                pushed = true;
             } else if (by_tma) {
 #pragma unroll 1
                 for (int k = 0; k < rounds; ++k) {
@@ -621,12 +627,15 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
         int w, u;
         walk.next(w, u);
         const TcProduct& p = P.p[w];
-        join_cluster<T, BN, 8>(p, u % p.tiles_i * BM, u / p.tiles_i * BN, smem_u32(base), rank, P.split_log, warp - 2);
+        __syncwarp();
+        if (!pushed) cluster_wait();
+        join_cluster<T, BN, 8>(p, u % p.tiles_i * BM, u / p.tiles_i * BN,
+                               reinterpret_cast<const float*>(base + (size_t)NS * STAGE), rank, P.split_log, warp - 2);
     }
     tc_fence_before();
-    if (CG > 1 || S > 1) {
+    if (CG > 1) {
         __syncwarp();
-        cluster_sync_all();  // no CTA leaves while another reads its shared memory or arrives on its barriers
+        cluster_sync_all();  // no CTA leaves while the other reads its shared memory or arrives on its barriers
     } else {
         __syncthreads();
     }
@@ -653,8 +662,7 @@ __device__ __forceinline__ void store_operand(uint16_t* dst, long long plane, co
         *reinterpret_cast<uint4*>(dst + 2 * plane) = l;
     } else {
         Pack8<T> w;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) w.v[u] = from_f32<T>(v[u]);
+        pack8(w, v);
         *reinterpret_cast<Pack8<T>*>(dst) = w;
     }
 }
@@ -681,8 +689,10 @@ __device__ void pack_block(const PackJob& j, long long blk) {
     for (int k = 0; k < j.steps; ++k) {
         const long long r = r0 + k * 8;
         if (r >= j.rows) break;
+        Pack8<T> x;
         float v[8];
-        load8((const T*)j.src + r * j.ld + c, j.cols - c, j.vec, v);
+        load_raw8((const T*)j.src + r * j.ld + c, j.cols - c, j.vec, x);
+        unpack8(x, v);
         store_operand<T>(j.dst + r * j.ldp + c, plane, v);
     }
 }
@@ -705,6 +715,56 @@ struct GradJob {
     int blocks_c, steps;
 };
 
+// U rows of dy and z on their way into registers while the U before are worked on.
+template <typename T, int ACT, int U>
+struct GradRows {
+    Pack8<T> d[U], z[U];
+    __device__ __forceinline__ void load(const GradJob& j, long long r0, int k0, int c) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const long long r = r0 + (k0 + k) * 8;
+            const int n = k0 + k < j.steps && r < j.M ? j.N - c : 0;
+            load_raw8((const T*)j.dy + r * j.lddy + c, n, j.vec, d[k]);
+            if (ACT != VF_ACT_NONE) load_raw8((const T*)j.z + r * j.ldz + c, n, j.vec, z[k]);
+        }
+    }
+    __device__ __forceinline__ void work(const GradJob& j, long long r0, int k0, int c, float (&s)[8]) {
+        const int n = j.N - c;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const long long r = r0 + (k0 + k) * 8;
+            if (k0 + k >= j.steps || r >= j.M) break;
+            float v[8], x[8];
+            unpack8(d[k], v);
+            if (ACT != VF_ACT_NONE) unpack8(z[k], x);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (ACT != VF_ACT_NONE) v[u] = act_grad<sizeof(T) == 2>(v[u], x[u], ACT);
+                s[u] += v[u];
+            }
+            if (j.dst != nullptr) store_operand<T>(j.dst + r * j.ldp + c, j.M * j.ldp, v);
+            if (j.dr != nullptr) {
+                Pack8<T> p;
+                pack8(p, v);
+                store_raw8((T*)j.dr + r * j.lddr + c, n, j.vec_r, p);
+            }
+        }
+    }
+};
+template <typename T, int ACT>
+__device__ __forceinline__ void grad_rows(const GradJob& j, long long r0, int c, float (&s)[8]) {
+    constexpr int U = sizeof(T) == 2 ? 2 : 1;
+    GradRows<T, ACT, U> a, b;
+    a.load(j, r0, 0, c);
+#pragma unroll 1
+    for (int k = 0; k < j.steps; k += 2 * U) {
+        b.load(j, r0, k + U, c);
+        a.work(j, r0, k, c, s);
+        a.load(j, r0, k + 2 * U, c);
+        b.work(j, r0, k + U, c, s);
+    }
+}
+
 template <typename T>
 __device__ void grad_block(const GradJob& j, long long blk) {
     __shared__ float sums[8][PACK_COLS];
@@ -713,46 +773,12 @@ __device__ void grad_block(const GradJob& j, long long blk) {
     const int c0 = (int)(blk % j.blocks_c) * PACK_COLS, cl = (threadIdx.x & 31) * 8, c = c0 + cl;
     float s[8] = {};
     if (c < j.N) {
-        const int n = j.N - c;
-#pragma unroll 2
-        for (int k = 0; k < j.steps; ++k) {
-            const long long r = rb * (8 * j.steps) + w + k * 8;
-            if (r >= j.M) break;
-            float v[8];
-            load8((const T*)j.dy + r * j.lddy + c, n, j.vec, v);
-            if (j.act != VF_ACT_NONE) {
-                float z[8];
-                load8((const T*)j.z + r * j.ldz + c, n, j.vec, z);
-                switch (j.act) {
-                    case VF_ACT_RELU:
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) v[u] = act_grad<sizeof(T) == 2>(v[u], z[u], VF_ACT_RELU);
-                        break;
-                    case VF_ACT_GELU:
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) v[u] = act_grad<sizeof(T) == 2>(v[u], z[u], VF_ACT_GELU);
-                        break;
-                    default:
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) v[u] = act_grad<sizeof(T) == 2>(v[u], z[u], VF_ACT_SILU);
-                }
-            }
-            if (j.dst != nullptr) store_operand<T>(j.dst + r * j.ldp + c, j.M * j.ldp, v);
-            if (j.dr != nullptr) {
-                T* o = (T*)j.dr + r * j.lddr + c;
-                Pack8<T> p;
-#pragma unroll
-                for (int u = 0; u < 8; ++u) p.v[u] = from_f32<T>(v[u]);
-                if (j.vec_r && n >= 8) {
-                    *reinterpret_cast<Pack8<T>*>(o) = p;
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        if (u < n) o[u] = p.v[u];
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) s[u] += v[u];
+        const long long r0 = rb * (8 * j.steps) + w;
+        switch (j.act) {
+            case VF_ACT_RELU: grad_rows<T, VF_ACT_RELU>(j, r0, c, s); break;
+            case VF_ACT_GELU: grad_rows<T, VF_ACT_GELU>(j, r0, c, s); break;
+            case VF_ACT_SILU: grad_rows<T, VF_ACT_SILU>(j, r0, c, s); break;
+            default: grad_rows<T, VF_ACT_NONE>(j, r0, c, s);
         }
     }
     if (j.part == nullptr) return;
@@ -769,7 +795,7 @@ __device__ void grad_block(const GradJob& j, long long blk) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(PACK_THREADS)
+__global__ void __launch_bounds__(PACK_THREADS, 3)
 linear_operands_k(const __grid_constant__ GradJob g, const __grid_constant__ PackJob a, const __grid_constant__ PackJob b) {
     grid_trigger();
     grid_wait();
@@ -844,11 +870,11 @@ bool aligned16(const void* p, long long ld, int e) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * e) % 16 == 0 && ld < (1LL << 37);
 }
 
-// Rows of a block are 8 * steps: 64, or fewer (down to 8) until the blocks fill the SMs. Depends on the sizes alone, so
-// that column sums are added in the same order on every device.
+// Rows of a block are 8 * steps: 256, or fewer (down to 8) until there are three blocks per SM. Depends on the sizes
+// alone, so that column sums are added in the same order on every device.
 int pack_steps(long long rows, int blocks_c) {
-    int steps = 8;
-    while (steps > 1 && (rows + 8 * steps - 1) / (8 * steps) * blocks_c < 592) steps /= 2;
+    int steps = 32;
+    while (steps > 1 && (rows + 8 * steps - 1) / (8 * steps) * blocks_c < 444) steps /= 2;
     return steps;
 }
 

@@ -132,6 +132,8 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -140,29 +142,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t saddr, uint32_t rank) {
+__device__ __forceinline__ void st_cluster(uint32_t saddr, uint32_t rank, float v) {
     uint32_t a;
-    float v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
-
-__device__ __forceinline__ float4 ld_cluster4(uint32_t saddr, uint32_t rank) {
-    uint32_t a;
-    float4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
-}
-
-template <typename T>
-struct alignas(16) Pack8 {
-    T v[8];
-};
 
 template <typename T, int N>
 __device__ __forceinline__ void activate(float (&v)[N], int act) {
@@ -188,49 +172,44 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
 // ahead (res8) so that several rows' loads are in flight.
 template <typename T>
 __device__ __forceinline__ void res8(const TcProduct& p, long long i, long long j, Pack8<T>& w) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u) w.v[u] = from_f32<T>(0.f);
-    if (p.res == nullptr || j >= p.J) return;
-    const T* r = (const T*)p.res + j * p.ldr + i;
-    if (i + 8 <= p.I) {
-        w = *reinterpret_cast<const Pack8<T>*>(r);
-    } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (i + u < p.I) w.v[u] = r[u];
-    }
-}
-template <typename T>
-__device__ __forceinline__ void put8(T* o, int n, const float (&v)[8]) {
-    Pack8<T> w;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) w.v[u] = from_f32<T>(v[u]);
-    if (n >= 8) {
-        *reinterpret_cast<Pack8<T>*>(o) = w;
-    } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (u < n) o[u] = w.v[u];
-    }
+    zero8(w);
+    if (p.res != nullptr && j < p.J) load_raw8((const T*)p.res + j * p.ldr + i, (int)min(8LL, p.I - i), true, w);
 }
 template <typename T>
 __device__ __forceinline__ void finish8(const TcProduct& p, long long i, long long j, float (&v)[8], const float (&bias)[8],
                                         const Pack8<T>& r) {
     const int n = (int)min(8LL, p.I - i);
+    float x[8];
+    unpack8(r, x);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] += bias[u] + to_f32(r.v[u]);
-    if (p.zout != nullptr) put8<T>((T*)p.zout + j * p.ldz + i, n, v);
+    for (int u = 0; u < 8; ++u) v[u] += bias[u] + x[u];
+    Pack8<T> w;
+    if (p.zout != nullptr) {
+        pack8(w, v);
+        store_raw8((T*)p.zout + j * p.ldz + i, n, true, w);
+    }
     activate<T>(v, p.act);
-    put8<T>((T*)p.out + j * p.ldo + i, n, v);
+    pack8(w, v);
+    store_raw8((T*)p.out + j * p.ldo + i, n, true, w);
 }
 
 // One element i of N rows j .. j + N - 1 per thread, a warp's lanes on consecutive elements: fp32 rows (a warp's access
 // is a whole 128-byte line) and rows that do not allow 16-byte accesses.
+// The residual's N rows of one element. Addresses are clamped into the tensor instead of guarded, so that all loads are
+// issued before one is used; what lies outside is never stored.
 template <typename T, int N>
 __device__ __forceinline__ void res_lane(const TcProduct& p, long long i, long long j, float (&r)[N]) {
+    if (p.res == nullptr) {
 #pragma unroll
-    for (int u = 0; u < N; ++u)
-        r[u] = (p.res != nullptr && i < p.I && j + u < p.J) ? to_f32(((const T*)p.res)[(j + u) * p.ldr + i]) : 0.f;
+        for (int u = 0; u < N; ++u) r[u] = 0.f;
+        return;
+    }
+    const T* q = (const T*)p.res + min(i, p.I - 1);
+    T v[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) v[u] = q[min(j + u, p.J - 1) * p.ldr];
+#pragma unroll
+    for (int u = 0; u < N; ++u) r[u] = to_f32(v[u]);
 }
 template <typename T, int N>
 __device__ __forceinline__ void finish_lane(const TcProduct& p, long long i, long long j, float (&v)[N], float bias,
@@ -271,25 +250,21 @@ __device__ __forceinline__ void split3x8(const float (&v)[8], uint4& h, uint4& m
     l = make_uint4(upper2(t[0], t[1]), upper2(t[2], t[3]), upper2(t[4], t[5]), upper2(t[6], t[7]));
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]) {
-    if (vec && n >= 8) {
-        const Pack8<T> w = *reinterpret_cast<const Pack8<T>*>(p);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = to_f32(w.v[u]);
-    } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = u < n ? to_f32(p[u]) : 0.f;
-    }
+// Split reductions. Each of the 2^log CTAs of a cluster finishes its share of the tile's BN columns; its shared memory at
+// `inbox` (BN x 512 bytes, used for nothing else) receives the others' partial sums of these columns, one slab of
+// share x 128 floats per sender. The cluster meets twice: every CTA has begun (arrive at the start, wait before the first
+// push), and every push has landed. Nothing is read from another CTA, so each leaves when it has finished.
+template <int BN>
+__device__ __forceinline__ void push_column(uint32_t inbox, int c, int lane128, int rank, int log, float v) {
+    constexpr int LOG_BN = BN == 16 ? 4 : BN == 32 ? 5 : BN == 64 ? 6 : BN == 128 ? 7 : 8;
+    const int w = BN >> log;  // columns of a share; BN is at least 16, the cluster at most 8
+    const int owner = c >> (LOG_BN - log), cl = c & (w - 1);
+    st_cluster(inbox + ((rank * w + cl) * BM + lane128) * 4, owner, v);
 }
-
-// Joins the 2^log partial tiles of a cluster (each CTA's in its shared memory at `part`: BN columns of 128 floats), each
-// CTA finishing its share of the columns. Called by every thread, converged; `ew` is the warp's place among the NW that
-// work (outside 0..NW-1: only the barrier). The caller joins the cluster once more before it leaves.
+// Called by every thread, converged, after its pushes; `ew` is the warp's place among the NW that work.
 template <typename T, int BN, int NW>
-__device__ __forceinline__ void join_cluster(const TcProduct& p, int i0, int j0, uint32_t part, int rank, int log, int ew) {
-    const int S = 1 << log, lane = threadIdx.x & 31, e = ew * 32 + lane;
-    const int c0 = share(BN, rank, log), c1 = share(BN, rank + 1, log);
+__device__ __forceinline__ void join_cluster(const TcProduct& p, int i0, int j0, const float* inbox, int rank, int log, int ew) {
+    const int S = 1 << log, lane = threadIdx.x & 31, e = ew * 32 + lane, w = BN >> log;
     const long long iv = (long long)i0 + (e & 15) * 8;
     float bias[8];
 #pragma unroll
@@ -298,47 +273,30 @@ __device__ __forceinline__ void join_cluster(const TcProduct& p, int i0, int j0,
     __syncwarp();
     cluster_sync_all();
     if (ew < 0 || ew >= NW) return;
-    // the loads of four ranks are issued before the first is used
     if (p.vec) {  // eight lanes of a column per thread
-        for (int c = c0 + (e >> 4); c < c1; c += 2 * NW) {
-            const long long j = (long long)j0 + c;
+        for (int c = e >> 4; c < w; c += 2 * NW) {
+            const long long j = (long long)j0 + rank * w + c;
             if (iv >= p.I || j >= p.J) continue;
             Pack8<T> r;
             res8<T>(p, iv, j, r);
             float o[8] = {};
-#pragma unroll
-            for (int k0 = 0; k0 < 8; k0 += 4) {
-                if (k0 >= S) break;
-                float4 x[4][2];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k0 + k < S) {
-                        x[k][0] = ld_cluster4(part + (c * BM + (e & 15) * 8) * 4, k0 + k);
-                        x[k][1] = ld_cluster4(part + (c * BM + (e & 15) * 8 + 4) * 4, k0 + k);
-                    }
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k0 + k < S) {
-                        o[0] += x[k][0].x, o[1] += x[k][0].y, o[2] += x[k][0].z, o[3] += x[k][0].w;
-                        o[4] += x[k][1].x, o[5] += x[k][1].y, o[6] += x[k][1].z, o[7] += x[k][1].w;
-                    }
+            for (int k = 0; k < S; ++k) {  // rank order
+                const float4* x = reinterpret_cast<const float4*>(inbox + (k * w + c) * BM + (e & 15) * 8);
+                const float4 a = x[0], b = x[1];
+                o[0] += a.x, o[1] += a.y, o[2] += a.z, o[3] += a.w;
+                o[4] += b.x, o[5] += b.y, o[6] += b.z, o[7] += b.w;
             }
             finish8<T>(p, iv, j, o, bias, r);
         }
     } else {  // four lanes, 32 apart, of a column per thread
-        for (int c = c0 + ew; c < c1; c += NW) {
-            const long long j = (long long)j0 + c;
+        for (int c = ew; c < w; c += NW) {
+            const long long j = (long long)j0 + rank * w + c;
             if (j >= p.J) continue;
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
                 const long long i = (long long)i0 + k * 32 + lane;
-                float x[8], o[1] = {0.f};
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < S) x[r] = ld_cluster(part + (c * BM + k * 32 + lane) * 4, r);
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < S) o[0] += x[r];
+                float o[1] = {0.f};
+                for (int r = 0; r < S; ++r) o[0] += inbox[(r * w + c) * BM + k * 32 + lane];
                 const float bl = (p.bias != nullptr && i < p.I) ? to_f32(((const T*)p.bias)[i]) : 0.f;
                 float res[1];
                 res_lane<T>(p, i, j, res);

@@ -29,6 +29,94 @@ __device__ __forceinline__ __half from_f32<__half>(float v) {
     return __float2half_rn(v);
 }
 
+// Eight values that lie together, as the words they are loaded and stored in (elements held one by one would take
+// a register each in the 16-bit types).
+template <typename T>
+struct alignas(16) Pack8 {
+    uint32_t w[2 * sizeof(T)];
+};
+__device__ __forceinline__ void unpack8(const Pack8<float>& p, float (&v)[8]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = __uint_as_float(p.w[u]);
+}
+__device__ __forceinline__ void unpack8(const Pack8<__nv_bfloat16>& p, float (&v)[8]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        v[2 * u] = __uint_as_float(p.w[u] << 16);
+        v[2 * u + 1] = __uint_as_float(p.w[u] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack8(const Pack8<__half>& p, float (&v)[8]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p.w[u]));
+        v[2 * u] = f.x;
+        v[2 * u + 1] = f.y;
+    }
+}
+__device__ __forceinline__ void pack8(Pack8<float>& p, const float (&v)[8]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) p.w[u] = __float_as_uint(v[u]);
+}
+__device__ __forceinline__ void pack8(Pack8<__nv_bfloat16>& p, const float (&v)[8]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * u], v[2 * u + 1]);
+        p.w[u] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+__device__ __forceinline__ void pack8(Pack8<__half>& p, const float (&v)[8]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const __half2 h = __floats2half2_rn(v[2 * u], v[2 * u + 1]);
+        p.w[u] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+// One element's bits; or_elem on a pack that holds zeros there.
+template <typename T>
+__device__ __forceinline__ void or_elem(Pack8<T>& p, int u, T x) {
+    if (sizeof(T) == 4)
+        p.w[u] = *reinterpret_cast<const uint32_t*>(&x);
+    else
+        p.w[u >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t*>(&x) << (16 * (u & 1));
+}
+template <typename T>
+__device__ __forceinline__ T get_elem(const Pack8<T>& p, int u) {
+    T x;
+    if (sizeof(T) == 4)
+        *reinterpret_cast<uint32_t*>(&x) = p.w[u];
+    else
+        *reinterpret_cast<uint16_t*>(&x) = (uint16_t)(p.w[u >> 1] >> (16 * (u & 1)));
+    return x;
+}
+template <typename T>
+__device__ __forceinline__ void zero8(Pack8<T>& p) {
+#pragma unroll
+    for (int u = 0; u < (int)(2 * sizeof(T)); ++u) p.w[u] = 0;
+}
+// The first n (8 at most) of eight values, zeros behind them. vec: p is 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load_raw8(const T* p, int n, bool vec, Pack8<T>& v) {
+    if (vec && n >= 8) {
+        v = *reinterpret_cast<const Pack8<T>*>(p);
+    } else {
+        zero8(v);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (u < n) or_elem(v, u, p[u]);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_raw8(T* p, int n, bool vec, const Pack8<T>& v) {
+    if (vec && n >= 8) {
+        *reinterpret_cast<Pack8<T>*>(p) = v;
+    } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (u < n) p[u] = get_elem(v, u);
+    }
+}
+
 // -------------------------------------------------------------------------------------------- activations
 __device__ __forceinline__ float exp2f_approx(float x) {
     float y;

@@ -7,6 +7,7 @@ there is no other implementation behind these names.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import os
@@ -632,21 +633,22 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, scale: float 
         if dtypes[i] is None or dev < 0 or g.get_device() != dev or not g.is_contiguous():
             raise ValueError(f"gradient {i} must be contiguous float32, bfloat16 or float16 on CUDA device {dev}, got "
                              f"{g.dtype} on {g.device}")
-    gp = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+    gp = array.array("Q", [g.data_ptr() for g in grads])
     op = gp
     if out is not None:
         for i, (g, o) in enumerate(zip(grads, outs)):
             if o.dtype is not g.dtype or o.get_device() != dev or o.shape != g.shape or not o.is_contiguous():
                 raise ValueError(f"out {i} must be contiguous {g.dtype} {list(g.shape)} on CUDA device {dev}, got "
                                  f"{o.dtype} {list(o.shape)} on {o.device}")
-        op = (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs])
-    sizes = (ctypes.c_longlong * n)(*[g.numel() for g in grads])
+        op = array.array("Q", [o.data_ptr() for o in outs])
+    sizes, types = array.array("q", [g.numel() for g in grads]), array.array("i", dtypes)
     nbytes = _clip_work(n, dev)
     # the norm and the workspace in one allocation: the workspace first, for its alignment
-    buf = torch.empty(nbytes // 4 + 1, device=f"cuda:{dev}", dtype=torch.float32)
+    buf = torch.empty_strided((nbytes // 4 + 1,), (1,), device=f"cuda:{dev}", dtype=torch.float32)
     norm = buf[-1]
-    _check(lib().vf_clip_grad_norm(n, gp, op, sizes, (ctypes.c_int * n)(*dtypes), float(scale), float(max_norm),
-                                   norm.data_ptr(), buf.data_ptr(), nbytes, torch._C._cuda_getCurrentRawStream(dev)))
+    _check(lib().vf_clip_grad_norm(n, gp.buffer_info()[0], op.buffer_info()[0], sizes.buffer_info()[0],
+                                   types.buffer_info()[0], scale, max_norm, norm.data_ptr(), buf.data_ptr(), nbytes,
+                                   torch._C._cuda_getCurrentRawStream(dev)))
     return norm, outs
 
 
