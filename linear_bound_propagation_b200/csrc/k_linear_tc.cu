@@ -959,12 +959,12 @@ cudaError_t cluster_limit(const void* kern, const cudaLaunchConfig_t* cfg, int* 
 }
 
 template <typename T, int PL, int BN>
-cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int count, int sms, cudaStream_t s) {
+cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int count, int split, int sms,
+                      cudaStream_t s) {
     constexpr int BK = block_k<PL>(), CG = pair_of<BN>();
     const bool bf16 = PL == 3 || std::is_same<T, __nv_bfloat16>::value;
     Maps m;
     memset(&m, 0, sizeof(m));
-    int min_nk = 1 << 30;
     long long tiles = 0;
     for (int k = 0; k < count; ++k) {
         TcProduct& p = P.p[k];
@@ -975,7 +975,6 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
         if (n > 0x3fffffffLL) return cudaErrorInvalidValue;  // tile numbers are ints
         p.tiles = (int)n;
         tiles += n;
-        min_nk = std::min(min_nk, p.nk);
         if (!make_map(&m.a[k], A[k].o, PL, A[k].mn, BK, BM, bf16) || !make_map(&m.b[k], B[k].o, PL, B[k].mn, BK, BN / CG, bf16))
             return cudaErrorInvalidValue;
         constexpr int R = epi_round<T, BN>();
@@ -1000,12 +999,12 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    // Few tiles: split the reduction over a cluster, each CTA keeping at least two blocks of it, as long as all clusters
-    // run at once (a cluster's CTAs share a GPC, so fewer may fit than the SMs suggest).
+    // The planned cluster, as long as all clusters run at once (a cluster's CTAs share a GPC, so fewer may fit than the SMs
+    // suggest).
     P.split = 1;
     P.split_log = 0;
     const int slots = sms * ctas_per_sm<BN>();
-    while (CG == 1 && count > 0 && P.split < 8 && tiles * P.split * 2 <= slots && min_nk >= P.split * 4) {
+    while (CG == 1 && P.split < split) {
         at[0].val.clusterDim.x = P.split * 2;
         cfg.numAttrs = 1;
         cfg.gridDim = dim3((unsigned)(tiles * P.split * 2));
@@ -1024,32 +1023,76 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
     return cudaLaunchKernelEx(&cfg, kern, m, P);
 }
 
+// A launch as planned: tile width, cluster size and estimated time in SM cycles. The estimate: a block of the reduction
+// costs what its MMAs take (fp32: twelve of 32 to 128 cycles; 16-bit: four, or the issuing thread's loop), a tile at least
+// its epilogue (30 cycles a column), a CTA 6000 cycles before and after, a join 4000; all measured on this kernel.
+struct Plan {
+    int bn, split;
+    double cost;
+};
+
+Plan plan(const TcProduct* p, int count, bool mn, bool f32, int sms) {
+    Plan best{64, 1, 1e300};
+    long long J = 1, I = 1;
+    for (int k = 0; k < count; ++k) {
+        J = std::max(J, p[k].J);
+        I = std::max(I, p[k].I);
+    }
+    for (int bn = 16; bn <= 256; bn *= 2) {
+        if (bn < 64 && (mn || J > bn)) continue;
+        if (bn > 64 && (J <= bn / 2 || (bn == 256 && I <= BM))) continue;
+        const int cg = bn == 256 ? 2 : 1, slots = sms * (bn <= 32 ? 2 : 1);
+        const double tb = f32 ? (bn == 256 ? 1536 : bn == 128 ? 1000 : bn == 64 ? 860 : 700) : (bn == 256 ? 560 : 480);
+        const double epi = 30.0 * bn;
+        for (int split = 1; split <= 8; split *= 2) {
+            double total = 0, longest = 0;
+            long long tiles = 0;
+            int min_nk = 1 << 30;
+            for (int k = 0; k < count; ++k) {
+                const long long n = (p[k].I + BM * cg - 1) / (BM * cg) * ((p[k].J + bn - 1) / bn);
+                const double t = std::max((double)((p[k].nk + split - 1) / split) * tb, epi);
+                tiles += n;
+                total += t * n * split;
+                longest = std::max(longest, t);
+                min_nk = std::min(min_nk, p[k].nk);
+            }
+            const long long workers = slots / cg;
+            if (split > 1 && (cg > 1 || tiles * split > slots || min_nk < 2 * split)) break;
+            double cost = tiles * split <= workers ? longest
+                          : count == 1             ? (double)((tiles * split + workers - 1) / workers) * longest
+                                                   : std::max(total / workers, longest) + 0.3 * longest;
+            cost += epi + 6000 + (split > 1 ? 4000 : 0);
+            if (cost < best.cost) best = Plan{bn, split, cost};
+        }
+    }
+    return best;
+}
+
 template <typename T, int PL>
 cudaError_t launch_pl(TcParams& P, const Side (&A)[2], const Side (&B)[2], int count, cudaStream_t s) {
     int sms = 0;
-    const cudaError_t e = device_sms(&sms);
+    cudaError_t e = device_sms(&sms);
     if (e != cudaSuccess) return e;
-    long long J = 1;
-    bool mn = false;
-    for (int k = 0; k < count; ++k) {
-        J = std::max(J, P.p[k].J);
-        mn = mn || B[k].mn;
+    const Plan both = plan(P.p, count, (count > 0 && B[0].mn) || (count > 1 && B[1].mn), PL == 3, sms);
+    if (count == 2) {
+        // products of very different shapes go one after the other, each in its own way
+        const Plan a = plan(P.p, 1, B[0].mn, PL == 3, sms), b = plan(P.p + 1, 1, B[1].mn, PL == 3, sms);
+        if (a.cost + b.cost + 4000 < both.cost) {
+            TcParams Q{};
+            Q.p[0] = P.p[1];
+            const Side A1[2] = {A[1], {}}, B1[2] = {B[1], {}};
+            P.p[1] = TcProduct{};
+            if ((e = launch_pl<T, PL>(P, A, B, 1, s)) != cudaSuccess) return e;
+            return launch_pl<T, PL>(Q, A1, B1, 1, s);
+        }
     }
-    if (!mn && J <= 16) return launch_bn<T, PL, 16>(P, A, B, count, sms, s);
-    if (!mn && J <= 32) return launch_bn<T, PL, 32>(P, A, B, count, sms, s);
-    // 256 columns halve the operand reads per MMA; narrower tiles where they fill more of the SMs
-    auto tiles = [&](int bn) {
-        long long n = 0;
-        for (int k = 0; k < count; ++k) n += (P.p[k].I + BM - 1) / BM * ((P.p[k].J + bn - 1) / bn);
-        return n;
-    };
-    auto cost = [&](int bn) { return (tiles(bn) + sms - 1) / sms * (bn + 48); };
-    long long I = 1;
-    for (int k = 0; k < count; ++k) I = std::max(I, P.p[k].I);
-    if (J > 128 && I > BM && cost(256) <= cost(128) && cost(256) <= cost(64))
-        return launch_bn<T, PL, 256>(P, A, B, count, sms, s);
-    if (J > 64 && cost(128) <= cost(64)) return launch_bn<T, PL, 128>(P, A, B, count, sms, s);
-    return launch_bn<T, PL, 64>(P, A, B, count, sms, s);
+    switch (both.bn) {
+        case 16: return launch_bn<T, PL, 16>(P, A, B, count, both.split, sms, s);
+        case 32: return launch_bn<T, PL, 32>(P, A, B, count, both.split, sms, s);
+        case 64: return launch_bn<T, PL, 64>(P, A, B, count, both.split, sms, s);
+        case 128: return launch_bn<T, PL, 128>(P, A, B, count, both.split, sms, s);
+        default: return launch_bn<T, PL, 256>(P, A, B, count, both.split, sms, s);
+    }
 }
 
 cudaError_t launch_products(int dtype, TcParams& P, const Side (&A)[2], const Side (&B)[2], int count, cudaStream_t s) {

@@ -132,9 +132,12 @@ int vf_linear_workspace(int dtype, long long M, int N, int K, int grad, size_t* 
     if (bytes == nullptr) return ops_fail(VF_ERR_ARG, "NULL pointer");
     OPS_TRY(check_kind(dtype, VF_ACT_NONE));
     OPS_TRY(check_sizes(M, N, K));
-    *bytes = use_tc(M, N, K) && (grad != 0 || !linear_direct_fits(dtype, M, N, K))
-                 ? linear_tc_workspace(dtype, M, N, K, grad != 0)
-                 : 0;
+    if (grad != 0 && linear_few_supported(M, N, K))
+        *bytes = linear_few_workspace(M, N, K);
+    else if (use_tc(M, N, K) && (grad != 0 || !linear_direct_fits(dtype, M, N, K)))
+        *bytes = linear_tc_workspace(dtype, M, N, K, grad != 0);
+    else
+        *bytes = 0;
     return VF_OK;
 }
 
@@ -180,11 +183,13 @@ int vf_linear_grad(int dtype, int act, const void* dy, long long lddy, const voi
     OPS_TRY(check_vector("db", db, dtype));
     if (dr != nullptr) OPS_TRY(check_matrix("dr", dr, M, N, lddr, dtype));
     const LinearGrad p{dtype, act, dy, lddy, z, ldz, x, ldx, W, ldw, M, N, K, dx, lddx, dW, lddw, db, dr, lddr};
-    if (!use_tc(M, N, K)) return launched(launch_linear_grad_ffma(p, (cudaStream_t)stream));
+    const bool few = linear_few_supported(M, N, K);
+    if (!few && !use_tc(M, N, K)) return launched(launch_linear_grad_ffma(p, (cudaStream_t)stream));
     OPS_TRY(check_aligned(work));
     size_t need = 0;
     const size_t have = work == nullptr ? 0 : work_bytes;
-    OPS_TRY(launched(launch_linear_grad_tc(p, work, have, &need, (cudaStream_t)stream)));
+    OPS_TRY(launched(few ? launch_linear_few_grad(p, work, have, &need, (cudaStream_t)stream)
+                         : launch_linear_grad_tc(p, work, have, &need, (cudaStream_t)stream)));
     return check_work(have, need);
 }
 
