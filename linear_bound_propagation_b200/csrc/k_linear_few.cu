@@ -1,10 +1,11 @@
 // Backward pass of the dense layer for a few rows (M <= 8) on the FFMA units.
 //
 // With so few rows the pass is W read once (dx = g W) and dW written once (dW = g^T x): 2 N K elements against 4 M N K
-// operations, bound by memory, and one loop over the rows of both serves both. A block takes a slab of rows n and a chunk
-// of columns k: g of the slab is formed once in shared memory (fp32, not rounded), x of the chunk stays in registers, and
-// each row of W and of dW passes through once. dx of a slab is a partial sum; a second launch adds the slabs in a fixed
-// order. db and dr come from the first chunk's blocks.
+// operations, bound by memory. A block takes a slab of rows n and a chunk of columns k of one of the two; g of the slab
+// is formed in shared memory (fp32, not rounded), a warp passes over the slab's rows with its accumulators (or its part of
+// x) in registers. dx of a slab is a partial sum; a second launch adds the slabs in a fixed order. db and dr come from the
+// first chunk's blocks. One block for both products kept W's loads waiting behind twice the registers: 8 x 4096 x 4096
+// bf16 52 us, apart 36 us.
 #include <algorithm>
 
 #include "vf_internal.cuh"
@@ -14,7 +15,7 @@ namespace vf {
 
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int MAX_M = 8;
 constexpr int MAX_SLAB = 1024;  // rows of g in shared memory: 32 KB for eight rows of inputs
 
@@ -26,101 +27,112 @@ struct FewParams {
     long long lddx, lddw, lddr;
     float* part;  // [slab][M][K], or nullptr: one slab, dx is written as it is
     int slab;     // rows of a slab
-    int tx;       // threads along k
+    int dx_z;     // blockIdx.z of the blocks for dx (the others: dW, db and dr), -1: none
 };
 
+// VEC consecutive elements of a row (16 bytes, or one element where rows are not aligned).
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Row {
-    T v[VEC];
-};
+__device__ __forceinline__ void load_row(const T* p, float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+        v[0] = to_f32(p[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        const float4 q = *reinterpret_cast<const float4*>(p);
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    } else {
+        unpack8(*reinterpret_cast<const Pack8<T>*>(p), v);
+    }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_row(T* p, const float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+        p[0] = from_f32<T>(v[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        Pack8<T> q;
+        pack8(q, v);
+        *reinterpret_cast<Pack8<T>*>(p) = q;
+    }
+}
 
 template <typename T, int VEC, int MB>
 __global__ void __launch_bounds__(THREADS) linear_few_grad_k(const __grid_constant__ FewParams P) {
-    extern __shared__ float g[];  // [MB][slab], then [THREADS * VEC] for the sum over ty
-    const int tx = threadIdx.x % P.tx, ty = threadIdx.x / P.tx, TY = THREADS / P.tx;
-    const int k = (blockIdx.x * P.tx + tx) * VEC;
+    extern __shared__ float g[];  // [MB][slab], then [WARPS][32 * VEC] for the sum over the warps
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int k = (blockIdx.x * 32 + lane) * VEC;
     const int n0 = blockIdx.y * P.slab, rows = min(P.slab, P.N - n0);
-    for (int i = threadIdx.x; i < MB * rows; i += THREADS) {
-        const int m = i / rows, n = n0 + i % rows;
-        float v = 0.f;
-        if (m < P.M) {
-            v = to_f32(((const T*)P.dy)[m * P.lddy + n]);
-            if (P.act != VF_ACT_NONE) v = act_grad<sizeof(T) == 2>(v, to_f32(((const T*)P.z)[m * P.ldz + n]), P.act);
-            if (P.dr != nullptr && blockIdx.x == 0) ((T*)P.dr)[m * P.lddr + n] = from_f32<T>(v);
+    const bool is_dx = (int)blockIdx.z == P.dx_z, first = !is_dx && blockIdx.x == 0;
+    for (int i = threadIdx.x; i < rows; i += THREADS) {
+        float v[MB], sum = 0.f;
+#pragma unroll
+        for (int m = 0; m < MB; ++m) v[m] = m < P.M ? to_f32(((const T*)P.dy)[m * P.lddy + n0 + i]) : 0.f;
+        if (P.act != VF_ACT_NONE) {
+            float z[MB];
+#pragma unroll
+            for (int m = 0; m < MB; ++m) z[m] = m < P.M ? to_f32(((const T*)P.z)[m * P.ldz + n0 + i]) : 0.f;
+#pragma unroll
+            for (int m = 0; m < MB; ++m) v[m] = act_grad<sizeof(T) == 2>(v[m], z[m], P.act);
         }
-        g[m * P.slab + i % rows] = v;
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+            g[m * P.slab + i] = v[m];
+            sum += v[m];
+            if (first && P.dr != nullptr && m < P.M) ((T*)P.dr)[m * P.lddr + n0 + i] = from_f32<T>(v[m]);
+        }
+        if (first && P.db != nullptr) ((T*)P.db)[n0 + i] = from_f32<T>(sum);
     }
     __syncthreads();
-    if (P.db != nullptr && blockIdx.x == 0)
-        for (int i = threadIdx.x; i < rows; i += THREADS) {
-            float s = 0.f;
-#pragma unroll
-            for (int m = 0; m < MB; ++m) s += g[m * P.slab + i];
-            ((T*)P.db)[n0 + i] = from_f32<T>(s);
-        }
-    const bool on = k < P.K;
-    float x[MB][VEC], acc[MB][VEC];
-#pragma unroll
-    for (int m = 0; m < MB; ++m) {
-        Row<T, VEC> r;
-        if (P.dW != nullptr && on && m < P.M) r = *reinterpret_cast<const Row<T, VEC>*>((const T*)P.x + m * P.ldx + k);
-#pragma unroll
-        for (int u = 0; u < VEC; ++u) {
-            x[m][u] = P.dW != nullptr && on && m < P.M ? to_f32(r.v[u]) : 0.f;
-            acc[m][u] = 0.f;
-        }
-    }
-    if (on) {
+    if (is_dx) {
+        float acc[MB][VEC] = {};
+        if (k < P.K) {
+            const T* W = (const T*)P.W + (long long)n0 * P.ldw + k;
 #pragma unroll 4
-        for (int r = ty; r < rows; r += TY) {
-            float w[VEC], d[VEC];
-            if (P.dx != nullptr) {
-                const Row<T, VEC> v = *reinterpret_cast<const Row<T, VEC>*>((const T*)P.W + (long long)(n0 + r) * P.ldw + k);
+            for (int r = warp; r < rows; r += WARPS) {
+                float w[VEC];
+                load_row<T, VEC>(W + (long long)r * P.ldw, w);
 #pragma unroll
-                for (int u = 0; u < VEC; ++u) w[u] = to_f32(v.v[u]);
-            } else {
+                for (int m = 0; m < MB; ++m) {
+                    const float gm = g[m * P.slab + r];
 #pragma unroll
-                for (int u = 0; u < VEC; ++u) w[u] = 0.f;
-            }
-#pragma unroll
-            for (int u = 0; u < VEC; ++u) d[u] = 0.f;
-#pragma unroll
-            for (int m = 0; m < MB; ++m) {
-                const float gm = g[m * P.slab + r];
-#pragma unroll
-                for (int u = 0; u < VEC; ++u) {
-                    acc[m][u] = fmaf(gm, w[u], acc[m][u]);
-                    d[u] = fmaf(gm, x[m][u], d[u]);
+                    for (int u = 0; u < VEC; ++u) acc[m][u] = fmaf(gm, w[u], acc[m][u]);
                 }
             }
-            if (P.dW != nullptr) {
-                Row<T, VEC> o;
-#pragma unroll
-                for (int u = 0; u < VEC; ++u) o.v[u] = from_f32<T>(d[u]);
-                *reinterpret_cast<Row<T, VEC>*>((T*)P.dW + (long long)(n0 + r) * P.lddw + k) = o;
-            }
         }
-    }
-    if (P.dx == nullptr) return;
-    float* red = g + MB * P.slab;
+        float* red = g + MB * P.slab;
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
-        if (m >= P.M) break;
-        __syncthreads();
+        for (int m = 0; m < MB; ++m) {
+            if (m >= P.M) break;
+            __syncthreads();
 #pragma unroll
-        for (int u = 0; u < VEC; ++u) red[(ty * P.tx + tx) * VEC + u] = acc[m][u];
-        __syncthreads();
-        // the sums over ty of the chunk's tx * VEC columns
-        for (int i = threadIdx.x; i < P.tx * VEC; i += THREADS) {
-            const int c = blockIdx.x * P.tx * VEC + i;
-            float s = 0.f;
-            for (int t = 0; t < TY; ++t) s += red[t * P.tx * VEC + i];
-            if (c < P.K) {
+            for (int u = 0; u < VEC; ++u) red[(warp * 32 + lane) * VEC + u] = acc[m][u];
+            __syncthreads();
+            const int c = blockIdx.x * 32 * VEC + threadIdx.x;
+            if (threadIdx.x < 32 * VEC && c < P.K) {
+                float s = 0.f;
+#pragma unroll
+                for (int t = 0; t < WARPS; ++t) s += red[t * 32 * VEC + threadIdx.x];
                 if (P.part != nullptr)
                     P.part[((long long)blockIdx.y * P.M + m) * P.K + c] = s;
                 else
                     ((T*)P.dx)[m * P.lddx + c] = from_f32<T>(s);
             }
+        }
+    } else if (P.dW != nullptr && k < P.K) {
+        float x[MB][VEC];
+#pragma unroll
+        for (int m = 0; m < MB; ++m) load_row<T, VEC>((const T*)P.x + (m < P.M ? m : 0) * P.ldx + k, x[m]);
+        T* dW = (T*)P.dW + (long long)n0 * P.lddw + k;
+#pragma unroll 2
+        for (int r = warp; r < rows; r += WARPS) {
+            float d[VEC] = {};
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+                if (m >= P.M) break;  // x of a row that does not exist may be infinite
+                const float gm = g[m * P.slab + r];
+#pragma unroll
+                for (int u = 0; u < VEC; ++u) d[u] = fmaf(gm, x[m][u], d[u]);
+            }
+            store_row<T, VEC>(dW + (long long)r * P.lddw, d);
         }
     }
 }
@@ -137,18 +149,15 @@ linear_few_join_k(const float* part, int slabs, int M, int K, T* dx, long long l
 }
 
 struct Shape {
-    int tx, chunks, slab, slabs;
+    int chunks, slab, slabs;
 };
 
-// Threads along k: as many vectors as a row has, 32 to 256. Slabs: enough blocks to fill the SMs a few times over, none
-// below four rows per thread row.
-Shape shape_of(int N, int K, int vec) {
+// Chunks of 32 vectors. Slabs: enough blocks to fill the SMs a few times over, but four rows a warp at least, and
+// partial sums of dx (fp32, M rows a slab) of no more than about a quarter of W's bytes.
+Shape shape_of(int M, int N, int K, int vec, int elem) {
     Shape s;
-    s.tx = 32;
-    while (s.tx < THREADS && s.tx * vec < K) s.tx *= 2;
-    s.chunks = (K + s.tx * vec - 1) / (s.tx * vec);
-    const int ty = THREADS / s.tx;
-    const int want = std::max(1, std::min((592 + s.chunks - 1) / s.chunks, (N + 4 * ty - 1) / (4 * ty)));
+    s.chunks = (K + 32 * vec - 1) / (32 * vec);
+    const int want = std::min({(592 + s.chunks - 1) / s.chunks, (N + 4 * WARPS - 1) / (4 * WARPS), std::max(1, (int)((long long)N * elem / (16 * M)))});
     s.slab = std::min(MAX_SLAB, (N + want - 1) / want);
     s.slabs = (N + s.slab - 1) / s.slab;
     return s;
@@ -162,15 +171,17 @@ bool rows_of(const void* p, long long ld, int vec) {
 template <typename T, int VEC, int MB>
 cudaError_t launch_mb(const FewParams& P, const Shape& s, cudaStream_t st) {
     const size_t smem = ((size_t)MB * s.slab + THREADS * VEC) * sizeof(float);
-    linear_few_grad_k<T, VEC, MB><<<dim3(s.chunks, s.slabs), THREADS, smem, st>>>(P);
+    const bool other = P.dW != nullptr || P.db != nullptr || P.dr != nullptr;
+    if (P.dx == nullptr && !other) return cudaSuccess;
+    linear_few_grad_k<T, VEC, MB><<<dim3(s.chunks, s.slabs, (P.dx != nullptr) + other), THREADS, smem, st>>>(P);
     return cudaGetLastError();
 }
 
 template <typename T, int VEC>
 cudaError_t launch_vec(const LinearGrad& f, FewParams& P, float* work, size_t have, size_t* need, cudaStream_t st) {
-    const Shape s = shape_of(f.N, f.K, VEC);
+    const Shape s = shape_of((int)f.M, f.N, f.K, VEC, sizeof(T));
     P.slab = s.slab;
-    P.tx = s.tx;
+    P.dx_z = f.dx != nullptr ? 0 : -1;
     *need = f.dx != nullptr && s.slabs > 1 ? (size_t)s.slabs * f.M * f.K * sizeof(float) : 0;
     if (*need > have) return cudaSuccess;  // the caller reports it
     P.part = *need > 0 ? work : nullptr;
@@ -193,9 +204,10 @@ template <typename T>
 cudaError_t launch_few(const LinearGrad& f, float* work, size_t have, size_t* need, cudaStream_t st) {
     FewParams P{f.dy,  f.act == VF_ACT_NONE ? nullptr : f.z, f.x, f.W, f.lddy, f.ldz, f.ldx, f.ldw, (int)f.M, f.N, f.K,
                 f.act, f.dx, f.dW, f.db, f.dr, f.lddx, f.lddw, f.lddr, nullptr, 0, 0};
-    const bool vec = f.K % 4 == 0 && (f.dx == nullptr || rows_of<T>(f.W, f.ldw, 4)) &&
-                     (f.dW == nullptr || (rows_of<T>(f.x, f.ldx, 4) && rows_of<T>(f.dW, f.lddw, 4)));
-    return vec ? launch_vec<T, 4>(f, P, work, have, need, st) : launch_vec<T, 1>(f, P, work, have, need, st);
+    constexpr int V = 16 / sizeof(T);
+    const bool vec = f.K % V == 0 && (f.dx == nullptr || rows_of<T>(f.W, f.ldw, V)) &&
+                     (f.dW == nullptr || (rows_of<T>(f.x, f.ldx, V) && rows_of<T>(f.dW, f.lddw, V)));
+    return vec ? launch_vec<T, V>(f, P, work, have, need, st) : launch_vec<T, 1>(f, P, work, have, need, st);
 }
 
 }  // namespace
@@ -204,9 +216,9 @@ bool linear_few_supported(long long M, int N, int K) {
     return M >= 1 && M <= MAX_M && N >= 1 && K >= 1 && (long long)N <= 65535LL * MAX_SLAB;
 }
 
-size_t linear_few_workspace(long long M, int N, int K) {
-    const Shape a = shape_of(N, K, 4), b = shape_of(N, K, 1);
-    const int slabs = std::max(a.slabs, b.slabs);
+size_t linear_few_workspace(int dtype, long long M, int N, int K) {
+    const int e = dtype == VF_F32 ? 4 : 2;
+    const int slabs = std::max(shape_of((int)M, N, K, 16 / e, e).slabs, shape_of((int)M, N, K, 1, e).slabs);
     return slabs > 1 ? (size_t)slabs * M * K * sizeof(float) : 0;
 }
 

@@ -72,6 +72,21 @@ struct TcParams {
     void* db;
 };
 
+// Tile number u of a product: its part of the reduction, its place among the tiles, and its blocks kb0 .. kb1 - 1 of the
+// reduction (of a part, or of a CTA's share where a cluster splits it).
+struct Place {
+    int part, i, j, kb0, kb1;
+    __device__ __forceinline__ Place(const TcParams& P, const TcProduct& p, int u, int rank) {
+        part = u & ((1 << p.plog) - 1);
+        u >>= p.plog;
+        j = u / p.tiles_i;
+        i = u - j * p.tiles_i;
+        const int r = P.split > 1 ? rank : part, log = P.split > 1 ? P.split_log : p.plog;
+        kb0 = share(p.nk, r, log);
+        kb1 = share(p.nk, r + 1, log);
+    }
+};
+
 // Tensor maps of a launch: operands, and where rows allow TMA the outputs, the residual and z of p[0].
 struct Maps {
     CUtensorMap a[2], b[2], out[2], res, z;
@@ -196,9 +211,15 @@ constexpr int smem_limit() {
     return BN <= 32 ? 115712 : 232448;
 }
 
+// Blocks per stage. The issuing thread spends about 350 cycles per stage on its barriers, more than the four MMAs of a narrow
+// 16-bit tile take: there a stage holds two blocks.
+template <int PL, int BN>
+constexpr int stage_blocks() {
+    return PL == 1 && BN <= 32 ? 2 : 1;
+}
 template <int PL, int BN>
 constexpr int stage_bytes() {
-    return PL * (BM + BN / pair_of<BN>()) * block_k<PL>() * 2;
+    return stage_blocks<PL, BN>() * PL * (BM + BN / pair_of<BN>()) * block_k<PL>() * 2;
 }
 
 // N columns of this lane, 32 elements apart. The 16-bit conversions work on pairs.
@@ -246,6 +267,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
     constexpr int BL = BN / CG;                              // rows of B that a CTA loads
     constexpr int A_PLANE = BM * BK * 2, B_PLANE = BL * BK * 2;
     constexpr int STAGE = stage_bytes<PL, BN>();
+    constexpr int KS = stage_blocks<PL, BN>(), BLOCK = STAGE / KS;  // blocks of a stage lie one after the other
     constexpr int NB = (PL == 1 || BN <= 128) ? 2 : 1;       // accumulator sets in TMEM
     constexpr int ACC_COLS = NB * BN;
     constexpr int USED_COLS = PL == 3 ? 2 * ACC_COLS : ACC_COLS;
@@ -333,10 +355,11 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
             int w, u;
             while (!*abort_flag && walk.next(w, u)) {
                 const TcProduct& p = P.p[w];
-                const int i0 = u % p.tiles_i * (BM * CG) + pr * BM, j0 = u / p.tiles_i * BN + pr * BL;
+                const Place at(P, p, u, rank);
+                const int i0 = at.i * (BM * CG) + pr * BM, j0 = at.j * BN + pr * BL;
                 const CUtensorMap* ma = &maps.a[w];
                 const CUtensorMap* mb = &maps.b[w];
-                const int kb0 = share(p.nk, rank, P.split_log), kb1 = share(p.nk, rank + 1, P.split_log);
+                const int kb0 = at.kb0, kb1 = at.kb1;
                 const bool a_mn = p.a_mn, b_mn = p.b_mn;
                 for (int kb = kb0; kb < kb1; ++kb, g.next(NS)) {
                     if (g.lap > 0 && !wait_phase(&empty[g.slot], (g.lap - 1) & 1, abort_flag)) break;
@@ -345,22 +368,24 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                     if (CG == 1 || pr == 0) mbar_expect_tx(&full[g.slot], STAGE * CG);
                     if (CG == 2) bar = leader_addr(&full[g.slot]);
 #pragma unroll
-                    for (int q = 0; q < PL; ++q) {
-                        uint8_t* a = st + q * A_PLANE;
-                        uint8_t* b = st + PL * A_PLANE + q * B_PLANE;
+                    for (int q = 0; q < PL * KS; ++q) {
+                        // plane q % PL of block q / PL (one of the two is always one)
+                        uint8_t* a = st + (q / PL) * BLOCK + (q % PL) * A_PLANE;
+                        uint8_t* b = st + (q / PL) * BLOCK + PL * A_PLANE + (q % PL) * B_PLANE;
+                        const int t0 = (kb * KS + q / PL) * BK;
                         if (a_mn) {
 #pragma unroll
                             for (int c = 0; c < BM / 64; ++c)
-                                load_operand<CG>(a + c * BK * 128, ma, bar, i0 + c * 64, kb * BK, q);
+                                load_operand<CG>(a + c * BK * 128, ma, bar, i0 + c * 64, t0, q % PL);
                         } else {
-                            load_operand<CG>(a, ma, bar, kb * BK, i0, q);
+                            load_operand<CG>(a, ma, bar, t0, i0, q % PL);
                         }
                         if (BL >= 64 && b_mn) {
 #pragma unroll
                             for (int c = 0; c < BL / 64; ++c)
-                                load_operand<CG>(b + c * BK * 128, mb, bar, j0 + c * 64, kb * BK, q);
+                                load_operand<CG>(b + c * BK * 128, mb, bar, j0 + c * 64, t0, q % PL);
                         } else {
-                            load_operand<CG>(b, mb, bar, kb * BK, j0, q);
+                            load_operand<CG>(b, mb, bar, t0, j0, q % PL);
                         }
                     }
                 }
@@ -388,7 +413,8 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
             int w, u;
             while (ok && !*abort_flag && walk.next(w, u)) {
                 const TcProduct& p = P.p[w];
-                const int kb0 = share(p.nk, rank, P.split_log), kb1 = share(p.nk, rank + 1, P.split_log);
+                const Place at(P, p, u, rank);
+                const int kb0 = at.kb0, kb1 = at.kb1;
                 const int a_mn = p.a_mn, b_mn = p.b_mn;
                 const uint32_t fmt = (PL == 3 || std::is_same<T, __nv_bfloat16>::value) ? 1u : 0u;
                 const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)a_mn << 15) |
@@ -425,8 +451,11 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                         break;
                     tc_fence_after();
 #pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk)
-                        mma_f16_ss<CG>(d, ah + kk * step_a, bh + kk * step_b, idesc, (in_chunk > 0 || kk > 0) ? 1u : 0u);
+                    for (int kk = 0; kk < KS * BK / 16; ++kk) {
+                        const uint32_t blk = kk / (BK / 16) * (BLOCK / 16), in = kk % (BK / 16);
+                        mma_f16_ss<CG>(d, ah + blk + in * step_a, bh + blk + in * step_b, idesc,
+                                       (in_chunk > 0 || kk > 0) ? 1u : 0u);
+                    }
                     commit<CG>(&empty[g.slot]);
                     ++in_chunk;
                     if (kb + 1 == kb1 || (PL == 3 && in_chunk == CHUNK)) {
@@ -470,9 +499,10 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
         int w, u;
         while (walk.next(w, u)) {
             const TcProduct& p = P.p[w];
-            const int i0 = u % p.tiles_i * (BM * CG) + pr * BM + q * 32, j0 = u / p.tiles_i * BN + part_no * PART;
+            const Place at(P, p, u, rank);
+            const int i0 = at.i * (BM * CG) + pr * BM + q * 32, j0 = at.j * BN + part_no * PART;
             const long long i = (long long)i0 + lane;
-            const bool by_tma = EPI_TMA && S == 1 && p.vec;
+            const bool by_tma = EPI_TMA && S == 1 && p.vec && p.plog == 0;
             const int rounds = by_tma && i0 < p.I && j0 < p.J ? (int)min((long long)PART / ROUND, (p.J - j0 + ROUND - 1) / ROUND) : 0;
             // the residual comes in while the products run
             if (by_tma && p.res != nullptr) {
@@ -486,7 +516,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
             const float bias = (p.bias != nullptr && i < p.I) ? to_f32(((const T*)p.bias)[i]) : 0.f;
             float r[LD];
             if (S == 1 && !by_tma) res_lane<T>(p, i, j0, r);
-            const int kb0 = share(p.nk, rank, P.split_log), kb1 = share(p.nk, rank + 1, P.split_log);
+            const int kb0 = at.kb0, kb1 = at.kb1;
             uint32_t acc_t = 0;  // TMEM columns that hold this warp's part of the finished tile
             bool alive = true;
             if (PL == 3) {
@@ -589,6 +619,18 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                     ob ^= 1;
                 }
                 if (!alive) break;
+            } else if (p.plog > 0) {
+                float* o = p.sums + ((long long)at.part * p.J + j0) * p.I + i;
+                const int n = (int)min((long long)PART, p.J - j0);
+#pragma unroll 1
+                for (int c = 0; c < PART; c += LD, o += LD * p.I) {
+                    uint32_t v[LD];
+                    tmem_ld<LD>(acc_t + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < LD; ++k)
+                        if (i < p.I && c + k < n) o[k * p.I] = __uint_as_float(v[k]);
+                }
             } else {
                 float rn[LD];
 #pragma unroll 1
@@ -627,9 +669,10 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
         int w, u;
         walk.next(w, u);
         const TcProduct& p = P.p[w];
+        const Place at(P, p, u, rank);
         __syncwarp();
         if (!pushed) cluster_wait();
-        join_cluster<T, BN, 8>(p, u % p.tiles_i * BM, u / p.tiles_i * BN,
+        join_cluster<T, BN, 8>(p, at.i * BM, at.j * BN,
                                reinterpret_cast<const float*>(base + (size_t)NS * STAGE), rank, P.split_log, warp - 2);
     }
     tc_fence_before();
@@ -808,6 +851,30 @@ linear_operands_k(const __grid_constant__ GradJob g, const __grid_constant__ Pac
         pack_block<T>(b, t - g.blocks - a.blocks);
 }
 
+// The sums of a reduction cut into parts, added in order.
+struct JoinJob {
+    const float* sums;
+    long long I, n;  // n = I * J
+    int parts;
+    void* out;
+    long long ldo;
+    int blocks;
+};
+constexpr int JOIN_THREADS = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(JOIN_THREADS)
+linear_join_k(const __grid_constant__ JoinJob a, const __grid_constant__ JoinJob b) {
+    grid_wait();
+    const JoinJob& j = (int)blockIdx.x < a.blocks ? a : b;
+    const long long e = ((long long)blockIdx.x - ((int)blockIdx.x < a.blocks ? 0 : a.blocks)) * JOIN_THREADS + threadIdx.x;
+    if (e >= j.n) return;
+    float s = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < j.parts; ++k) s += j.sums[k * j.n + e];
+    ((T*)j.out)[e / j.I * j.ldo + e % j.I] = from_f32<T>(s);
+}
+
 // ------------------------------------------------------------------------------------------------- host side
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -939,6 +1006,138 @@ struct Side {
     bool mn;
 };
 
+int blocks_of(int dtype, long long t) {
+    const int bk = dtype == VF_F32 ? block_k<3>() : block_k<1>();
+    return (int)((t + bk - 1) / bk);
+}
+
+// A launch as planned: tile width, cluster size, parts of each product's reduction (log 2) and estimated time in SM cycles.
+struct Plan {
+    int bn, split, plog[2];
+    double cost;
+};
+
+// Products of a call: output extents and blocks of the reduction, the longer reduction first.
+struct Extents {
+    long long I[2], J[2];
+    int nk[2], count;
+    bool mn[2];  // B contiguous along j: tiles of 64 columns and more
+};
+
+// Estimated cycles of one tile: a block of the reduction costs what its MMAs take (fp32: twelve of 32 to 128 cycles;
+// 16-bit: four, or the issuing thread's loop), a tile at least its epilogue, 30 cycles a column; measured on this kernel.
+double tile_cycles(int nk, bool f32, int bn) {
+    const double tb = f32 ? (bn == 256 ? 1536 : bn == 128 ? 1000 : bn == 64 ? 860 : 700) : (bn == 256 ? 560 : bn >= 64 ? 480 : 290);
+    return std::max(nk * tb, 30.0 * bn);
+}
+
+// The cheapest launch by estimate: tiles per worker times their cycles, plus an epilogue, 6000 cycles before and after,
+// 4000 for a join over a cluster; parts cost another launch and their sums' way through L2 (1300 bytes a cycle). Parts
+// are taken until a tile is no longer than the average worker's load, eight blocks of the reduction each at least.
+Plan plan(const Extents& x, bool f32, bool parts, int sms) {
+    Plan best{64, 1, {0, 0}, 1e300};
+    long long J = 1, I = 1;
+    bool mn = false;
+    for (int k = 0; k < x.count; ++k) {
+        J = std::max(J, x.J[k]);
+        I = std::max(I, x.I[k]);
+        mn = mn || x.mn[k];
+    }
+    for (int bn = 16; bn <= 256; bn *= 2) {
+        if (bn < 64 && (mn || J > bn)) continue;
+        if (bn > 64 && (J <= bn / 2 || (bn == 256 && I <= BM))) continue;
+        const int cg = bn == 256 ? 2 : 1, slots = sms * (bn <= 32 ? 2 : 1), workers = slots / cg;
+        auto tiles_of = [&](int k) { return (x.I[k] + BM * cg - 1) / (BM * cg) * ((x.J[k] + bn - 1) / bn); };
+        auto consider = [&](int split, const int (&plog)[2]) {
+            double total = 0, longest = 0, join = 0;
+            long long tiles = 0;
+            for (int k = 0; k < x.count; ++k) {
+                const int cut = split << plog[k];
+                const double t = tile_cycles((x.nk[k] + cut - 1) / cut, f32, bn);
+                const long long n = tiles_of(k) * cut;
+                tiles += n;
+                total += t * n;
+                longest = std::max(longest, t);
+                if (plog[k] > 0) join += (double)(x.I[k] * x.J[k]) * (8 << plog[k]) / 1300;
+            }
+            double cost = tiles <= workers     ? longest
+                          : x.count == 1 ? (double)((tiles + workers - 1) / workers) * longest
+                                         : std::max(total / workers, longest) + 0.3 * longest;
+            cost += 30.0 * bn + 6000 + (split > 1 ? 4000 : 0) + (join > 0 ? 8000 + join : 0);
+            if (cost < best.cost) best = Plan{bn, split, {plog[0], plog[1]}, cost};
+        };
+        long long tiles = 0;
+        int min_nk = 1 << 30;
+        double load = 0;
+        for (int k = 0; k < x.count; ++k) {
+            tiles += tiles_of(k);
+            min_nk = std::min(min_nk, x.nk[k]);
+            load += tile_cycles(x.nk[k], f32, bn) * tiles_of(k) / workers;
+        }
+        for (int split = 1; split <= 8; split *= 2) {
+            if (split > 1 && (cg > 1 || tiles * split > slots || min_nk < 4 * split)) break;
+            consider(split, {0, 0});
+        }
+        if (parts) {
+            int plog[2] = {0, 0};
+            for (int k = 0; k < x.count; ++k)
+                while (plog[k] < 4 && x.nk[k] >> plog[k] >= 16 && tile_cycles(x.nk[k] >> plog[k], f32, bn) > load) ++plog[k];
+            if (plog[0] + plog[1] > 0) consider(1, plog);
+        }
+    }
+    return best;
+}
+
+// One launch for all products, or one for each.
+struct Plans {
+    bool apart;
+    Plan a, b;  // of all, or of the first and the second
+};
+Plans plans(const Extents& x, bool f32, bool parts, int sms) {
+    Plans r{false, plan(x, f32, parts, sms), {}};
+    if (x.count < 2) return r;
+    Extents y = x, z = x;
+    y.count = z.count = 1;
+    z.I[0] = x.I[1];
+    z.J[0] = x.J[1];
+    z.nk[0] = x.nk[1];
+    z.mn[0] = x.mn[1];
+    const Plan a = plan(y, f32, parts, sms), b = plan(z, f32, parts, sms);
+    return a.cost + b.cost + 4000 < r.a.cost ? Plans{true, a, b} : r;
+}
+int plog_of(const Plans& p, int k) { return p.apart && k == 1 ? p.b.plog[0] : p.a.plog[k]; }
+
+// The backward pass's products, dx and dW as far as wanted.
+Extents grad_extents(int dtype, long long M, int N, int K, bool dx, bool dW) {
+    Extents x{};
+    if (dx) {
+        x.I[0] = K;
+        x.J[0] = M;
+        x.nk[0] = blocks_of(dtype, N);
+        x.count = 1;
+    }
+    if (dW) {
+        const int k = x.count++;
+        x.I[k] = K;
+        x.J[k] = N;
+        x.nk[k] = blocks_of(dtype, M);
+        x.mn[k] = true;
+    }
+    if (x.count == 2 && x.nk[1] > x.nk[0]) {
+        std::swap(x.I[0], x.I[1]);
+        std::swap(x.J[0], x.J[1]);
+        std::swap(x.nk[0], x.nk[1]);
+        std::swap(x.mn[0], x.mn[1]);
+    }
+    return x;
+}
+size_t sums_bytes(const Extents& x, const Plans& p) {
+    size_t n = 0;
+    for (int k = 0; k < x.count; ++k)
+        if (plog_of(p, k) > 0) n += (size_t)round_up(((x.I[k] * x.J[k]) << plog_of(p, k)) * 4, 256);
+    return n;
+}
+
 // Clusters of cfg's size that run at once on the current device (asked once per kernel, size and device).
 cudaError_t cluster_limit(const void* kern, const cudaLaunchConfig_t* cfg, int* fit) {
     static std::mutex mu;
@@ -970,15 +1169,16 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
         TcProduct& p = P.p[k];
         p.a_mn = A[k].mn;
         p.b_mn = B[k].mn;
+        p.nk = (p.nk + stage_blocks<PL, BN>() - 1) / stage_blocks<PL, BN>();  // stages from here on
         p.tiles_i = (int)((p.I + BM * CG - 1) / (BM * CG));
-        const long long n = (long long)p.tiles_i * ((p.J + BN - 1) / BN);
+        const long long n = ((long long)p.tiles_i * ((p.J + BN - 1) / BN)) << p.plog;
         if (n > 0x3fffffffLL) return cudaErrorInvalidValue;  // tile numbers are ints
         p.tiles = (int)n;
         tiles += n;
         if (!make_map(&m.a[k], A[k].o, PL, A[k].mn, BK, BM, bf16) || !make_map(&m.b[k], B[k].o, PL, B[k].mn, BK, BN / CG, bf16))
             return cudaErrorInvalidValue;
         constexpr int R = epi_round<T, BN>();
-        if (BN >= 64 && p.vec &&
+        if (BN >= 64 && p.vec && p.plog == 0 &&
             (!make_rows<T>(&m.out[k], p.out, p.I, p.J, p.ldo, R) ||
              (p.res != nullptr && !make_rows<T>(&m.res, p.res, p.I, p.J, p.ldr, R)) ||
              (p.zout != nullptr && !make_rows<T>(&m.z, p.zout, p.I, p.J, p.ldz, R))))
@@ -1016,96 +1216,72 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
     }
     P.workers = (int)std::min<long long>(tiles, P.split > 1 ? tiles : slots / CG);
     if (tiles == 0) P.workers = std::min((P.N + 255) / 256, sms);
-    P.gap = P.split > 1 || count < 2 ? 1 : std::max(1, (P.p[0].nk + P.p[1].nk / 2) / P.p[1].nk);
+    P.gap = 1;
+    if (P.split == 1 && count == 2) {
+        // as long as a tile of p[0], but no more than evens out over the workers that its last turn leaves idle
+        const int rem = P.p[0].tiles % P.workers;
+        const double a = tile_cycles(P.p[0].nk >> P.p[0].plog, PL == 3, BN), b = tile_cycles(P.p[1].nk >> P.p[1].plog, PL == 3, BN);
+        P.gap = std::max(1, std::min((int)(a / b + 0.5), (P.p[1].tiles + P.workers - rem - 1) / (P.workers - rem)));
+    }
     cfg.gridDim = dim3((unsigned)(P.workers * CG * P.split));
     at[0].val.clusterDim.x = CG * P.split;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, m, P);
 }
 
-// A launch as planned: tile width, cluster size and estimated time in SM cycles. The estimate: a block of the reduction
-// costs what its MMAs take (fp32: twelve of 32 to 128 cycles; 16-bit: four, or the issuing thread's loop), a tile at least
-// its epilogue (30 cycles a column), a CTA 6000 cycles before and after, a join 4000; all measured on this kernel.
-struct Plan {
-    int bn, split;
-    double cost;
-};
-
-Plan plan(const TcProduct* p, int count, bool mn, bool f32, int sms) {
-    Plan best{64, 1, 1e300};
-    long long J = 1, I = 1;
-    for (int k = 0; k < count; ++k) {
-        J = std::max(J, p[k].J);
-        I = std::max(I, p[k].I);
+template <typename T, int PL>
+cudaError_t launch_as(TcParams& P, const Side (&A)[2], const Side (&B)[2], int count, const Plan& plan, int sms,
+                      cudaStream_t s) {
+    switch (plan.bn) {
+        case 16: return launch_bn<T, PL, 16>(P, A, B, count, plan.split, sms, s);
+        case 32: return launch_bn<T, PL, 32>(P, A, B, count, plan.split, sms, s);
+        case 64: return launch_bn<T, PL, 64>(P, A, B, count, plan.split, sms, s);
+        case 128: return launch_bn<T, PL, 128>(P, A, B, count, plan.split, sms, s);
+        default: return launch_bn<T, PL, 256>(P, A, B, count, plan.split, sms, s);
     }
-    for (int bn = 16; bn <= 256; bn *= 2) {
-        if (bn < 64 && (mn || J > bn)) continue;
-        if (bn > 64 && (J <= bn / 2 || (bn == 256 && I <= BM))) continue;
-        const int cg = bn == 256 ? 2 : 1, slots = sms * (bn <= 32 ? 2 : 1);
-        const double tb = f32 ? (bn == 256 ? 1536 : bn == 128 ? 1000 : bn == 64 ? 860 : 700) : (bn == 256 ? 560 : 480);
-        const double epi = 30.0 * bn;
-        for (int split = 1; split <= 8; split *= 2) {
-            double total = 0, longest = 0;
-            long long tiles = 0;
-            int min_nk = 1 << 30;
-            for (int k = 0; k < count; ++k) {
-                const long long n = (p[k].I + BM * cg - 1) / (BM * cg) * ((p[k].J + bn - 1) / bn);
-                const double t = std::max((double)((p[k].nk + split - 1) / split) * tb, epi);
-                tiles += n;
-                total += t * n * split;
-                longest = std::max(longest, t);
-                min_nk = std::min(min_nk, p[k].nk);
-            }
-            const long long workers = slots / cg;
-            if (split > 1 && (cg > 1 || tiles * split > slots || min_nk < 2 * split)) break;
-            double cost = tiles * split <= workers ? longest
-                          : count == 1             ? (double)((tiles * split + workers - 1) / workers) * longest
-                                                   : std::max(total / workers, longest) + 0.3 * longest;
-            cost += epi + 6000 + (split > 1 ? 4000 : 0);
-            if (cost < best.cost) best = Plan{bn, split, cost};
-        }
-    }
-    return best;
 }
 
 template <typename T, int PL>
-cudaError_t launch_pl(TcParams& P, const Side (&A)[2], const Side (&B)[2], int count, cudaStream_t s) {
-    int sms = 0;
-    cudaError_t e = device_sms(&sms);
-    if (e != cudaSuccess) return e;
-    const Plan both = plan(P.p, count, (count > 0 && B[0].mn) || (count > 1 && B[1].mn), PL == 3, sms);
-    if (count == 2) {
-        // products of very different shapes go one after the other, each in its own way
-        const Plan a = plan(P.p, 1, B[0].mn, PL == 3, sms), b = plan(P.p + 1, 1, B[1].mn, PL == 3, sms);
-        if (a.cost + b.cost + 4000 < both.cost) {
-            TcParams Q{};
-            Q.p[0] = P.p[1];
-            const Side A1[2] = {A[1], {}}, B1[2] = {B[1], {}};
-            P.p[1] = TcProduct{};
-            if ((e = launch_pl<T, PL>(P, A, B, 1, s)) != cudaSuccess) return e;
-            return launch_pl<T, PL>(Q, A1, B1, 1, s);
-        }
+cudaError_t launch_pl(TcParams& P, const Side (&A)[2], const Side (&B)[2], int count, const Plans& plans, int sms,
+                      cudaStream_t s) {
+    JoinJob join[2] = {};
+    for (int k = 0; k < count; ++k) {
+        TcProduct& p = P.p[k];
+        p.plog = plog_of(plans, k);
+        if (p.plog > 0) join[k] = JoinJob{p.sums, p.I, p.I * p.J, 1 << p.plog, p.out, p.ldo, (int)((p.I * p.J + JOIN_THREADS - 1) / JOIN_THREADS)};
     }
-    switch (both.bn) {
-        case 16: return launch_bn<T, PL, 16>(P, A, B, count, both.split, sms, s);
-        case 32: return launch_bn<T, PL, 32>(P, A, B, count, both.split, sms, s);
-        case 64: return launch_bn<T, PL, 64>(P, A, B, count, both.split, sms, s);
-        case 128: return launch_bn<T, PL, 128>(P, A, B, count, both.split, sms, s);
-        default: return launch_bn<T, PL, 256>(P, A, B, count, both.split, sms, s);
+    cudaError_t e;
+    if (!plans.apart) {
+        e = launch_as<T, PL>(P, A, B, count, plans.a, sms, s);
+    } else {
+        TcParams Q{};
+        Q.p[0] = P.p[1];
+        const Side A1[2] = {A[1], {}}, B1[2] = {B[1], {}};
+        P.p[1] = TcProduct{};
+        e = launch_as<T, PL>(P, A, B, 1, plans.a, sms, s);
+        if (e == cudaSuccess) e = launch_as<T, PL>(Q, A1, B1, 1, plans.b, sms, s);
     }
+    const int blocks = join[0].blocks + join[1].blocks;
+    if (e != cudaSuccess || blocks == 0) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(JOIN_THREADS);
+    cfg.stream = s;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, linear_join_k<T>, join[0], join[1]);
 }
 
-cudaError_t launch_products(int dtype, TcParams& P, const Side (&A)[2], const Side (&B)[2], int count, cudaStream_t s) {
+cudaError_t launch_products(int dtype, TcParams& P, const Side (&A)[2], const Side (&B)[2], int count, const Plans& plans,
+                            int sms, cudaStream_t s) {
     switch (dtype) {
-        case VF_F32: return launch_pl<float, 3>(P, A, B, count, s);
-        case VF_BF16: return launch_pl<__nv_bfloat16, 1>(P, A, B, count, s);
-        default: return launch_pl<__half, 1>(P, A, B, count, s);
+        case VF_F32: return launch_pl<float, 3>(P, A, B, count, plans, sms, s);
+        case VF_BF16: return launch_pl<__nv_bfloat16, 1>(P, A, B, count, plans, sms, s);
+        default: return launch_pl<__half, 1>(P, A, B, count, plans, sms, s);
     }
-}
-
-int blocks_of(int dtype, long long t) {
-    const int bk = dtype == VF_F32 ? block_k<3>() : block_k<1>();
-    return (int)((t + bk - 1) / bk);
 }
 
 int col_blocks(int N) { return (N + PACK_COLS - 1) / PACK_COLS; }
@@ -1124,8 +1300,16 @@ bool linear_tc_in_place(const LinearFwd& f) {
 
 size_t linear_tc_workspace(int dtype, long long M, int N, int K, bool grad) {
     size_t n = operand_bytes(dtype, M, K) + operand_bytes(dtype, N, K);
-    if (grad) n += operand_bytes(dtype, M, N) + (size_t)round_up(row_blocks(M, N) * N * 4, 256);
-    return n;
+    if (!grad) return n;
+    n += operand_bytes(dtype, M, N) + (size_t)round_up(row_blocks(M, N) * N * 4, 256);
+    int sms = 0;
+    if (device_sms(&sms) != cudaSuccess) return n;
+    size_t sums = 0;
+    for (int want = 1; want < 4; ++want) {  // dx, dW, both
+        const Extents x = grad_extents(dtype, M, N, K, want & 1, (want & 2) != 0);
+        sums = std::max(sums, sums_bytes(x, plans(x, dtype == VF_F32, true, sms)));
+    }
+    return n + sums;
 }
 
 cudaError_t launch_linear_tc(const LinearFwd& f, void* work, size_t have, size_t* need, cudaStream_t s) {
@@ -1154,7 +1338,14 @@ cudaError_t launch_linear_tc(const LinearFwd& f, void* work, size_t have, size_t
     p.act = f.act;
     p.vec = aligned16(f.y, f.ldy, e) && (f.r == nullptr || aligned16(f.r, f.ldr, e)) &&
             (f.z == nullptr || aligned16(f.z, f.ldz, e));
-    return launch_products(f.dtype, P, A, B, 1, s);
+    Extents x{};
+    x.I[0] = p.I;
+    x.J[0] = p.J;
+    x.nk[0] = p.nk;
+    x.count = 1;
+    int sms = 0;
+    if ((err = device_sms(&sms)) != cudaSuccess) return err;
+    return launch_products(f.dtype, P, A, B, 1, plans(x, f.dtype == VF_F32, false, sms), sms, s);
 }
 
 cudaError_t launch_linear_grad_tc(const LinearGrad& f, void* work, size_t have, size_t* need, cudaStream_t s) {
@@ -1217,21 +1408,27 @@ cudaError_t launch_linear_grad_tc(const LinearGrad& f, void* work, size_t have, 
         p.ldo = f.lddw;
         p.vec = aligned16(f.dW, f.lddw, e);
     }
-    *need = w.used;
-    if (w.used > have) return cudaSuccess;  // the caller reports it
     if (count == 2 && P.p[1].nk > P.p[0].nk) {
         std::swap(P.p[0], P.p[1]);
         std::swap(A[0], A[1]);
         std::swap(B[0], B[1]);
     }
-    cudaError_t err = launch_operands(f.dtype, gj, jw, jx, s);
+    int sms = 0;
+    cudaError_t err = device_sms(&sms);
+    if (err != cudaSuccess) return err;
+    const Plans how = plans(grad_extents(f.dtype, f.M, f.N, f.K, f.dx != nullptr, f.dW != nullptr), f.dtype == VF_F32, true, sms);
+    for (int k = 0; k < count; ++k)
+        if (plog_of(how, k) > 0) P.p[k].sums = (float*)w.take((size_t)((P.p[k].I * P.p[k].J) << plog_of(how, k)) * 4);
+    *need = w.used;
+    if (w.used > have) return cudaSuccess;  // the caller reports it
+    err = launch_operands(f.dtype, gj, jw, jx, s);
     if (err != cudaSuccess) return err;
     if (count == 0 && f.db == nullptr) return cudaSuccess;
     P.part = gj.part;
     P.nparts = (int)row_blocks(f.M, f.N);
     P.N = f.N;
     P.db = f.db;
-    return launch_products(f.dtype, P, A, B, count, s);
+    return launch_products(f.dtype, P, A, B, count, how, sms, s);
 }
 
 cudaError_t device_sms(int* sms) {

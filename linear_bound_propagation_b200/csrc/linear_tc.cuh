@@ -28,6 +28,8 @@ struct TcProduct {
     long long ldz;
     int act;
     int vec;             // output, residual and z rows all allow 16-byte accesses (and TMA)
+    int plog;            // k_linear_tc.cu: the reduction is cut into 2^plog parts, each a tile of its own
+    float* sums;         // their fp32 sums, [part][J][I]
 };
 
 // Start of the r-th of 2^log parts of n blocks.

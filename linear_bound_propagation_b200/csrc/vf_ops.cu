@@ -133,7 +133,7 @@ int vf_linear_workspace(int dtype, long long M, int N, int K, int grad, size_t* 
     OPS_TRY(check_kind(dtype, VF_ACT_NONE));
     OPS_TRY(check_sizes(M, N, K));
     if (grad != 0 && linear_few_supported(M, N, K))
-        *bytes = linear_few_workspace(M, N, K);
+        *bytes = linear_few_workspace(dtype, M, N, K);
     else if (use_tc(M, N, K) && (grad != 0 || !linear_direct_fits(dtype, M, N, K)))
         *bytes = linear_tc_workspace(dtype, M, N, K, grad != 0);
     else
