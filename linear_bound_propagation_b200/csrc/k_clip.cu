@@ -189,10 +189,17 @@ clip_scale_k(const __grid_constant__ Table tab, const double* part, int nparts, 
     }
 }
 
+// One sum for the partial sums of many launches, in a fixed order.
+__global__ void __launch_bounds__(THREADS) clip_join_k(double* part, int nparts, double* sum) {
+    double d = 0.0;
+    for (int i = threadIdx.x; i < nparts; i += THREADS) d += part[i];
+    const double s = block_sum(d);
+    if (threadIdx.x == 0) *sum = s;
+}
+
 cudaError_t grid_limit(int* blocks) {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    const cudaError_t e = device_sms(&sms);
     *blocks = sms * BLOCKS_PER_SM;
     return e;
 }
@@ -220,7 +227,7 @@ void fill(const ClipList& l, int* t, Table* tab) {
 
 long long clip_work_doubles(int n, int sms) {
     // a launch ends early only when 2^31 chunks (32 TiB) are reached, so ceil(n / MAX_TENSORS) launches always do
-    return (long long)std::max(1, (n + MAX_TENSORS - 1) / MAX_TENSORS) * sms * BLOCKS_PER_SM;
+    return (long long)std::max(1, (n + MAX_TENSORS - 1) / MAX_TENSORS) * sms * BLOCKS_PER_SM + 1;  // and clip_join_k's
 }
 
 cudaError_t launch_clip(const ClipList& l, float scale, float max_norm, float* norm, double* work, cudaStream_t s) {
@@ -236,6 +243,12 @@ cudaError_t launch_clip(const ClipList& l, float scale, float max_norm, float* n
         clip_norm_k<<<grid, THREADS, 0, s>>>(tab, work + parts);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         parts += grid;
+    }
+    if (parts > limit) {  // every block of the second pass adds the partial sums: not those of many launches
+        clip_join_k<<<1, THREADS, 0, s>>>(work, parts, work + parts);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        work += parts;
+        parts = 1;
     }
     bool wrote = false;
     for (int t = 0; t < l.n || !wrote;) {

@@ -24,6 +24,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cstdlib>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -66,6 +67,7 @@ struct TcParams {
     int workers;         // CTAs, pairs or clusters that walk the tiles
     int split, split_log;  // CTAs per tile (cluster size), a power of two
     int stages;
+    int test_stall;        // tests only: the first CTA never makes its first copies, so that a bounded wait expires
     // column sums of g, joined here: db[n] = sum_q part[q * N + n]
     const float* part;
     int nparts, N;
@@ -367,6 +369,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                     uint32_t bar = smem_u32(&full[g.slot]);
                     if (CG == 1 || pr == 0) mbar_expect_tx(&full[g.slot], STAGE * CG);
                     if (CG == 2) bar = leader_addr(&full[g.slot]);
+                    if (P.test_stall && blockIdx.x == 0 && g.lap == 0 && g.slot == 0) continue;
 #pragma unroll
                     for (int q = 0; q < PL * KS; ++q) {
                         // plane q % PL of block q / PL (one of the two is always one)
@@ -1214,6 +1217,7 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
         P.split *= 2;
         ++P.split_log;
     }
+    P.test_stall = getenv("VF_TEST_OPS_STALL") != nullptr;
     P.workers = (int)std::min<long long>(tiles, P.split > 1 ? tiles : slots / CG);
     if (tiles == 0) P.workers = std::min((P.N + 255) / 256, sms);
     P.gap = 1;

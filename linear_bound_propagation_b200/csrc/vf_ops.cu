@@ -6,7 +6,6 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
-#include <new>
 #include <vector>
 
 #include "vf.h"
@@ -77,14 +76,26 @@ int check_work(size_t have, size_t need) {
 }
 
 int launched(cudaError_t e) {
-    return e == cudaSuccess ? VF_OK : ops_fail(VF_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+    if (e == cudaSuccess) return VF_OK;
+    cudaGetLastError();  // reported here, not by the caller's next check
+    return ops_fail(VF_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+}
+
+// Runs an entry point's body; what the C++ library throws (it can run out of host memory) does not cross the ABI.
+template <typename F>
+int guarded(F body) {
+    try {
+        return body();
+    } catch (...) {
+        return VF_ERR_CUDA;
+    }
 }
 
 int sm_count(int* sms) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-    return e == cudaSuccess ? VF_OK : ops_fail(VF_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
+    const cudaError_t e = device_sms(sms);
+    if (e == cudaSuccess) return VF_OK;
+    cudaGetLastError();
+    return ops_fail(VF_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
 }
 
 struct Range {
@@ -94,29 +105,25 @@ struct Range {
 
 // Every output range is disjoint from every other output and from every input but, exactly, its own.
 int check_overlaps(const ClipList& l) {
-    try {
-        std::vector<Range> outs;
-        outs.reserve(l.n);
-        for (int t = 0; t < l.n; ++t) {
-            const uintptr_t lo = reinterpret_cast<uintptr_t>(l.out[t]);
-            if (l.size[t] > 0) outs.push_back(Range{lo, lo + (uintptr_t)l.size[t] * elem_bytes(l.dtype[t]), t});
-        }
-        std::sort(outs.begin(), outs.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
-        for (size_t i = 1; i < outs.size(); ++i)
-            if (outs[i].lo < outs[i - 1].hi)
-                return ops_fail(VF_ERR_ARG, "outputs %d and %d overlap", outs[i - 1].t, outs[i].t);
-        for (int t = 0; t < l.n; ++t) {
-            if (l.size[t] == 0) continue;
-            const uintptr_t lo = reinterpret_cast<uintptr_t>(l.in[t]);
-            const uintptr_t hi = lo + (uintptr_t)l.size[t] * elem_bytes(l.dtype[t]);
-            // the outputs are disjoint and sorted: the first that ends after lo is the only one to begin looking at
-            auto it = std::upper_bound(outs.begin(), outs.end(), lo, [](uintptr_t v, const Range& r) { return v < r.hi; });
-            for (; it != outs.end() && it->lo < hi; ++it)
-                if (it->t != t || it->lo != lo)
-                    return ops_fail(VF_ERR_ARG, "gradient %d overlaps output %d", t, it->t);
-        }
-    } catch (const std::bad_alloc&) {
-        return ops_fail(VF_ERR_WORKSPACE, "out of host memory");
+    std::vector<Range> outs;
+    outs.reserve(l.n);
+    for (int t = 0; t < l.n; ++t) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(l.out[t]);
+        if (l.size[t] > 0) outs.push_back(Range{lo, lo + (uintptr_t)l.size[t] * elem_bytes(l.dtype[t]), t});
+    }
+    std::sort(outs.begin(), outs.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    for (size_t i = 1; i < outs.size(); ++i)
+        if (outs[i].lo < outs[i - 1].hi)
+            return ops_fail(VF_ERR_ARG, "outputs %d and %d overlap", outs[i - 1].t, outs[i].t);
+    for (int t = 0; t < l.n; ++t) {
+        if (l.size[t] == 0) continue;
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(l.in[t]);
+        const uintptr_t hi = lo + (uintptr_t)l.size[t] * elem_bytes(l.dtype[t]);
+        // the outputs are disjoint and sorted: the first that ends after lo is the only one to begin looking at
+        auto it = std::upper_bound(outs.begin(), outs.end(), lo, [](uintptr_t v, const Range& r) { return v < r.hi; });
+        for (; it != outs.end() && it->lo < hi; ++it)
+            if (it->t != t || it->lo != lo)
+                return ops_fail(VF_ERR_ARG, "gradient %d overlaps output %d", t, it->t);
     }
     return VF_OK;
 }
@@ -129,68 +136,74 @@ bool use_tc(long long M, int N, int K) { return linear_tc_supported(M, N, K) && 
 extern "C" {
 
 int vf_linear_workspace(int dtype, long long M, int N, int K, int grad, size_t* bytes) {
-    if (bytes == nullptr) return ops_fail(VF_ERR_ARG, "NULL pointer");
-    OPS_TRY(check_kind(dtype, VF_ACT_NONE));
-    OPS_TRY(check_sizes(M, N, K));
-    if (grad != 0 && linear_few_supported(M, N, K))
-        *bytes = linear_few_workspace(dtype, M, N, K);
-    else if (use_tc(M, N, K) && (grad != 0 || !linear_direct_fits(dtype, M, N, K)))
-        *bytes = linear_tc_workspace(dtype, M, N, K, grad != 0);
-    else
-        *bytes = 0;
-    return VF_OK;
+    return guarded([&]() -> int {
+        if (bytes == nullptr) return ops_fail(VF_ERR_ARG, "NULL pointer");
+        OPS_TRY(check_kind(dtype, VF_ACT_NONE));
+        OPS_TRY(check_sizes(M, N, K));
+        if (grad != 0 && linear_few_supported(M, N, K))
+            *bytes = linear_few_workspace(dtype, M, N, K);
+        else if (use_tc(M, N, K) && (grad != 0 || !linear_direct_fits(dtype, M, N, K)))
+            *bytes = linear_tc_workspace(dtype, M, N, K, grad != 0);
+        else
+            *bytes = 0;
+        return VF_OK;
+    });
 }
 
 int vf_linear(int dtype, int act, const void* x, long long ldx, const void* W, long long ldw, const void* b,
               const void* r, long long ldr, long long M, int N, int K, void* y, long long ldy, void* z, long long ldz,
               void* work, size_t work_bytes, void* stream) {
-    OPS_TRY(check_kind(dtype, act));
-    OPS_TRY(check_sizes(M, N, K));
-    if (M == 0 || N == 0) return VF_OK;
-    OPS_TRY(check_matrix("x", x, M, K, ldx, dtype));
-    OPS_TRY(check_matrix("W", W, N, K, ldw, dtype));
-    OPS_TRY(check_vector("b", b, dtype));
-    if (r != nullptr) OPS_TRY(check_matrix("r", r, M, N, ldr, dtype));
-    OPS_TRY(check_matrix("y", y, M, N, ldy, dtype));
-    if (z != nullptr) OPS_TRY(check_matrix("z", z, M, N, ldz, dtype));
-    const LinearFwd p{dtype, act, x, ldx, W, ldw, b, r, ldr, M, N, K, y, ldy, z, ldz};
-    if (!use_tc(M, N, K)) return launched(launch_linear_ffma(p, (cudaStream_t)stream));
-    if (!linear_tc_in_place(p) && linear_direct_fits(dtype, M, N, K))
-        return launched(launch_linear_direct(p, (cudaStream_t)stream));
-    OPS_TRY(check_aligned(work));
-    size_t need = 0;
-    const size_t have = work == nullptr ? 0 : work_bytes;
-    OPS_TRY(launched(launch_linear_tc(p, work, have, &need, (cudaStream_t)stream)));
-    return check_work(have, need);
+    return guarded([&]() -> int {
+        OPS_TRY(check_kind(dtype, act));
+        OPS_TRY(check_sizes(M, N, K));
+        if (M == 0 || N == 0) return VF_OK;
+        OPS_TRY(check_matrix("x", x, M, K, ldx, dtype));
+        OPS_TRY(check_matrix("W", W, N, K, ldw, dtype));
+        OPS_TRY(check_vector("b", b, dtype));
+        if (r != nullptr) OPS_TRY(check_matrix("r", r, M, N, ldr, dtype));
+        OPS_TRY(check_matrix("y", y, M, N, ldy, dtype));
+        if (z != nullptr) OPS_TRY(check_matrix("z", z, M, N, ldz, dtype));
+        const LinearFwd p{dtype, act, x, ldx, W, ldw, b, r, ldr, M, N, K, y, ldy, z, ldz};
+        if (!use_tc(M, N, K)) return launched(launch_linear_ffma(p, (cudaStream_t)stream));
+        if (!linear_tc_in_place(p) && linear_direct_fits(dtype, M, N, K))
+            return launched(launch_linear_direct(p, (cudaStream_t)stream));
+        OPS_TRY(check_aligned(work));
+        size_t need = 0;
+        const size_t have = work == nullptr ? 0 : work_bytes;
+        OPS_TRY(launched(launch_linear_tc(p, work, have, &need, (cudaStream_t)stream)));
+        return check_work(have, need);
+    });
 }
 
 int vf_linear_grad(int dtype, int act, const void* dy, long long lddy, const void* z, long long ldz, const void* x,
                    long long ldx, const void* W, long long ldw, long long M, int N, int K, void* dx, long long lddx,
                    void* dW, long long lddw, void* db, void* dr, long long lddr, void* work, size_t work_bytes,
                    void* stream) {
-    OPS_TRY(check_kind(dtype, act));
-    OPS_TRY(check_sizes(M, N, K));
-    OPS_TRY(check_matrix("dy", dy, M, N, lddy, dtype));
-    if (act != VF_ACT_NONE) OPS_TRY(check_matrix("z", z, M, N, ldz, dtype));
-    if (dx != nullptr) {
-        OPS_TRY(check_matrix("W", W, N, K, ldw, dtype));
-        OPS_TRY(check_matrix("dx", dx, M, K, lddx, dtype));
-    }
-    if (dW != nullptr) {
-        OPS_TRY(check_matrix("x", x, M, K, ldx, dtype));
-        OPS_TRY(check_matrix("dW", dW, N, K, lddw, dtype));
-    }
-    OPS_TRY(check_vector("db", db, dtype));
-    if (dr != nullptr) OPS_TRY(check_matrix("dr", dr, M, N, lddr, dtype));
-    const LinearGrad p{dtype, act, dy, lddy, z, ldz, x, ldx, W, ldw, M, N, K, dx, lddx, dW, lddw, db, dr, lddr};
-    const bool few = linear_few_supported(M, N, K);
-    if (!few && !use_tc(M, N, K)) return launched(launch_linear_grad_ffma(p, (cudaStream_t)stream));
-    OPS_TRY(check_aligned(work));
-    size_t need = 0;
-    const size_t have = work == nullptr ? 0 : work_bytes;
-    OPS_TRY(launched(few ? launch_linear_few_grad(p, work, have, &need, (cudaStream_t)stream)
-                         : launch_linear_grad_tc(p, work, have, &need, (cudaStream_t)stream)));
-    return check_work(have, need);
+    return guarded([&]() -> int {
+        OPS_TRY(check_kind(dtype, act));
+        OPS_TRY(check_sizes(M, N, K));
+        OPS_TRY(check_matrix("dy", dy, M, N, lddy, dtype));
+        if (act != VF_ACT_NONE) OPS_TRY(check_matrix("z", z, M, N, ldz, dtype));
+        if (dx != nullptr) {
+            OPS_TRY(check_matrix("W", W, N, K, ldw, dtype));
+            OPS_TRY(check_matrix("dx", dx, M, K, lddx, dtype));
+        }
+        if (dW != nullptr) {
+            OPS_TRY(check_matrix("x", x, M, K, ldx, dtype));
+            OPS_TRY(check_matrix("dW", dW, N, K, lddw, dtype));
+        }
+        OPS_TRY(check_vector("db", db, dtype));
+        if (dr != nullptr) OPS_TRY(check_matrix("dr", dr, M, N, lddr, dtype));
+        const LinearGrad p{dtype, act, dy, lddy, z, ldz, x, ldx, W, ldw, M, N, K, dx, lddx, dW, lddw, db, dr, lddr};
+        const bool few = linear_few_supported(M, N, K);
+        if (!few && !use_tc(M, N, K)) return launched(launch_linear_grad_ffma(p, (cudaStream_t)stream));
+        OPS_TRY(check_aligned(work));
+        size_t need = 0;
+        const size_t have = work == nullptr ? 0 : work_bytes;
+        OPS_TRY(launched(few ? launch_linear_few_grad(p, work, have, &need, (cudaStream_t)stream)
+                             : launch_linear_grad_tc(p, work, have, &need, (cudaStream_t)stream)));
+        return check_work(have, need);
+    });
 }
 
 int vf_ops_check(void) {
@@ -213,26 +226,28 @@ int vf_clip_workspace(int n, size_t* bytes) {
 
 int vf_clip_grad_norm(int n, const void* const* grads, void* const* outs, const long long* sizes, const int* dtypes,
                       float scale, float max_norm, float* norm, void* work, size_t work_bytes, void* stream) {
-    if (n < 0) return ops_fail(VF_ERR_ARG, "negative number of gradients");
-    if (norm == nullptr || (n > 0 && (!grads || !outs || !sizes || !dtypes))) return ops_fail(VF_ERR_ARG, "NULL pointer");
-    if (!std::isfinite(scale) || scale < 0.f) return ops_fail(VF_ERR_NONFINITE, "scale must be finite and >= 0");
-    if (std::isnan(max_norm) || max_norm < 0.f) return ops_fail(VF_ERR_ARG, "max_norm must be >= 0");
-    const ClipList l{n, grads, outs, sizes, dtypes};
-    long long bytes = 0;
-    for (int t = 0; t < n; ++t) {
-        OPS_TRY(check_kind(dtypes[t], VF_ACT_NONE));
-        if (sizes[t] < 0 || sizes[t] > (1LL << 42)) return ops_fail(VF_ERR_ARG, "gradient %d has %lld elements", t, sizes[t]);
-        OPS_TRY(check_matrix("gradient", grads[t], 1, sizes[t], sizes[t], dtypes[t]));
-        OPS_TRY(check_matrix("output", outs[t], 1, sizes[t], sizes[t], dtypes[t]));
-        bytes += sizes[t] * elem_bytes(dtypes[t]);
-        if (bytes > (1LL << 44)) return ops_fail(VF_ERR_UNSUPPORTED, "gradients of over 16 TiB");
-    }
-    OPS_TRY(check_overlaps(l));
-    size_t need = 0;
-    OPS_TRY(vf_clip_workspace(n, &need));
-    OPS_TRY(check_aligned(work));
-    OPS_TRY(check_work(work == nullptr ? 0 : work_bytes, need));
-    return launched(launch_clip(l, scale, max_norm, norm, (double*)work, (cudaStream_t)stream));
+    return guarded([&]() -> int {
+        if (n < 0) return ops_fail(VF_ERR_ARG, "negative number of gradients");
+        if (norm == nullptr || (n > 0 && (!grads || !outs || !sizes || !dtypes))) return ops_fail(VF_ERR_ARG, "NULL pointer");
+        if (!std::isfinite(scale) || scale < 0.f) return ops_fail(VF_ERR_NONFINITE, "scale must be finite and >= 0");
+        if (std::isnan(max_norm) || max_norm < 0.f) return ops_fail(VF_ERR_ARG, "max_norm must be >= 0");
+        const ClipList l{n, grads, outs, sizes, dtypes};
+        long long bytes = 0;
+        for (int t = 0; t < n; ++t) {
+            OPS_TRY(check_kind(dtypes[t], VF_ACT_NONE));
+            if (sizes[t] < 0 || sizes[t] > (1LL << 42)) return ops_fail(VF_ERR_ARG, "gradient %d has %lld elements", t, sizes[t]);
+            OPS_TRY(check_matrix("gradient", grads[t], 1, sizes[t], sizes[t], dtypes[t]));
+            OPS_TRY(check_matrix("output", outs[t], 1, sizes[t], sizes[t], dtypes[t]));
+            bytes += sizes[t] * elem_bytes(dtypes[t]);
+            if (bytes > (1LL << 44)) return ops_fail(VF_ERR_UNSUPPORTED, "gradients of over 16 TiB");
+        }
+        OPS_TRY(check_overlaps(l));
+        size_t need = 0;
+        OPS_TRY(vf_clip_workspace(n, &need));
+        OPS_TRY(check_aligned(work));
+        OPS_TRY(check_work(work == nullptr ? 0 : work_bytes, need));
+        return launched(launch_clip(l, scale, max_norm, norm, (double*)work, (cudaStream_t)stream));
+    });
 }
 
 }  // extern "C"

@@ -12,6 +12,9 @@ Tolerances are worst-case sums of the roundings each output passes (u = 2^-24):
 * the output's own rounding: half a step, eps / 2 relative, plus half a subnormal step for float16.
 """
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -173,6 +176,130 @@ def test_many_large_tiles(dtype, M, N, K):
     got = vf.linear_grad(r, x, W)
     assert torch.equal(got["dx"], (r.double() @ W.double()).to(dtype))
     assert torch.equal(got["dW"], (r.double().t() @ x.double()).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K", [(5557, 64, 64), (8000, 10, 200), (3000, 300, 40), (64, 5000, 24), (24, 40, 6000),
+                                   (6, 3000, 520), (8, 33, 1027)])
+def test_unequal_products_of_the_backward_pass(dtype, M, N, K):
+    """Long reductions behind few tiles, few rows, and one product much larger than the other: exact on whole numbers
+    (every sum stays below 2^24), and within the roundings with an activation."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    x, W, r, dy = (torch.randint(-2, 3, s, generator=gen, device="cuda").to(dtype) for s in ((M, K), (N, K), (M, N), (M, N)))
+    g = dy.double() * (r.double() > 0)
+    want = {"dx": g @ W.double(), "dW": g.t() @ x.double(), "db": g.sum(0), "dr": g}
+    for need in (("dx", "dW", "db", "dr"), ("dx",), ("dW",), ("dW", "db"), ("dx", "dr")):
+        got = vf.linear_grad(dy, x, W, act="relu", z=r, need=need)
+        for k in need:
+            assert torch.equal(got[k], want[k].to(dtype)), (need, k)
+    check_grad(dtype, M, N, K, "gelu", 0, 0, 7)
+    check_grad(dtype, M, N, K, "silu", 3, 1, 8)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K", [(4096, 1016, 256), (2050, 264, 72), (700, 1030, 64), (16, 640, 2048)])
+def test_in_place_over_the_residual(dtype, M, N, K):
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x, W, r = randn(gen, M, K, dtype), randn(gen, N, K, dtype, K ** -0.5), randn(gen, M, N, dtype)
+    want = vf.linear(x, W, residual=r, act="gelu")["y"]
+    for _ in range(2):
+        buf = r.clone()
+        assert vf.linear(x, W, residual=buf, act="gelu", out=buf)["y"] is buf
+        assert torch.equal(buf, want)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows of x, y and z whose elements lie more than 2^31 apart, forward and backward, against sampled rows."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    M, N, K = 33000, 24, 66000
+    x = torch.empty(M, K, device="cuda", dtype=torch.bfloat16)
+    for i in range(0, M, 3000):
+        x[i:i + 3000] = torch.randn(3000, K, generator=gen, device="cuda")[:x[i:i + 3000].shape[0]].bfloat16()
+    W = randn(gen, N, K, torch.bfloat16, K ** -0.5)
+    rows = torch.tensor([0, 1, 2048, 32766, M - 1], device="cuda")
+    y = vf.linear(x, W)["y"]
+    z, S = x[rows].double() @ W.double().t(), x[rows].double().abs() @ W.double().abs().t()
+    ez = acc_tol(K) * S
+    assert worst(y[rows], z, ez + 2.0 ** -8 * (z.abs() + ez)) <= 1.0
+    dy = randn(gen, M, N, torch.bfloat16)
+    g = vf.linear_grad(dy, x, W, need=("dx", "dW"))
+    dx, S = dy[rows].double() @ W.double(), dy[rows].double().abs() @ W.double().abs()
+    ex = acc_tol(N) * S
+    assert worst(g["dx"][rows], dx, ex + 2.0 ** -8 * (dx.abs() + ex)) <= 1.0
+    cols = torch.tensor([0, 40000, K - 1], device="cuda")
+    dW, S = dy.double().t() @ x[:, cols].double(), dy.double().abs().t() @ x[:, cols].double().abs()
+    ew = acc_tol(M) * S
+    assert worst(g["dW"][:, cols], dW, ew + 2.0 ** -8 * (dW.abs() + ew)) <= 1.0
+    vf.ops_check()
+    del dx, dW, S, z, g, y, dy
+    flat = x.view(-1)[:2 ** 31 + 4099]
+    flat[2 ** 31 + 7] = 3000.0
+    want = math.sqrt(sum(float((c.double() ** 2).sum()) for c in torch.split(flat, 1 << 27)))
+    norm, _ = vf.clip_grad_norm([flat], float("inf"))
+    assert abs(float(norm) - want) <= 18 * U * want
+    vf.clip_grad_norm([flat], want / 2)
+    assert abs(float(flat[2 ** 31 + 7]) - 1500.0) <= 1500.0 * 2.0 ** -8
+
+
+def test_workspace_is_checked_before_anything_runs():
+    x, W = torch.ones(300, 200, device="cuda"), torch.ones(400, 200, device="cuda")
+    y = torch.full((300, 400), 7.0, device="cuda")
+    L = vf.lib()
+    args = (0, 0, x.data_ptr(), 200, W.data_ptr(), 200, None, None, 0)
+    buf = torch.empty(1 << 20, device="cuda", dtype=torch.uint8)
+    dW, dy = torch.full((4000, 200), 7.0, device="cuda"), torch.ones(3000, 4000, device="cuda")
+    xl = torch.ones(3000, 200, device="cuda")
+    for work, nbytes, code in ((None, 0, vf.VF_ERR_WORKSPACE), (buf.data_ptr(), 1 << 20, vf.VF_ERR_WORKSPACE),
+                               (buf.data_ptr() + 8, 1 << 19, vf.VF_ERR_ARG)):
+        assert L.vf_linear_grad(0, 0, dy.data_ptr(), 4000, None, 0, xl.data_ptr(), 200, None, 0, 3000, 4000, 200, None, 0,
+                                dW.data_ptr(), 200, None, None, 0, work, nbytes, None) == code
+    assert L.vf_linear(*args, 300, 400, 200, y.data_ptr(), 400, None, 0, None, 0, None) in (vf.VF_OK, vf.VF_ERR_WORKSPACE)
+    torch.cuda.synchronize()
+    assert (dW == 7.0).all()
+
+
+def test_a_wait_that_runs_out_is_reported(monkeypatch):
+    """Host-set hook: the first CTA never makes its first copies, so its bounded waits expire; the call returns, the
+    check reports it once, and later calls are right. One CTA per tile, and a pair of CTAs."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    for M, N, K in ((64, 128, 256), (4096, 1024, 256)):
+        x, W = randn(gen, M, K, torch.bfloat16), randn(gen, N, K, torch.bfloat16)
+        want = vf.linear(x, W)["y"].clone()
+        vf.ops_check()
+        monkeypatch.setenv("VF_TEST_OPS_STALL", "1")
+        vf.linear(x, W)
+        monkeypatch.delenv("VF_TEST_OPS_STALL")
+        with pytest.raises(vf.VfError) as e:
+            vf.ops_check()
+        assert e.value.code == vf.VF_ERR_TIMEOUT
+        vf.ops_check()
+        assert torch.equal(vf.linear(x, W)["y"], want)
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    code = """
+import torch
+from linear_bound_propagation_b200 import vf
+x, W = torch.ones(512, 256, device="cuda"), torch.ones(384, 256, device="cuda")
+xb, Wb = x.bfloat16(), W.bfloat16()
+few = torch.ones(3, 256, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    outs = [vf.linear(x, W)["y"], vf.linear(xb, Wb, act="relu")["y"], vf.linear(x[:, 1:], W[:, 1:])["y"]]
+    d = vf.linear_grad(torch.ones_like(outs[0]), x, W)
+    f = vf.linear_grad(torch.ones(3, 384, device="cuda"), few, W)
+    norm, c = vf.clip_grad_norm([d["dW"]], 1.0, out=[torch.empty_like(d["dW"])])
+g.replay()
+torch.cuda.synchronize()
+assert (outs[0] == 256).all() and (outs[1] == 256).all() and (outs[2] == 255).all()
+assert (d["dx"] == 384).all() and (d["dW"] == 512).all() and (f["dx"] == 384).all() and (f["dW"] == 3).all()
+assert abs(float(norm) - 512 * (384 * 256) ** 0.5) < 1
+vf.ops_check()
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -359,6 +486,14 @@ def test_clip_matches_formula(dtype, sizes):
             out = [o if o.numel() == g.numel() else torch.empty_like(g) for o, g in zip(out, grads)]
             clip_check(grads, max_norm, scale, out)
         clip_check([randn(gen, 1, n, dtype)[0] for n in sizes], max_norm, scale, None, in_place=True)
+
+
+def test_clip_of_many_large_gradients():
+    """More gradients than one launch takes, each launch with a full grid: the partial sums are added apart."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    flat = torch.randn(250 * 60000, generator=gen, device="cuda")
+    grads = list(torch.split(flat, 60000))
+    clip_check(grads, 10.0, 1.0, [torch.empty_like(g) for g in grads])
 
 
 def test_clip_of_mixed_types_and_shapes():
