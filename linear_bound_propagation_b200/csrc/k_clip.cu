@@ -7,7 +7,7 @@
 // device and a captured launch keeps its own table. Pass 1 leaves one partial sum per block, pass 2 adds them in a
 // fixed order in every block: no atomics, the same bits on every run.
 //
-// Squares are added in fp32 over one thread's 64 bytes (at most 32 terms) and in fp64 beyond that. Where such a
+// Squares are added in fp32 over one thread's 32 bytes (at most 16 terms) and in fp64 beyond that. Where such a
 // partial sum leaves the range in which fp32 squares are exact enough (overflow above 1e19, underflow below 1e-15 per
 // element), that thread's elements are squared again in fp64, so norms of any finite fp32 or bf16 values come out.
 #include <algorithm>
@@ -21,8 +21,7 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int MAX_TENSORS = 100;            // 3.2 KB of the 4 KB parameter space
-constexpr int CHUNK_BYTES = THREADS * 64;   // one block iteration: four 16-byte loads per thread
-constexpr int BLOCKS_PER_SM = 8;
+constexpr int BLOCKS_PER_SM = 8;            // of the first pass
 
 struct Table {
     const void* in[MAX_TENSORS];
@@ -33,14 +32,27 @@ struct Table {
     int n;
 };
 
-__host__ __device__ __forceinline__ int chunk_elems(int dtype) { return CHUNK_BYTES / (dtype == VF_F32 ? 4 : 2); }
+// A chunk is what a block takes at a time: V 16-byte loads per thread.
+__host__ __device__ __forceinline__ int chunk_elems(int dtype, int V) { return THREADS * 16 * V / (dtype == VF_F32 ? 4 : 2); }
+// The tensor that chunk c belongs to.
+__device__ __forceinline__ int tensor_of(const Table& tab, int c) {
+    int lo = 0, hi = tab.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (c >= tab.first[mid])
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
 
 template <typename T, int N>
 struct alignas(16) Vec {
     T v[N];
 };
 
-// Sum of squares of n <= 32 values, see the header.
+// Sum of squares of n <= 16 values, see the header.
 template <typename T>
 __device__ __forceinline__ double squares(const T* v, int n) {
     float s = 0.f;
@@ -61,19 +73,8 @@ __device__ __forceinline__ double squares(const T* v, int n) {
     return (double)s;
 }
 
-// Accesses that should not push out of L2 what is still to be read from it.
-template <typename V>
-__device__ __forceinline__ V load_once(const V* p) {
-    const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p));
-    return *reinterpret_cast<const V*>(&q);
-}
-template <typename V>
-__device__ __forceinline__ void store_out(V* p, const V& v) {
-    __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&v));
-}
-
 // One chunk of a tensor: elements [e0, e1). `head` elements come before the first 16-byte boundary.
-template <typename T>
+template <typename T, int V>
 __device__ __forceinline__ double chunk_squares(const T* __restrict__ p, long long e0, long long e1) {
     constexpr int N = 16 / sizeof(T);
     const T* q = p + e0;
@@ -82,11 +83,17 @@ __device__ __forceinline__ double chunk_squares(const T* __restrict__ p, long lo
     const int nv = (len - head) / N;
     const Vec<T, N>* b = reinterpret_cast<const Vec<T, N>*>(q + head);
     double d = 0.0;
-    if (nv == 4 * THREADS) {
-        T v[4 * N];
+    if (nv == V * THREADS) {
+        Vec<T, N> v[V];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) *reinterpret_cast<Vec<T, N>*>(v + u * N) = b[threadIdx.x + u * THREADS];
-        d = squares(v, 4 * N);
+        for (int u = 0; u < V; ++u) v[u] = b[threadIdx.x + u * THREADS];
+#pragma unroll
+        for (int u = 0; u < V; u += 2) {  // two vectors at a time in fp32
+            T w[2 * N];
+            *reinterpret_cast<Vec<T, N>*>(w) = v[u];
+            *reinterpret_cast<Vec<T, N>*>(w + N) = v[u + 1];
+            d += squares(w, 2 * N);
+        }
     } else {
         for (int i = threadIdx.x; i < nv; i += THREADS) {
             const Vec<T, N> w = b[i];
@@ -111,24 +118,25 @@ __device__ __forceinline__ double block_sum(double d) {
     return t;
 }
 
+template <int V>
 __global__ void __launch_bounds__(THREADS) clip_norm_k(const __grid_constant__ Table tab, double* part) {
     double d = 0.0;
     int t = 0;
     for (int c = blockIdx.x; c < tab.first[tab.n]; c += gridDim.x) {
         while (c >= tab.first[t + 1]) ++t;
-        const long long e = chunk_elems(tab.dtype[t]);
+        const long long e = chunk_elems(tab.dtype[t], V);
         const long long e0 = (c - tab.first[t]) * e, e1 = min(tab.size[t], e0 + e);
         switch (tab.dtype[t]) {
-            case VF_F32: d += chunk_squares((const float*)tab.in[t], e0, e1); break;
-            case VF_BF16: d += chunk_squares((const __nv_bfloat16*)tab.in[t], e0, e1); break;
-            default: d += chunk_squares((const __half*)tab.in[t], e0, e1); break;
+            case VF_F32: d += chunk_squares<float, V>((const float*)tab.in[t], e0, e1); break;
+            case VF_BF16: d += chunk_squares<__nv_bfloat16, V>((const __nv_bfloat16*)tab.in[t], e0, e1); break;
+            default: d += chunk_squares<__half, V>((const __half*)tab.in[t], e0, e1); break;
         }
     }
     const double s = block_sum(d);
     if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-template <typename T>
+template <typename T, int V>
 __device__ __forceinline__ void chunk_scale(const T* p, T* out, long long e0, long long e1, float f) {
     constexpr int N = 16 / sizeof(T);
     const T* q = p + e0;
@@ -142,15 +150,15 @@ __device__ __forceinline__ void chunk_scale(const T* p, T* out, long long e0, lo
     const int nv = (len - head) / N;
     const Vec<T, N>* b = reinterpret_cast<const Vec<T, N>*>(q + head);
     Vec<T, N>* ob = reinterpret_cast<Vec<T, N>*>(o + head);
-    if (nv == 4 * THREADS) {
-        Vec<T, N> v[4];
+    if (nv == V * THREADS) {
+        Vec<T, N> v[V];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = load_once(b + threadIdx.x + u * THREADS);
+        for (int u = 0; u < V; ++u) v[u] = b[threadIdx.x + u * THREADS];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < V; ++u) {
 #pragma unroll
             for (int i = 0; i < N; ++i) v[u].v[i] = from_f32<T>(to_f32(v[u].v[i]) * f);
-            store_out(ob + threadIdx.x + u * THREADS, v[u]);
+            ob[threadIdx.x + u * THREADS] = v[u];
         }
     } else {
         for (int i = threadIdx.x; i < nv; i += THREADS) {
@@ -165,6 +173,7 @@ __device__ __forceinline__ void chunk_scale(const T* p, T* out, long long e0, lo
     if (tail < len) o[tail] = from_f32<T>(to_f32(q[tail]) * f);
 }
 
+template <int V>
 __global__ void __launch_bounds__(THREADS)
 clip_scale_k(const __grid_constant__ Table tab, const double* part, int nparts, float scale, float max_norm, float* norm,
              int write_norm) {
@@ -174,22 +183,25 @@ clip_scale_k(const __grid_constant__ Table tab, const double* part, int nparts, 
     if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
     const bool clip = n > (double)max_norm && !isinf(n);  // NaN compares false
     const float f = (float)(clip ? (double)scale * ((double)max_norm / n) : (double)scale);
+    if (tab.n == 0) return;
     // backwards: what the norm's pass read last is still in L2
-    int t = tab.n - 1;
-    for (int c = tab.first[tab.n] - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
+    int c = tab.first[tab.n] - 1 - (int)blockIdx.x;
+    for (int t = c < 0 ? 0 : tensor_of(tab, c); c >= 0; c -= gridDim.x) {
         while (c < tab.first[t]) --t;
         if (tab.in[t] == tab.out[t] && f == 1.f) continue;
-        const long long e = chunk_elems(tab.dtype[t]);
+        const long long e = chunk_elems(tab.dtype[t], V);
         const long long e0 = (c - tab.first[t]) * e, e1 = min(tab.size[t], e0 + e);
         switch (tab.dtype[t]) {
-            case VF_F32: chunk_scale((const float*)tab.in[t], (float*)tab.out[t], e0, e1, f); break;
-            case VF_BF16: chunk_scale((const __nv_bfloat16*)tab.in[t], (__nv_bfloat16*)tab.out[t], e0, e1, f); break;
-            default: chunk_scale((const __half*)tab.in[t], (__half*)tab.out[t], e0, e1, f); break;
+            case VF_F32: chunk_scale<float, V>((const float*)tab.in[t], (float*)tab.out[t], e0, e1, f); break;
+            case VF_BF16:
+                chunk_scale<__nv_bfloat16, V>((const __nv_bfloat16*)tab.in[t], (__nv_bfloat16*)tab.out[t], e0, e1, f);
+                break;
+            default: chunk_scale<__half, V>((const __half*)tab.in[t], (__half*)tab.out[t], e0, e1, f); break;
         }
     }
 }
 
-// One sum for the partial sums of many launches, in a fixed order.
+// One sum for many partial sums, in a fixed order.
 __global__ void __launch_bounds__(THREADS) clip_join_k(double* part, int nparts, double* sum) {
     double d = 0.0;
     for (int i = threadIdx.x; i < nparts; i += THREADS) d += part[i];
@@ -205,13 +217,13 @@ cudaError_t grid_limit(int* blocks) {
 }
 
 // Fills `tab` with tensors from index *t on, as many as fit; advances *t.
-void fill(const ClipList& l, int* t, Table* tab) {
+void fill(const ClipList& l, int* t, Table* tab, int V) {
     tab->n = 0;
     tab->first[0] = 0;
     for (; *t < l.n && tab->n < MAX_TENSORS; ++*t) {
         if (l.size[*t] == 0) continue;
         const int k = tab->n;
-        const long long e = chunk_elems(l.dtype[*t]);
+        const long long e = chunk_elems(l.dtype[*t], V);
         const long long chunks = (l.size[*t] + e - 1) / e;
         if (tab->first[k] + chunks > 0x7fffffffLL) break;  // chunk numbers stay ints; the next launch takes it
         tab->in[k] = l.in[*t];
@@ -234,13 +246,21 @@ cudaError_t launch_clip(const ClipList& l, float scale, float max_norm, float* n
     int limit = 0;
     cudaError_t e = grid_limit(&limit);
     if (e != cudaSuccess) return e;
+    long long bytes = 0;
+    for (int t = 0; t < l.n; ++t) bytes += l.size[t] * (l.dtype[t] == VF_F32 ? 4 : 2);
+    // First pass: a fixed number of blocks, each with a partial sum. Eight loads in flight per thread pay where the list
+    // is long (560 MB: 92 us against 98 us with four), four leave more blocks to a short one.
+    const int V = bytes >= (64LL << 20) ? 8 : 4;
     Table tab;
     int parts = 0;
     for (int t = 0; t < l.n;) {
-        fill(l, &t, &tab);
+        fill(l, &t, &tab, V);
         if (tab.n == 0) continue;
         const int grid = std::min(tab.first[tab.n], limit);
-        clip_norm_k<<<grid, THREADS, 0, s>>>(tab, work + parts);
+        if (V == 8)
+            clip_norm_k<8><<<grid, THREADS, 0, s>>>(tab, work + parts);
+        else
+            clip_norm_k<4><<<grid, THREADS, 0, s>>>(tab, work + parts);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         parts += grid;
     }
@@ -250,12 +270,18 @@ cudaError_t launch_clip(const ClipList& l, float scale, float max_norm, float* n
         work += parts;
         parts = 1;
     }
+    // Second pass: 32 blocks per SM, four times what is resident. Blocks that come and go spread reads and writes better
+    // (560 MB read and written: 173 us, with eight blocks per SM 188 us); one per chunk would cost 30 us in blocks alone
+    // where nothing is left to write.
     bool wrote = false;
     for (int t = 0; t < l.n || !wrote;) {
-        fill(l, &t, &tab);
+        fill(l, &t, &tab, V);
         if (tab.n == 0 && wrote) continue;
-        clip_scale_k<<<std::max(1, std::min(tab.first[tab.n], limit)), THREADS, 0, s>>>(tab, work, parts, scale, max_norm,
-                                                                                       norm, wrote ? 0 : 1);
+        const int grid = std::max(1, std::min(tab.first[tab.n], 4 * limit));
+        if (V == 8)
+            clip_scale_k<8><<<grid, THREADS, 0, s>>>(tab, work, parts, scale, max_norm, norm, wrote ? 0 : 1);
+        else
+            clip_scale_k<4><<<grid, THREADS, 0, s>>>(tab, work, parts, scale, max_norm, norm, wrote ? 0 : 1);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         wrote = true;
     }
