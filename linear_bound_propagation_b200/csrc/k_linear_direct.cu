@@ -135,7 +135,7 @@ constexpr int direct_stage() {
     return PL * (BM + BN) * 128;
 }
 
-template <typename T, int PL, int BN, bool VEC>
+template <typename T, int PL, int BN, bool VA, bool VB>
 __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_constant__ DirectParams P) {
     constexpr int A_PLANE = BM * 128, B_PLANE = BN * 128;
     constexpr int STAGE = direct_stage<PL, BN>();
@@ -220,8 +220,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_const
             }
         }
     } else {
-        Loader<T, NA, BM, VEC> a(P.a, i0, kb0);
-        Loader<T, NBC, BN, VEC> b(P.b, j0, kb0);
+        Loader<T, NA, BM, VA> a(P.a, i0, kb0);
+        Loader<T, NBC, BN, VB> b(P.b, j0, kb0);
         Ring g;
         bool ok = true;
         auto stage = [&](int kb, int h) {
@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_const
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             uint8_t* st = base + (size_t)g.slot * STAGE;
-            store_block<T, PL, NA, BM, VEC>(st, A_PLANE, a.h[h]);
-            store_block<T, PL, NBC, BN, VEC>(st + PL * A_PLANE, B_PLANE, b.h[h]);
+            store_block<T, PL, NA, BM, VA>(st, A_PLANE, a.h[h]);
+            store_block<T, PL, NBC, BN, VB>(st + PL * A_PLANE, B_PLANE, b.h[h]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[g.slot]);
@@ -327,13 +327,13 @@ int split_log(long long tiles, int nk, bool f32, int sms) {
     return best;
 }
 
-template <typename T, int PL, int BN, bool VEC>
+template <typename T, int PL, int BN, bool VA, bool VB>
 cudaError_t launch_bn(DirectParams& P, int sms, cudaStream_t s) {
     TcProduct& p = P.p;
     p.nk = blocks_of(P.Tn);
     p.tiles_i = (int)((p.I + BM - 1) / BM);
     p.tiles = (int)(p.tiles_i * ((p.J + BN - 1) / BN));
-    auto kern = linear_direct_k<T, PL, BN, VEC>;
+    auto kern = linear_direct_k<T, PL, BN, VA, VB>;
     cudaError_t e = allow_dyn_smem((const void*)kern, SMEM_LIMIT);
     if (e != cudaSuccess) return e;
     const int need = direct_stage<PL, BN>();
@@ -355,16 +355,26 @@ cudaError_t launch_bn(DirectParams& P, int sms, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kern, P);
 }
 
-template <typename T, int PL, bool VEC>
+template <typename T, int PL, bool VA, bool VB>
 cudaError_t launch_pl(DirectParams& P, cudaStream_t s) {
     int sms = 0;
     cudaError_t e = device_sms(&sms);
     if (e != cudaSuccess) return e;
     switch (columns(P.p.J)) {
-        case 16: return launch_bn<T, PL, 16, VEC>(P, sms, s);
-        case 32: return launch_bn<T, PL, 32, VEC>(P, sms, s);
-        default: return launch_bn<T, PL, 64, VEC>(P, sms, s);
+        case 16: return launch_bn<T, PL, 16, VA, VB>(P, sms, s);
+        case 32: return launch_bn<T, PL, 32, VA, VB>(P, sms, s);
+        default: return launch_bn<T, PL, 64, VA, VB>(P, sms, s);
     }
+}
+
+template <typename T, int PL>
+cudaError_t launch_vec(DirectParams& P, bool va, bool vb, cudaStream_t s) {
+    // both: fp32 only, 16-bit rows of 16-byte alignment are read by TMA in place (k_linear_tc.cu)
+    if constexpr (PL == 3)
+        if (va && vb) return launch_pl<T, PL, true, true>(P, s);
+    if (va && !vb) return launch_pl<T, PL, true, false>(P, s);
+    if (vb && !va) return launch_pl<T, PL, false, true>(P, s);
+    return launch_pl<T, PL, false, false>(P, s);
 }
 
 int elem(int dtype) { return dtype == VF_F32 ? 4 : 2; }
@@ -372,12 +382,14 @@ bool aligned(const void* p, long long ld, int e) { return (reinterpret_cast<uint
 
 }  // namespace
 
-// Every tile has an SM to itself, and fp32 sums can be cut into parts of MAX_CHUNK blocks.
+// Every tile has an SM to itself: fp32 with the reduction cut into parts of MAX_CHUNK blocks, which are up to eight.
 bool linear_direct_fits(int dtype, long long M, int N, int K) {
-    int sms = 0;
+    int sms = 0, parts = 1;
     if (device_sms(&sms) != cudaSuccess) return false;
+    if (dtype == VF_F32)
+        while (parts * MAX_CHUNK < blocks_of(K)) parts *= 2;
     const int bn = columns(M);
-    return ((long long)N + BM - 1) / BM * ((M + bn - 1) / bn) <= sms && (dtype != VF_F32 || blocks_of(K) <= MAX_CHUNK * 8);
+    return parts <= 8 && ((long long)N + BM - 1) / BM * ((M + bn - 1) / bn) * parts <= sms;
 }
 
 cudaError_t launch_linear_direct(const LinearFwd& f, cudaStream_t s) {
@@ -399,12 +411,11 @@ cudaError_t launch_linear_direct(const LinearFwd& f, cudaStream_t s) {
     p.act = f.act;
     p.vec = aligned(f.y, f.ldy, e) && (f.r == nullptr || aligned(f.r, f.ldr, e)) &&
             (f.z == nullptr || aligned(f.z, f.ldz, e));
-    const bool vec = aligned(f.x, f.ldx, e) && aligned(f.W, f.ldw, e);
+    const bool va = aligned(f.W, f.ldw, e), vb = aligned(f.x, f.ldx, e);
     switch (f.dtype) {
-        case VF_F32: return vec ? launch_pl<float, 3, true>(P, s) : launch_pl<float, 3, false>(P, s);
-        // 16-bit rows of 16-byte alignment are read by TMA in place (k_linear_tc.cu)
-        case VF_BF16: return launch_pl<__nv_bfloat16, 1, false>(P, s);
-        default: return launch_pl<__half, 1, false>(P, s);
+        case VF_F32: return launch_vec<float, 3>(P, va, vb, s);
+        case VF_BF16: return launch_vec<__nv_bfloat16, 1>(P, va, vb, s);
+        default: return launch_vec<__half, 1>(P, va, vb, s);
     }
 }
 

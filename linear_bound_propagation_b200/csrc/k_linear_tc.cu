@@ -44,16 +44,18 @@ using namespace lin;
 
 __device__ int g_ops_timeout;
 
-// Epilogue warps: 16 behind the 256-column tiles, each with a quarter of the columns of its 32 lanes, else 8 with half.
+// Epilogue warps: 16 behind the 256-column tiles, each with a quarter of the columns of its 32 lanes, 8 with half of them,
+// or 4 with all of a narrow tile's.
 template <int BN>
 constexpr int epi_warps() {
-    return BN == 256 ? 16 : 8;
+    return BN == 256 ? 16 : BN >= 64 ? 8 : 4;
 }
 template <int BN>
 constexpr int threads_of() {
     return 64 + 32 * epi_warps<BN>();
 }
 constexpr int MAX_STAGES = 8;
+constexpr int SMEM_LIMIT = 232448;  // 227 KB, static shared memory included
 constexpr int CHUNK = 16;           // k-blocks of 32 between two additions of the h h accumulator (PL = 3)
 
 template <int PL>
@@ -202,17 +204,6 @@ template <int BN>
 constexpr int pair_of() {
     return BN == 256 ? 2 : 1;
 }
-// Calls of few rows stream the weights: two CTAs per SM keep more loads in flight, and clusters of eight find room.
-template <int BN>
-constexpr int ctas_per_sm() {
-    return BN <= 32 ? 2 : 1;
-}
-// Shared memory of a CTA, static included: 227 KB, or half an SM's 228 KB less the 1 KB that each CTA costs.
-template <int BN>
-constexpr int smem_limit() {
-    return BN <= 32 ? 115712 : 232448;
-}
-
 // Blocks per stage. The issuing thread spends about 350 cycles per stage on its barriers, more than the four MMAs of a narrow
 // 16-bit tile take: there a stage holds two blocks.
 template <int PL, int BN>
@@ -262,7 +253,7 @@ __device__ __forceinline__ void put_round(T* buf, const float (&v)[N], const CUt
 }
 
 template <typename T, int PL, int BN>
-__global__ void __launch_bounds__(threads_of<BN>(), ctas_per_sm<BN>())
+__global__ void __launch_bounds__(threads_of<BN>(), 1)
 linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams P) {
     constexpr int BK = block_k<PL>();
     constexpr int CG = pair_of<BN>();
@@ -675,7 +666,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
         const Place at(P, p, u, rank);
         __syncwarp();
         if (!pushed) cluster_wait();
-        join_cluster<T, BN, 8>(p, at.i * BM, at.j * BN,
+        join_cluster<T, BN, EW>(p, at.i * BM, at.j * BN,
                                reinterpret_cast<const float*>(base + (size_t)NS * STAGE), rank, P.split_log, warp - 2);
     }
     tc_fence_before();
@@ -1049,7 +1040,7 @@ Plan plan(const Extents& x, bool f32, bool parts, int sms) {
     for (int bn = 16; bn <= 256; bn *= 2) {
         if (bn < 64 && (mn || J > bn)) continue;
         if (bn > 64 && (J <= bn / 2 || (bn == 256 && I <= BM))) continue;
-        const int cg = bn == 256 ? 2 : 1, slots = sms * (bn <= 32 ? 2 : 1), workers = slots / cg;
+        const int cg = bn == 256 ? 2 : 1, slots = sms, workers = slots / cg;
         auto tiles_of = [&](int k) { return (x.I[k] + BM * cg - 1) / (BM * cg) * ((x.J[k] + bn - 1) / bn); };
         auto consider = [&](int split, const int (&plog)[2]) {
             double total = 0, longest = 0, join = 0;
@@ -1188,10 +1179,10 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
             return cudaErrorInvalidValue;
     }
     auto kern = linear_tc_k<T, PL, BN>;
-    cudaError_t e = allow_dyn_smem((const void*)kern, smem_limit<BN>() - 1024);
+    cudaError_t e = allow_dyn_smem((const void*)kern, SMEM_LIMIT - 1024);
     if (e != cudaSuccess) return e;
     const int need = stage_bytes<PL, BN>();
-    P.stages = std::min(MAX_STAGES, (smem_limit<BN>() - 1024 - 1024 - epi_bytes<BN>()) / need);
+    P.stages = std::min(MAX_STAGES, (SMEM_LIMIT - 1024 - 1024 - epi_bytes<BN>()) / need);
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(threads_of<BN>());
     cfg.dynamicSmemBytes = 1024 + (size_t)P.stages * need + epi_bytes<BN>();
@@ -1206,7 +1197,7 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
     // suggest).
     P.split = 1;
     P.split_log = 0;
-    const int slots = sms * ctas_per_sm<BN>();
+    const int slots = sms;
     while (CG == 1 && P.split < split) {
         at[0].val.clusterDim.x = P.split * 2;
         cfg.numAttrs = 1;
@@ -1219,7 +1210,7 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
     }
     P.test_stall = getenv("VF_TEST_OPS_STALL") != nullptr;
     P.workers = (int)std::min<long long>(tiles, P.split > 1 ? tiles : slots / CG);
-    if (tiles == 0) P.workers = std::min((P.N + 255) / 256, sms);
+    if (tiles == 0) P.workers = std::min((P.N + 127) / 128, sms);
     P.gap = 1;
     if (P.split == 1 && count == 2) {
         // as long as a tile of p[0], but no more than evens out over the workers that its last turn leaves idle

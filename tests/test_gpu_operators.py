@@ -303,6 +303,25 @@ vf.ops_check()
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K", [(9, 200, 300), (130, 140, 520), (300, 3712, 1472)])
+def test_one_operand_off_its_alignment(dtype, M, N, K):
+    """x or W alone starts, or has rows, off a 16-byte boundary: exact on whole numbers."""
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    x, W = (torch.randint(-2, 3, s, generator=gen, device="cuda").to(dtype) for s in ((M, K), (N, K)))
+    want = (x.double() @ W.double().t()).to(dtype)
+    px = torch.zeros(M, K + 1, device="cuda", dtype=dtype)[:, :K].copy_(x)
+    pw = torch.zeros(N * K + 1, device="cuda", dtype=dtype)[1:].view(N, K).copy_(W)
+    assert torch.equal(vf.linear(px, W)["y"], want)
+    assert torch.equal(vf.linear(x, pw)["y"], want)
+    assert torch.equal(vf.linear(px, pw)["y"], want)
+    dy = torch.randint(-2, 3, (M, N), generator=gen, device="cuda").to(dtype)
+    for a, b in ((px, W), (x, pw)):
+        got = vf.linear_grad(dy, a, b)
+        assert torch.equal(got["dx"], (dy.double() @ W.double()).to(dtype))
+        assert torch.equal(got["dW"], (dy.double().t() @ x.double()).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_empty_sizes(dtype):
     e = lambda *s: torch.zeros(*s, device="cuda", dtype=dtype)  # noqa: E731
     assert vf.linear(e(0, 4), e(3, 4), e(3))["y"].shape == (0, 3)
