@@ -26,7 +26,9 @@ __device__ int g_direct_timeout;
 constexpr int BK = 64;             // steps of the reduction per block: 128-byte rows in shared memory
 constexpr int WORKERS = 512;       // loading and finishing threads
 constexpr int THREADS = WORKERS + 32;
-constexpr int MAX_CHUNK = 8;       // fp32: most blocks added up in TMEM without a stop (512 products, as k_linear_tc.cu)
+constexpr int CHUNK = 4;           // fp32: blocks added up in one accumulator (256 products, as k_linear_tc.cu)
+// fp32: accumulators of h h products, one after the other, all added in registers at the end; TMEM has 512 columns.
+constexpr int accumulators(int bn) { return bn == 64 ? 4 : 8; }
 
 // rows x Tn operand at p: element (r, t) at p[r * ld + t].
 struct Source {
@@ -139,8 +141,8 @@ template <typename T, int PL, int BN, bool VA, bool VB>
 __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_constant__ DirectParams P) {
     constexpr int A_PLANE = BM * 128, B_PLANE = BN * 128;
     constexpr int STAGE = direct_stage<PL, BN>();
-    constexpr int USED_COLS = PL == 3 ? 2 * BN : BN;
-    constexpr int TMEM_COLS = USED_COLS < 32 ? 32 : USED_COLS;
+    constexpr int COR = accumulators(BN) * BN;                     // columns of the small products
+    constexpr int TMEM_COLS = PL == 3 ? (BN == 16 ? 256 : 512) : BN < 32 ? 32 : BN;
     constexpr int FW = BN >= 32 ? 16 : 8;                          // finishing warps
     constexpr int PART = BN / (FW / 4);                            // columns of one
     constexpr int NA = BM * 8 / WORKERS;                           // times eight elements of A per thread
@@ -196,20 +198,22 @@ __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_const
                 if (!wait_phase(&full[g.slot], g.lap & 1, abort_flag)) break;
                 tc_fence_after();
                 const uint64_t ah = a0 + (uint32_t)(g.slot * (STAGE / 16)), bh = b0 + (uint32_t)(g.slot * (STAGE / 16));
+                const int at = kb - kb0;
+                const uint32_t d = PL == 3 ? tmem + at / CHUNK * BN : tmem;
 #pragma unroll
                 for (int kk = 0; kk < BK / 16; ++kk) {
                     const uint64_t h = ah + kk * 2, H = bh + kk * 2;  // 32 bytes along a line
-                    const uint32_t more = kb > kb0 || kk > 0 ? 1u : 0u;
+                    const uint32_t more = at > 0 || kk > 0 ? 1u : 0u;
                     if (PL == 3) {
                         const uint64_t m = h + A_PLANE / 16, l = m + A_PLANE / 16;
                         const uint64_t M = H + B_PLANE / 16, L = M + B_PLANE / 16;
-                        mma_f16_ss<1>(tmem + BN, l, H, idesc, more);
-                        mma_f16_ss<1>(tmem + BN, h, L, idesc, 1u);
-                        mma_f16_ss<1>(tmem + BN, m, M, idesc, 1u);
-                        mma_f16_ss<1>(tmem + BN, m, H, idesc, 1u);
-                        mma_f16_ss<1>(tmem + BN, h, M, idesc, 1u);
+                        mma_f16_ss<1>(tmem + COR, l, H, idesc, more);
+                        mma_f16_ss<1>(tmem + COR, h, L, idesc, 1u);
+                        mma_f16_ss<1>(tmem + COR, m, M, idesc, 1u);
+                        mma_f16_ss<1>(tmem + COR, m, H, idesc, 1u);
+                        mma_f16_ss<1>(tmem + COR, h, M, idesc, 1u);
                     }
-                    mma_f16_ss<1>(tmem, h, H, idesc, more);
+                    mma_f16_ss<1>(d, h, H, idesc, PL == 3 ? (at % CHUNK > 0 || kk > 0 ? 1u : 0u) : more);
                 }
                 mma_commit(&empty[g.slot]);
             }
@@ -261,17 +265,21 @@ __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_const
             pushed = true;
 #pragma unroll 1
             for (int c = 0; c < PART; c += LD) {
-                uint32_t v[LD], x[LD];
-                tmem_ld<LD>(acc + c, v);
-                if (PL == 3) tmem_ld<LD>(acc + BN + c, x);
+                uint32_t v[LD];
+                float o[LD];
+                tmem_ld<LD>(acc + (PL == 3 ? COR : 0) + c, v);
                 if (S == 1 && c + LD < PART) res_lane<T>(p, i, (long long)jw + c + LD, rn);
                 tmem_wait_ld();
-                float o[LD];
 #pragma unroll
-                for (int k = 0; k < LD; ++k)
-                    o[k] = kb1 == kb0 ? 0.f  // a share of no blocks
-                           : PL == 3 ? __uint_as_float(v[k]) + __uint_as_float(x[k])
-                                     : __uint_as_float(v[k]);
+                for (int k = 0; k < LD; ++k) o[k] = kb1 > kb0 ? __uint_as_float(v[k]) : 0.f;  // a share may hold no blocks
+                if (PL == 3)
+#pragma unroll 1
+                    for (int a = 0; a < (kb1 - kb0 + CHUNK - 1) / CHUNK; ++a) {
+                        tmem_ld<LD>(acc + a * BN + c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < LD; ++k) o[k] += __uint_as_float(v[k]);
+                    }
                 if (S > 1) {
 #pragma unroll
                     for (int k = 0; k < LD; ++k)
@@ -310,13 +318,13 @@ int columns(long long M) { return M > 32 ? 64 : M > 16 ? 32 : 16; }
 
 // Cluster size (log 2) of the split reduction of `tiles` tiles over nk blocks. In units of one block's time: a CTA costs
 // about five blocks before and after its products and two more for the join; the estimate is the longest CTA or the SMs'
-// share of the total (clusters of eight leave SMs unused). fp32: at least as many parts as MAX_CHUNK asks for.
-int split_log(long long tiles, int nk, bool f32, int sms) {
+// share of the total (clusters of eight leave SMs unused). `most`: blocks that a CTA can add up.
+int split_log(long long tiles, int nk, int most, int sms) {
     int best = 0;
     double best_cost = 1e30;
     for (int log = 0; log <= 3; ++log) {
         const int S = 1 << log, part = (nk + S - 1) / S;
-        if (f32 && part > MAX_CHUNK) continue;
+        if (part > most) continue;
         const double cta = 5.0 + part + (log > 0 ? 2.0 : 0.0);
         const double cost = std::max(cta, cta * S * tiles / sms * (log == 3 ? 1.3 : 1.1));
         if (cost < best_cost) {
@@ -338,7 +346,7 @@ cudaError_t launch_bn(DirectParams& P, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int need = direct_stage<PL, BN>();
     P.stages = std::min(4, (SMEM_LIMIT - 1024 - BN * 512) / need);
-    P.split_log = split_log(p.tiles, p.nk, PL == 3, sms);
+    P.split_log = split_log(p.tiles, p.nk, PL == 3 ? CHUNK * accumulators(BN) : 1 << 30, sms);
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(THREADS);
     cfg.gridDim = dim3((unsigned)(p.tiles << P.split_log));
@@ -382,13 +390,13 @@ bool aligned(const void* p, long long ld, int e) { return (reinterpret_cast<uint
 
 }  // namespace
 
-// Every tile has an SM to itself: fp32 with the reduction cut into parts of MAX_CHUNK blocks, which are up to eight.
+// Every tile has an SM to itself: fp32 with the reduction cut into as many parts as the accumulators ask for, up to eight.
 bool linear_direct_fits(int dtype, long long M, int N, int K) {
     int sms = 0, parts = 1;
     if (device_sms(&sms) != cudaSuccess) return false;
-    if (dtype == VF_F32)
-        while (parts * MAX_CHUNK < blocks_of(K)) parts *= 2;
     const int bn = columns(M);
+    if (dtype == VF_F32)
+        while (parts * CHUNK * accumulators(bn) < blocks_of(K)) parts *= 2;
     return parts <= 8 && ((long long)N + BM - 1) / BM * ((M + bn - 1) / bn) * parts <= sms;
 }
 

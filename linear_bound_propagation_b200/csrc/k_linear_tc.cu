@@ -12,8 +12,10 @@
 // fp32 (PL = 3): x = h + m + l, three bf16 pieces of 8 significand bits each, by truncation, so the pieces hold all 24
 // bits and bf16's exponent range is fp32's. Six of the nine products are formed (h h, h m, m h, m m, h l, l h); the
 // three left out are below 2^-24 of the largest. An MMA adds its products to the accumulator with truncation (measured:
-// a sum of positive terms over 512 MMAs comes out 1e-5 low), so the five small products go to an accumulator of their own, and
-// the h h accumulator is added to registers, rounding to nearest, every CHUNK of the reduction.
+// 2.2e-8 of the sum per MMA, low for sums of positive terms), so the five small products go to an accumulator of their own, and
+// both are added to registers, rounding to nearest: h h every CHUNK blocks, the small ones every COR_CHUNKS chunks. Error against
+// 64 bits at a reduction of 1024, signed normal values: 3.0e-7 (2-norm; a plain fp32 product 5.7e-7);
+// at 4096, positive values: 6.2e-7 (8.4e-7).
 //
 // Roles (one CTA per SM, or a pair of CTAs on two SMs for 256 x 256 tiles; persistent over the tiles): warp 0 TMA
 // producer, warp 1 MMA issuer, warps 2 and up epilogue (lane quarter warp % 4 of TMEM, four warps to a share of the
@@ -56,7 +58,8 @@ constexpr int threads_of() {
 }
 constexpr int MAX_STAGES = 8;
 constexpr int SMEM_LIMIT = 232448;  // 227 KB, static shared memory included
-constexpr int CHUNK = 16;           // k-blocks of 32 between two additions of the h h accumulator (PL = 3)
+constexpr int CHUNK = 8;       // fp32: blocks of 32 between two additions of the h h accumulator
+constexpr int COR_CHUNKS = 8;  // and chunks between two of the small products'
 
 template <int PL>
 constexpr int block_k() {
@@ -401,7 +404,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
     } else if (warp == 1) {
         if (pr == 0 && elect_one()) {
             // --------------------------------------------------------------------------------- MMA issuer
-            Ring g, chunk, tile;  // stages; accumulator sets (one chunk each); small-product sets (one tile each)
+            Ring g, chunk, cor;  // stages; accumulator sets (a chunk each); sets of the small products (COR_CHUNKS chunks)
             bool ok = true;
             Walk walk(P, worker);
             int w, u;
@@ -418,26 +421,26 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                 const uint64_t a0 = operand_desc<BK>(smem_u32(base), a_mn);
                 const uint64_t b0 = operand_desc<BK>(smem_u32(base) + PL * A_PLANE, b_mn);
                 const uint32_t step_a = (a_mn ? 2048 : 32) / 16, step_b = (b_mn ? 2048 : 32) / 16;
-                const uint32_t cor = tmem + ACC_COLS + (uint32_t)tile.slot * BN;
-                int in_chunk = 0;
+                int in_chunk = 0, in_cor = 0;
                 for (int kb = kb0; kb < kb1; ++kb, g.next(NS)) {
                     if (!(ok = wait_phase(&full[g.slot], g.lap & 1, abort_flag))) break;
                     const uint32_t d = tmem + (uint32_t)chunk.slot * BN;
                     const uint64_t ah = a0 + (uint32_t)(g.slot * (STAGE / 16)), bh = b0 + (uint32_t)(g.slot * (STAGE / 16));
                     if (PL == 3) {
-                        if (kb == kb0 && tile.lap > 0 &&
-                            !(ok = wait_phase(&cor_empty[tile.slot], (tile.lap - 1) & 1, abort_flag)))
+                        if (in_cor == 0 && in_chunk == 0 && cor.lap > 0 &&
+                            !(ok = wait_phase(&cor_empty[cor.slot], (cor.lap - 1) & 1, abort_flag)))
                             break;
                         tc_fence_after();
+                        const uint32_t dc = tmem + ACC_COLS + (uint32_t)cor.slot * BN;
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk) {
                             const uint64_t h = ah + kk * step_a, m = h + A_PLANE / 16, l = m + A_PLANE / 16;
                             const uint64_t H = bh + kk * step_b, M = H + B_PLANE / 16, L = M + B_PLANE / 16;
-                            mma_f16_ss<CG>(cor, l, H, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
-                            mma_f16_ss<CG>(cor, h, L, idesc, 1u);
-                            mma_f16_ss<CG>(cor, m, M, idesc, 1u);
-                            mma_f16_ss<CG>(cor, m, H, idesc, 1u);
-                            mma_f16_ss<CG>(cor, h, M, idesc, 1u);
+                            mma_f16_ss<CG>(dc, l, H, idesc, (in_cor > 0 || in_chunk > 0 || kk > 0) ? 1u : 0u);
+                            mma_f16_ss<CG>(dc, h, L, idesc, 1u);
+                            mma_f16_ss<CG>(dc, m, M, idesc, 1u);
+                            mma_f16_ss<CG>(dc, m, H, idesc, 1u);
+                            mma_f16_ss<CG>(dc, h, M, idesc, 1u);
                         }
                     }
                     if (in_chunk == 0 && chunk.lap > 0 &&
@@ -456,9 +459,12 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                         commit<CG>(&acc_full[chunk.slot]);
                         chunk.next(NB);
                         in_chunk = 0;
+                        if (PL == 3 && (kb + 1 == kb1 || ++in_cor == COR_CHUNKS)) {
+                            cor.next(NB);
+                            in_cor = 0;
+                        }
                     }
                 }
-                tile.next(NB);
             }
             // TMEM is never freed, nor the stages reused, under MMAs in flight: one last commit tracks them all
             if (CG == 1)
@@ -485,7 +491,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
             }
         constexpr int ROUND = epi_round<T, BN>(), RL = ROUND < 16 ? 8 : 16;
         T* buf = reinterpret_cast<T*>(base + (size_t)NS * STAGE + (EPI_TMA ? e * (65536 / EW) : 0));  // 4 x 32 x ROUND
-        Ring chunk, tile;     // as the MMA issuer counts them
+        Ring chunk, cor;      // as the MMA issuer counts them
         Ring rin;             // residual rounds consumed
         int pending = 0;      // residual rounds loaded and not yet consumed
         int ob = 0;           // output buffer in turn
@@ -538,10 +544,25 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                         __syncwarp();
                         if (lane == 0) arrive_leader<CG>(&acc_empty[chunk.slot]);
                         chunk.next(NB);
+                        if ((ch + 1) % COR_CHUNKS == 0) {
+                            const uint32_t cor_t = tmem + lane_base + ACC_COLS + cor.slot * BN;
+#pragma unroll
+                            for (int c = 0; c < PART; c += LD) {
+                                uint32_t v[LD];
+                                tmem_ld<LD>(cor_t + c, v);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < LD; ++k) acc[c + k] += __uint_as_float(v[k]);
+                            }
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_leader<CG>(&cor_empty[cor.slot]);
+                            cor.next(NB);
+                        }
                     }
                 }
                 if (!alive) break;
-                const uint32_t cor_t = tmem + lane_base + ACC_COLS + tile.slot * BN;
+                const uint32_t cor_t = tmem + lane_base + ACC_COLS + cor.slot * BN;
 #pragma unroll
                 for (int c = 0; c < PART; c += LD) {  // the finished sums go back to TMEM for the rolled loops below
                     uint32_t v[LD];
@@ -555,7 +576,8 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_leader<CG>(&cor_empty[tile.slot]);
+                if (lane == 0) arrive_leader<CG>(&cor_empty[cor.slot]);
+                cor.next(NB);
             } else {
                 if (!__all_sync(0xffffffffu, wait_phase(&acc_full[chunk.slot], chunk.lap & 1, abort_flag))) break;
                 tc_fence_after();
@@ -645,7 +667,6 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
             __syncwarp();
             if (lane == 0) arrive_leader<CG>(&acc_empty[chunk.slot]);
             chunk.next(NB);
-            tile.next(NB);
         }
         // stores have read their buffers and reached memory, and no load into them is left behind
         if (lane == 0) {
