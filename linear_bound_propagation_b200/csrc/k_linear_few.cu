@@ -1,4 +1,4 @@
-// Backward pass of the dense layer for a few rows (M <= 8) on the FFMA units.
+// Backward pass of the dense layer for a few rows on the FFMA units: up to eight of fp32, up to four of 16 bits.
 //
 // With so few rows the pass is W read once (dx = g W) and dW written once (dW = g^T x): 2 N K elements against 4 M N K
 // operations, bound by memory. A block takes a slab of rows n and a chunk of columns k of one of the two; g of the slab
@@ -6,6 +6,11 @@
 // x) in registers. dx of a slab is a partial sum; a second launch adds the slabs in a fixed order. db and dr come from the
 // first chunk's blocks. One block for both products kept W's loads waiting behind twice the registers: 8 x 4096 x 4096
 // bf16 52 us, apart 36 us.
+//
+// Measured here and on the tensor cores (k_linear_tc.cu), which pad the rows to 16, M x 4096 x 4096 with relu in us:
+//   bf16   1: 15.9 and 29.0   2: 16.5 and 29.3   4: 22.2 and 28.4   5: 32.2 and 28.6   8: 35.9 and 28.8
+//   fp32   1: 26.7 and 91.4   4: 34.4 and 91.2   8: 46.2 and 91.3
+// so eight rows of fp32 and four of 16 bits stay here. One row of fp32: 2 N K elements in 26.7 us, 5.0 TB/s.
 #include <algorithm>
 
 #include "vf_internal.cuh"
@@ -16,7 +21,7 @@ namespace vf {
 namespace {
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
-constexpr int MAX_M = 8;
+constexpr int max_rows(int elem) { return elem == 4 ? 8 : 4; }
 constexpr int MAX_SLAB = 1024;  // rows of g in shared memory: 32 KB for eight rows of inputs
 
 struct FewParams {
@@ -190,10 +195,10 @@ cudaError_t launch_vec(const LinearGrad& f, FewParams& P, float* work, size_t ha
         e = launch_mb<T, VEC, 1>(P, s, st);
     else if (f.M == 2)
         e = launch_mb<T, VEC, 2>(P, s, st);
-    else if (f.M <= 4)
+    else if (max_rows(sizeof(T)) == 4 || f.M <= 4)
         e = launch_mb<T, VEC, 4>(P, s, st);
     else
-        e = launch_mb<T, VEC, 8>(P, s, st);
+        e = launch_mb<T, VEC, max_rows(sizeof(T))>(P, s, st);
     if (e != cudaSuccess || P.part == nullptr) return e;
     linear_few_join_k<T><<<(unsigned)((f.M * f.K + THREADS - 1) / THREADS), THREADS, 0, st>>>(P.part, s.slabs, (int)f.M, f.K,
                                                                                              (T*)f.dx, f.lddx);
@@ -212,8 +217,8 @@ cudaError_t launch_few(const LinearGrad& f, float* work, size_t have, size_t* ne
 
 }  // namespace
 
-bool linear_few_supported(long long M, int N, int K) {
-    return M >= 1 && M <= MAX_M && N >= 1 && K >= 1 && (long long)N <= 65535LL * MAX_SLAB;
+bool linear_few_supported(int dtype, long long M, int N, int K) {
+    return M >= 1 && M <= max_rows(dtype == VF_F32 ? 4 : 2) && N >= 1 && K >= 1 && (long long)N <= 65535LL * MAX_SLAB;
 }
 
 size_t linear_few_workspace(int dtype, long long M, int N, int K) {

@@ -128,7 +128,10 @@ int check_overlaps(const ClipList& l) {
     return VF_OK;
 }
 
-// Products too small to fill a few tensor-core tiles, and empty ones, run on the FFMA kernels.
+// Small products, and empty ones, run on the FFMA kernels, whose time goes with the reduction's length. M x N x K in us, FFMA
+// and tensor cores: fp32 forward 16x32x64 4.4 and 3.9, 64x32x16 3.4 and 4.8, 16x16x256 11.1 and 5.0, backward 16x32x64 4.2
+// and 5.8, 64x32x32 8.1 and 6.6; bf16 forward 64x32x16 4.8 and 4.0, 16x16x256 17.3 and 4.1, backward 16x64x128 5.6 and 6.1,
+// 128x64x32 11.3 and 6.4.
 bool use_tc(long long M, int N, int K) { return linear_tc_supported(M, N, K) && (double)M * N * K >= 32768.0; }
 
 }  // namespace
@@ -140,7 +143,7 @@ int vf_linear_workspace(int dtype, long long M, int N, int K, int grad, size_t* 
         if (bytes == nullptr) return ops_fail(VF_ERR_ARG, "NULL pointer");
         OPS_TRY(check_kind(dtype, VF_ACT_NONE));
         OPS_TRY(check_sizes(M, N, K));
-        if (grad != 0 && linear_few_supported(M, N, K))
+        if (grad != 0 && linear_few_supported(dtype, M, N, K))
             *bytes = linear_few_workspace(dtype, M, N, K);
         else if (use_tc(M, N, K) && (grad != 0 || !linear_direct_fits(dtype, M, N, K)))
             *bytes = linear_tc_workspace(dtype, M, N, K, grad != 0);
@@ -195,7 +198,7 @@ int vf_linear_grad(int dtype, int act, const void* dy, long long lddy, const voi
         OPS_TRY(check_vector("db", db, dtype));
         if (dr != nullptr) OPS_TRY(check_matrix("dr", dr, M, N, lddr, dtype));
         const LinearGrad p{dtype, act, dy, lddy, z, ldz, x, ldx, W, ldw, M, N, K, dx, lddx, dW, lddw, db, dr, lddr};
-        const bool few = linear_few_supported(M, N, K);
+        const bool few = linear_few_supported(dtype, M, N, K);
         if (!few && !use_tc(M, N, K)) return launched(launch_linear_grad_ffma(p, (cudaStream_t)stream));
         OPS_TRY(check_aligned(work));
         size_t need = 0;

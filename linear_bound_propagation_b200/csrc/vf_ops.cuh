@@ -257,7 +257,7 @@ cudaError_t launch_linear_ffma(const LinearFwd& p, cudaStream_t s);
 cudaError_t launch_linear_grad_ffma(const LinearGrad& p, cudaStream_t s);
 
 // Backward pass of a few rows (k_linear_few.cu); workspace as for the tensor-core launches below.
-bool linear_few_supported(long long M, int N, int K);
+bool linear_few_supported(int dtype, long long M, int N, int K);
 size_t linear_few_workspace(int dtype, long long M, int N, int K);
 cudaError_t launch_linear_few_grad(const LinearGrad& p, void* work, size_t have, size_t* need, cudaStream_t s);
 
