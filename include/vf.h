@@ -370,8 +370,10 @@ typedef enum {
 } vf_act;
 
 /* Bytes of workspace that vf_linear (grad = 0) or vf_linear_grad (grad = 1) may need for these sizes, whatever the
- * strides and alignment. May be 0. vf_linear needs none (NULL, 0) where x and W are of a 16-bit type, 16-byte aligned
- * and have row strides that are multiples of 8. A call whose workspace is too small launches nothing. [host] */
+ * strides and alignment; with grad = VF_FORWARD_ALIGNED, vf_linear where x and W are 16-byte aligned and their row
+ * strides are multiples of 16 bytes. May be 0 (NULL is then accepted). A call whose workspace is too small launches
+ * nothing. [host] */
+enum { VF_FORWARD_ALIGNED = 2 };
 int vf_linear_workspace(int dtype, long long M, int N, int K, int grad, size_t* bytes);
 
 /* Dense layer with bias, residual and activation:  y = act(z),  z = x W^T + b + r.

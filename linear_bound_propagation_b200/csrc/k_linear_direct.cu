@@ -391,13 +391,23 @@ bool aligned(const void* p, long long ld, int e) { return (reinterpret_cast<uint
 }  // namespace
 
 // Every tile has an SM to itself: fp32 with the reduction cut into as many parts as the accumulators ask for, up to eight.
-bool linear_direct_fits(int dtype, long long M, int N, int K) {
+// Against a laid-out copy and k_linear_tc.cu (M x N x K, us, here and there): fp32 16x512x512 5.2 and 8.4, 1024x256x784
+// 10.3 and 13.2, 512x1024x1024 14.2 and 16.9; many waves of tiles, fp32 297x3712x1472 118 and 33.
+// Rows that are not 16-byte aligned are loaded element by element. In fp32 that costs more than the copy where several
+// columns of tiles load the same W and a CTA takes many such lines: x and W unaligned, 256x256x256 8.4 and 9.7,
+// 1024x256x784 16.1 and 14.0, 512x1024x1024 26.5 and 17.7; one column of tiles, 16x2048x4096, 35.8 and 37.9. In 16 bits the
+// two are close (bf16 1024x256x784 9.5 and 10.1, 777x1001x512 12.8 and 9.5), and a call that waits for the host is shorter
+// with one launch (9.9 and 14.3).
+bool linear_direct_fits(int dtype, long long M, int N, int K, bool x_aligned, bool w_aligned) {
     int sms = 0, parts = 1;
     if (device_sms(&sms) != cudaSuccess) return false;
-    const int bn = columns(M);
-    if (dtype == VF_F32)
-        while (parts * CHUNK * accumulators(bn) < blocks_of(K)) parts *= 2;
-    return parts <= 8 && ((long long)N + BM - 1) / BM * ((M + bn - 1) / bn) * parts <= sms;
+    const int bn = columns(M), nk = blocks_of(K), most = dtype == VF_F32 ? CHUNK * accumulators(bn) : 1 << 30;
+    while (parts * most < nk && parts <= 8) parts *= 2;
+    const long long tiles = ((long long)N + BM - 1) / BM * ((M + bn - 1) / bn);
+    if (parts > 8 || tiles * parts > sms) return false;
+    if (dtype != VF_F32 || M <= bn) return true;
+    const int S = 1 << split_log(tiles, nk, most, sms);
+    return ((x_aligned ? 0 : bn) + (w_aligned ? 0 : BM)) * ((nk + S - 1) / S) < 512;
 }
 
 cudaError_t launch_linear_direct(const LinearFwd& f, cudaStream_t s) {

@@ -134,6 +134,10 @@ int check_overlaps(const ClipList& l) {
 // 128x64x32 11.3 and 6.4.
 bool use_tc(long long M, int N, int K) { return linear_tc_supported(M, N, K) && (double)M * N * K >= 32768.0; }
 
+bool aligned16(const void* p, long long ld, int dtype) {
+    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)ld * elem_bytes(dtype)) & 15) == 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -143,12 +147,15 @@ int vf_linear_workspace(int dtype, long long M, int N, int K, int grad, size_t* 
         if (bytes == nullptr) return ops_fail(VF_ERR_ARG, "NULL pointer");
         OPS_TRY(check_kind(dtype, VF_ACT_NONE));
         OPS_TRY(check_sizes(M, N, K));
-        if (grad != 0 && linear_few_supported(dtype, M, N, K))
+        const bool aligned = grad == VF_FORWARD_ALIGNED;
+        if (grad < 0 || grad > VF_FORWARD_ALIGNED) return ops_fail(VF_ERR_ARG, "grad = %d", grad);
+        if (grad == 1 && linear_few_supported(dtype, M, N, K))
             *bytes = linear_few_workspace(dtype, M, N, K);
-        else if (use_tc(M, N, K) && (grad != 0 || !linear_direct_fits(dtype, M, N, K)))
-            *bytes = linear_tc_workspace(dtype, M, N, K, grad != 0);
-        else
+        else if (!use_tc(M, N, K) || (aligned && (dtype != VF_F32 || linear_direct_fits(dtype, M, N, K, true, true))) ||
+                 (grad == 0 && linear_direct_fits(dtype, M, N, K, false, false)))
             *bytes = 0;
+        else
+            *bytes = linear_tc_workspace(dtype, M, N, K, grad == 1);
         return VF_OK;
     });
 }
@@ -168,7 +175,7 @@ int vf_linear(int dtype, int act, const void* x, long long ldx, const void* W, l
         if (z != nullptr) OPS_TRY(check_matrix("z", z, M, N, ldz, dtype));
         const LinearFwd p{dtype, act, x, ldx, W, ldw, b, r, ldr, M, N, K, y, ldy, z, ldz};
         if (!use_tc(M, N, K)) return launched(launch_linear_ffma(p, (cudaStream_t)stream));
-        if (!linear_tc_in_place(p) && linear_direct_fits(dtype, M, N, K))
+        if (!linear_tc_in_place(p) && linear_direct_fits(dtype, M, N, K, aligned16(x, ldx, dtype), aligned16(W, ldw, dtype)))
             return launched(launch_linear_direct(p, (cudaStream_t)stream));
         OPS_TRY(check_aligned(work));
         size_t need = 0;

@@ -274,7 +274,7 @@ cudaError_t device_sms(int* sms);  // SMs of the current device
 
 // Forward product that lays its operands out itself (k_linear_direct.cu): any strides and alignment, no workspace, for the
 // sizes that `fits` accepts.
-bool linear_direct_fits(int dtype, long long M, int N, int K);
+bool linear_direct_fits(int dtype, long long M, int N, int K, bool x_aligned, bool w_aligned);
 cudaError_t launch_linear_direct(const LinearFwd& p, cudaStream_t s);
 cudaError_t direct_take_timeout(int* flag);
 

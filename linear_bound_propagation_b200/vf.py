@@ -32,6 +32,7 @@ SYMBOLS = ["vf_net_create", "vf_net_destroy", "vf_net_node_size", "vf_net_total_
            "vf_net_node_info", "vf_bab_verify", "vf_bab_search", "vf_abi_layout", "vf_linear_workspace", "vf_linear",
            "vf_linear_grad", "vf_clip_workspace", "vf_clip_grad_norm", "vf_ops_check"]
 VF_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+VF_FORWARD_ALIGNED = 2
 VF_ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 NOALLOC_SCRATCH_FLOATS = 1 << 22
 
@@ -565,8 +566,7 @@ def linear(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tensor] = None,
         y = out
         yp, ldy = _matrix("out", y, shape, tt, dev)
     z = torch.empty_strided(shape, (N, 1), device=x.device, dtype=tt) if want_z else None
-    # 16-bit operands with 16-byte rows are read in place
-    nbytes = 0 if dtype and (xp | wp) & 15 == 0 and (ldx | ldw) & 7 == 0 else _linear_work(dtype, M, N, K, 0)
+    nbytes = _linear_work(dtype, M, N, K, 0 if (xp | wp | (ldx | ldw) * tt.itemsize) & 15 else VF_FORWARD_ALIGNED)
     work = torch.empty_strided((nbytes,), (1,), device=x.device, dtype=torch.uint8) if nbytes else None
     _check(lib().vf_linear(dtype, a, xp, ldx, wp, ldw, bp, rp, ldr, M, N, K, yp, ldy, None if z is None else z.data_ptr(),
                            N, None if work is None else work.data_ptr(), nbytes,

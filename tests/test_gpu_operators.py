@@ -258,6 +258,18 @@ def test_workspace_is_checked_before_anything_runs():
     assert (dW == 7.0).all()
 
 
+@pytest.mark.parametrize("pad_x,pad_w", [(0, 0), (0, 1), (1, 0), (1, 1)])
+def test_alignment_changes_the_kernel_not_the_result(pad_x, pad_w):
+    """One wave of tiles in fp32: rows of 16-byte alignment need no workspace, others may go through a laid-out copy.
+    Whole numbers: every sum is exact."""
+    M, N, K = 500, 1000, 900
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    x = torch.randint(-3, 4, (M, K + pad_x), generator=gen, device="cuda").float()[:, :K]
+    W = torch.randint(-3, 4, (N, K + pad_w), generator=gen, device="cuda").float()[:, :K]
+    assert vf._linear_work(0, M, N, K, vf.VF_FORWARD_ALIGNED) == 0 < vf._linear_work(0, M, N, K, 0)
+    assert (vf.linear(x, W)["y"].double() == x.double() @ W.double().t()).all()
+
+
 def test_a_wait_that_runs_out_is_reported(monkeypatch):
     """Host-set hook: the first CTA never makes its first copies, so its bounded waits expire; the call returns, the
     check reports it once, and later calls are right. One CTA per tile, and a pair of CTAs."""

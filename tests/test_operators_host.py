@@ -48,6 +48,7 @@ def test_sizes_beyond_32_bit_tiles_are_refused():
     assert vf.lib().vf_linear_workspace(0, 1 << 31, 8, 8, 0, ctypes.byref(n)) == vf.VF_ERR_UNSUPPORTED
     assert vf.lib().vf_linear_workspace(7, 8, 8, 8, 0, ctypes.byref(n)) == vf.VF_ERR_ARG
     assert vf.lib().vf_linear_workspace(0, 8, 8, 8, 0, None) == vf.VF_ERR_ARG
+    assert vf.lib().vf_linear_workspace(0, 8, 8, 8, 3, ctypes.byref(n)) == vf.VF_ERR_ARG
 
 
 def test_empty_outputs_are_no_ops_without_a_device():
