@@ -389,7 +389,7 @@ int vf_linear(int dtype, int act, const void* x, long long ldx, const void* W, l
 /* Backward pass of vf_linear for dy [M, N], the gradient of y:  g = dy act'(z),
  *   dx [M, K] = g W,  dW [N, K] = g^T x,  db [N] = sum over rows of g,  dr [M, N] = g.
  * Every output may be NULL (not computed); z may be NULL for VF_ACT_NONE, W without dx, x without dW. Outputs are
- * written, not accumulated; M = 0 writes zeros to dW and db, N = 0 zeros to dx. For 16-bit types g is rounded to the
+ * written, not accumulated; M = 0 writes zeros to dW and db, N = 0 zeros to dx. For 16-bit types g may be rounded to the
  * element type where it enters the products (relu's and none's g is exact); db adds the unrounded g. */
 int vf_linear_grad(int dtype, int act, const void* dy, long long lddy, const void* z, long long ldz, const void* x,
                    long long ldx, const void* W, long long ldw, long long M, int N, int K, void* dx, long long lddx,
@@ -407,7 +407,7 @@ int vf_ops_check(void);
  * each (input and output alike; they may differ between gradients); norm [device] one float. scale >= 0 undoes a loss
  * scale (1 for none); max_norm >= 0, INFINITY to measure and scale only. outs[t] is grads[t] itself (in place) or
  * overlaps no gradient and no other output; overlaps are refused. A norm that is not finite clips nothing: the gradients
- * are scaled by `scale` alone and *norm reports it. Squares are summed in fp64 beyond 32 terms, with
+ * are scaled by `scale` alone and *norm reports it. Squares are summed in fp64 beyond 16 terms, with
  * no overflow or underflow for finite elements. The slope gradients of vf_alpha_grad and vf_alpha_beta_grad and the
  * weight gradients of vf_linear_grad are the intended input. The workspace is vf_clip_workspace(n) bytes (of
  * the current device). */

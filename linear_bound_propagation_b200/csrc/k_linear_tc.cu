@@ -1061,7 +1061,7 @@ Plan plan(const Extents& x, bool f32, bool parts, int sms) {
     for (int bn = 16; bn <= 256; bn *= 2) {
         if (bn < 64 && (mn || J > bn)) continue;
         if (bn > 64 && (J <= bn / 2 || (bn == 256 && I <= BM))) continue;
-        const int cg = bn == 256 ? 2 : 1, slots = sms, workers = slots / cg;
+        const int cg = bn == 256 ? 2 : 1, workers = sms / cg;
         auto tiles_of = [&](int k) { return (x.I[k] + BM * cg - 1) / (BM * cg) * ((x.J[k] + bn - 1) / bn); };
         auto consider = [&](int split, const int (&plog)[2]) {
             double total = 0, longest = 0, join = 0;
@@ -1090,7 +1090,7 @@ Plan plan(const Extents& x, bool f32, bool parts, int sms) {
             load += tile_cycles(x.nk[k], f32, bn) * tiles_of(k) / workers;
         }
         for (int split = 1; split <= 8; split *= 2) {
-            if (split > 1 && (cg > 1 || tiles * split > slots || min_nk < 4 * split)) break;
+            if (split > 1 && (cg > 1 || tiles * split > sms || min_nk < 4 * split)) break;
             consider(split, {0, 0});
         }
         if (parts) {
@@ -1218,7 +1218,6 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
     // suggest).
     P.split = 1;
     P.split_log = 0;
-    const int slots = sms;
     while (CG == 1 && P.split < split) {
         at[0].val.clusterDim.x = P.split * 2;
         cfg.numAttrs = 1;
@@ -1230,7 +1229,7 @@ cudaError_t launch_bn(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
         ++P.split_log;
     }
     P.test_stall = getenv("VF_TEST_OPS_STALL") != nullptr;
-    P.workers = (int)std::min<long long>(tiles, P.split > 1 ? tiles : slots / CG);
+    P.workers = (int)std::min<long long>(tiles, P.split > 1 ? tiles : sms / CG);
     if (tiles == 0) P.workers = std::min((P.N + 127) / 128, sms);
     P.gap = 1;
     if (P.split == 1 && count == 2) {

@@ -102,7 +102,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
                  : "memory");
 }
 
-// Bounded wait like mbar_wait, without the suspend-time hint: with it a waiting warp woke late.
+// Bounded wait like mbar_wait, without its suspend-time hint: the roles wait for one another every few hundred cycles.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
     if (mbar_test(bar, parity)) return true;
     const long long t0 = clock64();
