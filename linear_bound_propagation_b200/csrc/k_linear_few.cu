@@ -1,18 +1,20 @@
-// Backward pass of the dense layer for a few rows on the FFMA units: up to eight of fp32, up to four of 16 bits.
+// Backward pass of the dense layer for a few rows on the FFMA units: up to 16 of fp32, up to eight of 16 bits.
 //
 // With so few rows the pass is W read once (dx = g W) and dW written once (dW = g^T x): 2 N K elements against 4 M N K
-// operations, bound by memory. A block takes a slab of rows n and a chunk of columns k of one of the two; g of the slab
-// is formed in shared memory (fp32, not rounded), a warp passes over the slab's rows with its accumulators (or its part of
-// x) in registers. dx of a slab is a partial sum; a second launch adds the slabs in a fixed order. db and dr come from the
-// first chunk's blocks. One block for both products kept W's loads waiting behind twice the registers: 8 x 4096 x 4096
-// bf16 52 us, apart 36 us.
+// operations, bound by memory and, from eight rows on, by the FFMA units. A block takes a slab of rows n and a chunk of
+// columns k of one of the two; g of the slab is formed in shared memory (fp32, not rounded), a warp passes over the slab's
+// rows with its accumulators (or its part of x) in registers. dx of a slab is a partial sum; a second launch adds the slabs
+// in a fixed order. db and dr come from the first chunk's blocks. One block for both products kept W's loads waiting behind
+// twice the registers: 8 x 4096 x 4096 bf16 52 us, apart 36 us; with the inputs' g together in shared memory (a load for
+// four of them) and the blocks chosen below 24.7 us.
 //
-// Measured here and on the tensor cores (k_linear_tc.cu), which pad the rows to 16, M x 4096 x 4096 with relu in us:
-//   bf16   1: 15.9 and 29.0   2: 16.5 and 29.3   4: 22.2 and 28.4   5: 32.2 and 28.6   8: 35.9 and 28.8
-//   fp32   1: 26.7 and 91.4   4: 34.4 and 91.2   8: 46.2 and 91.3
-// so eight rows of fp32 and four of 16 bits stay here. One row of fp32: 2 N K elements in 26.7 us, 5.0 TB/s.
+// Measured here and on the tensor cores (k_linear_tc.cu), which pad the rows to 16, with relu in us:
+//   bf16   x 4096 x 4096   1: 12.4 and 28.7   4: 14.4 and 28.4   8: 24.7 and 28.5   8 x 1024 x 1024: 7.6 and 9.7
+//   fp32   x 4096 x 4096   1: 23.6 and 85.9   8: 35.3 and 85.9  16: 57.0 and 86.8  16 x 1024 x 1024: 9.9 and 12.9
+// One row: 2 N K elements in 23.6 us (fp32, 5.7 TB/s) and 12.4 us (bf16, 5.4 TB/s).
 #include <algorithm>
 
+#include "linear_tc.cuh"
 #include "vf_internal.cuh"
 #include "vf_ops.cuh"
 
@@ -21,8 +23,15 @@ namespace vf {
 namespace {
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
-constexpr int max_rows(int elem) { return elem == 4 ? 8 : 4; }
-constexpr int MAX_SLAB = 1024;  // rows of g in shared memory: 32 KB for eight rows of inputs
+constexpr int max_rows(int elem) { return elem == 4 ? 16 : 8; }
+// Columns of g in shared memory, 32 KB of them at most for `rows` rows of inputs (a power of two).
+constexpr int max_slab(int rows) { return 8192 / rows; }
+// M rounded up to what the kernel is built for.
+int rows_built(int M) {
+    int r = 1;
+    while (r < M) r *= 2;
+    return r;
+}
 
 struct FewParams {
     const void *dy, *z, *x, *W;
@@ -60,13 +69,46 @@ __device__ __forceinline__ void store_row(T* p, const float (&v)[VEC]) {
     }
 }
 
+// g of one row of W, all MB inputs: they lie together in shared memory, so that a warp gets four of them per load.
+template <int MB>
+__device__ __forceinline__ void load_g(const float* p, float (&v)[MB]) {
+    if constexpr (MB >= 4) {
+#pragma unroll
+        for (int m = 0; m < MB; m += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(p + m);
+            v[m] = q.x, v[m + 1] = q.y, v[m + 2] = q.z, v[m + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < MB; ++m) v[m] = p[m];
+    }
+}
+template <int MB>
+__device__ __forceinline__ void store_g(float* p, const float (&v)[MB]) {
+    if constexpr (MB >= 4) {
+#pragma unroll
+        for (int m = 0; m < MB; m += 4) *reinterpret_cast<float4*>(p + m) = make_float4(v[m], v[m + 1], v[m + 2], v[m + 3]);
+    } else {
+#pragma unroll
+        for (int m = 0; m < MB; ++m) p[m] = v[m];
+    }
+}
+
+// Inputs whose partial sums of dx the warps of a block join at a time: 16 KB of shared memory at most.
+template <int VEC, int MB>
+constexpr int join_rows() {
+    return VEC == 8 ? (MB < 2 ? MB : 2) : (MB < 4 ? MB : 4);
+}
+
 template <typename T, int VEC, int MB>
-__global__ void __launch_bounds__(THREADS) linear_few_grad_k(const __grid_constant__ FewParams P) {
-    extern __shared__ float g[];  // [MB][slab], then [WARPS][32 * VEC] for the sum over the warps
+__global__ void __launch_bounds__(THREADS, MB * VEC >= 64 || MB == 16 ? 2 : 1)
+linear_few_grad_k(const __grid_constant__ FewParams P) {
+    extern __shared__ __align__(16) float g[];  // [slab][MB], then [join_rows][WARPS][32 * VEC] for the sum over the warps
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int k = (blockIdx.x * 32 + lane) * VEC;
     const int n0 = blockIdx.y * P.slab, rows = min(P.slab, P.N - n0);
     const bool is_dx = (int)blockIdx.z == P.dx_z, first = !is_dx && blockIdx.x == 0;
+    lin::grid_trigger();
     for (int i = threadIdx.x; i < rows; i += THREADS) {
         float v[MB], sum = 0.f;
 #pragma unroll
@@ -80,10 +122,10 @@ __global__ void __launch_bounds__(THREADS) linear_few_grad_k(const __grid_consta
         }
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            g[m * P.slab + i] = v[m];
             sum += v[m];
             if (first && P.dr != nullptr && m < P.M) ((T*)P.dr)[m * P.lddr + n0 + i] = from_f32<T>(v[m]);
         }
+        store_g<MB>(g + i * MB, v);
         if (first && P.db != nullptr) ((T*)P.db)[n0 + i] = from_f32<T>(sum);
     }
     __syncthreads();
@@ -93,33 +135,36 @@ __global__ void __launch_bounds__(THREADS) linear_few_grad_k(const __grid_consta
             const T* W = (const T*)P.W + (long long)n0 * P.ldw + k;
 #pragma unroll 4
             for (int r = warp; r < rows; r += WARPS) {
-                float w[VEC];
+                float w[VEC], gr[MB];
                 load_row<T, VEC>(W + (long long)r * P.ldw, w);
+                load_g<MB>(g + r * MB, gr);
 #pragma unroll
-                for (int m = 0; m < MB; ++m) {
-                    const float gm = g[m * P.slab + r];
+                for (int m = 0; m < MB; ++m)
 #pragma unroll
-                    for (int u = 0; u < VEC; ++u) acc[m][u] = fmaf(gm, w[u], acc[m][u]);
-                }
+                    for (int u = 0; u < VEC; ++u) acc[m][u] = fmaf(gr[m], w[u], acc[m][u]);
             }
         }
+        constexpr int R = join_rows<VEC, MB>(), COLS = 32 * VEC;
         float* red = g + MB * P.slab;
 #pragma unroll
-        for (int m = 0; m < MB; ++m) {
-            if (m >= P.M) break;
+        for (int m0 = 0; m0 < MB; m0 += R) {
+            if (m0 >= P.M) break;
             __syncthreads();
 #pragma unroll
-            for (int u = 0; u < VEC; ++u) red[(warp * 32 + lane) * VEC + u] = acc[m][u];
+            for (int m = 0; m < R; ++m)
+#pragma unroll
+                for (int u = 0; u < VEC; ++u) red[(m * WARPS + warp) * COLS + lane * VEC + u] = acc[m0 + m][u];
             __syncthreads();
-            const int c = blockIdx.x * 32 * VEC + threadIdx.x;
-            if (threadIdx.x < 32 * VEC && c < P.K) {
+            for (int e = threadIdx.x; e < R * COLS; e += THREADS) {
+                const int m = e / COLS, c = blockIdx.x * COLS + e % COLS;
+                if (m0 + m >= P.M || c >= P.K) continue;
                 float s = 0.f;
 #pragma unroll
-                for (int t = 0; t < WARPS; ++t) s += red[t * 32 * VEC + threadIdx.x];
+                for (int t = 0; t < WARPS; ++t) s += red[(m * WARPS + t) * COLS + e % COLS];
                 if (P.part != nullptr)
-                    P.part[((long long)blockIdx.y * P.M + m) * P.K + c] = s;
+                    P.part[((long long)blockIdx.y * P.M + m0 + m) * P.K + c] = s;
                 else
-                    ((T*)P.dx)[m * P.lddx + c] = from_f32<T>(s);
+                    ((T*)P.dx)[(m0 + m) * P.lddx + c] = from_f32<T>(s);
             }
         }
     } else if (P.dW != nullptr && k < P.K) {
@@ -129,13 +174,13 @@ __global__ void __launch_bounds__(THREADS) linear_few_grad_k(const __grid_consta
         T* dW = (T*)P.dW + (long long)n0 * P.lddw + k;
 #pragma unroll 2
         for (int r = warp; r < rows; r += WARPS) {
-            float d[VEC] = {};
+            float d[VEC] = {}, gr[MB];
+            load_g<MB>(g + r * MB, gr);
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
                 if (m >= P.M) break;  // x of a row that does not exist may be infinite
-                const float gm = g[m * P.slab + r];
 #pragma unroll
-                for (int u = 0; u < VEC; ++u) d[u] = fmaf(gm, x[m][u], d[u]);
+                for (int u = 0; u < VEC; ++u) d[u] = fmaf(gr[m], x[m][u], d[u]);
             }
             store_row<T, VEC>(dW + (long long)r * P.lddw, d);
         }
@@ -145,6 +190,7 @@ __global__ void __launch_bounds__(THREADS) linear_few_grad_k(const __grid_consta
 template <typename T>
 __global__ void __launch_bounds__(THREADS)
 linear_few_join_k(const float* part, int slabs, int M, int K, T* dx, long long lddx) {
+    lin::grid_wait();
     const long long i = (long long)blockIdx.x * THREADS + threadIdx.x, n = (long long)M * K;
     if (i >= n) return;
     float s = 0.f;
@@ -157,13 +203,17 @@ struct Shape {
     int chunks, slab, slabs;
 };
 
-// Chunks of 32 vectors. Slabs: enough blocks to fill the SMs a few times over, but four rows a warp at least, and
-// partial sums of dx (fp32, M rows a slab) of no more than about a quarter of W's bytes.
+// Chunks of 32 vectors. Slabs: as many blocks for each product as lie beside each other on the SMs at the kernel's registers,
+// but four rows a warp at least, and partial sums of dx (fp32, M rows a slab) of no more than about a quarter of W's bytes.
+// M x 4096 x 4096 with 148, 296 and 592 blocks, us:
+//   fp32   1: 37.3 27.5 23.6   2: 36.5 26.9 27.9   8: 40.0 35.3 39.8   12 x 1024 x 1024: 10.5 14.4 14.4
+//   bf16   1: 12.4 12.8 17.0   4: 14.4 18.2 20.6   8: 24.7 27.9 34.9
 Shape shape_of(int M, int N, int K, int vec, int elem) {
     Shape s;
     s.chunks = (K + 32 * vec - 1) / (32 * vec);
-    const int want = std::min({(592 + s.chunks - 1) / s.chunks, (N + 4 * WARPS - 1) / (4 * WARPS), std::max(1, (int)((long long)N * elem / (16 * M)))});
-    s.slab = std::min(MAX_SLAB, (N + want - 1) / want);
+    const int blocks = elem == 2 || M > 8 ? 148 : M > 1 ? 296 : 592;
+    const int want = std::min({std::max(1, blocks / s.chunks), (N + 4 * WARPS - 1) / (4 * WARPS), std::max(1, (int)((long long)N * elem / (16 * M)))});
+    s.slab = std::min(max_slab(rows_built(M)), (N + want - 1) / want);
     s.slabs = (N + s.slab - 1) / s.slab;
     return s;
 }
@@ -175,7 +225,7 @@ bool rows_of(const void* p, long long ld, int vec) {
 
 template <typename T, int VEC, int MB>
 cudaError_t launch_mb(const FewParams& P, const Shape& s, cudaStream_t st) {
-    const size_t smem = ((size_t)MB * s.slab + THREADS * VEC) * sizeof(float);
+    const size_t smem = ((size_t)MB * s.slab + join_rows<VEC, MB>() * THREADS * VEC) * sizeof(float);
     const bool other = P.dW != nullptr || P.db != nullptr || P.dr != nullptr;
     if (P.dx == nullptr && !other) return cudaSuccess;
     linear_few_grad_k<T, VEC, MB><<<dim3(s.chunks, s.slabs, (P.dx != nullptr) + other), THREADS, smem, st>>>(P);
@@ -191,18 +241,24 @@ cudaError_t launch_vec(const LinearGrad& f, FewParams& P, float* work, size_t ha
     if (*need > have) return cudaSuccess;  // the caller reports it
     P.part = *need > 0 ? work : nullptr;
     cudaError_t e;
-    if (f.M == 1)
-        e = launch_mb<T, VEC, 1>(P, s, st);
-    else if (f.M == 2)
-        e = launch_mb<T, VEC, 2>(P, s, st);
-    else if (max_rows(sizeof(T)) == 4 || f.M <= 4)
-        e = launch_mb<T, VEC, 4>(P, s, st);
-    else
-        e = launch_mb<T, VEC, max_rows(sizeof(T))>(P, s, st);
+    switch (rows_built((int)f.M)) {
+        case 1: e = launch_mb<T, VEC, 1>(P, s, st); break;
+        case 2: e = launch_mb<T, VEC, 2>(P, s, st); break;
+        case 4: e = launch_mb<T, VEC, 4>(P, s, st); break;
+        case 8: e = launch_mb<T, VEC, 8>(P, s, st); break;
+        default: e = launch_mb<T, VEC, max_rows(sizeof(T))>(P, s, st);  // 16, fp32 only
+    }
     if (e != cudaSuccess || P.part == nullptr) return e;
-    linear_few_join_k<T><<<(unsigned)((f.M * f.K + THREADS - 1) / THREADS), THREADS, 0, st>>>(P.part, s.slabs, (int)f.M, f.K,
-                                                                                             (T*)f.dx, f.lddx);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    cfg.gridDim = dim3((unsigned)((f.M * f.K + THREADS - 1) / THREADS));
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = st;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, linear_few_join_k<T>, (const float*)P.part, s.slabs, (int)f.M, f.K, (T*)f.dx, f.lddx);
 }
 
 template <typename T>
@@ -218,7 +274,8 @@ cudaError_t launch_few(const LinearGrad& f, float* work, size_t have, size_t* ne
 }  // namespace
 
 bool linear_few_supported(int dtype, long long M, int N, int K) {
-    return M >= 1 && M <= max_rows(dtype == VF_F32 ? 4 : 2) && N >= 1 && K >= 1 && (long long)N <= 65535LL * MAX_SLAB;
+    return M >= 1 && M <= max_rows(dtype == VF_F32 ? 4 : 2) && N >= 1 && K >= 1 &&
+           (long long)N <= 65535LL * max_slab(rows_built((int)M));
 }
 
 size_t linear_few_workspace(int dtype, long long M, int N, int K) {

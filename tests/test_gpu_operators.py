@@ -258,6 +258,23 @@ def test_workspace_is_checked_before_anything_runs():
     assert (dW == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M", [2, 4, 5, 8, 9, 13, 16, 17])
+@pytest.mark.parametrize("N,K,pad", [(1, 129, 0), (517, 36, 4), (4099, 264, 8), (2050, 515, 1)])
+def test_backward_of_a_few_rows_is_exact_on_whole_numbers(dtype, M, N, K, pad):
+    """Every sum is a whole number below 2^24, so fp32 holds it and one rounding remains. Nothing is written behind a row."""
+    gen = torch.Generator(device="cuda").manual_seed(M * 7 + N)
+
+    def whole(rows, cols):
+        return torch.randint(-3, 4, (rows, cols + pad), generator=gen, device="cuda").to(dtype)[:, :cols]
+
+    dy, z, x, W = whole(M, N), whole(M, N), whole(M, K), whole(N, K)
+    g = dy.double() * (z > 0)
+    got = vf.linear_grad(dy, x, W, act="relu", z=z, need=("dx", "dW", "db", "dr"))
+    for name, want in (("dx", g @ W.double()), ("dW", g.t() @ x.double()), ("db", g.sum(0)), ("dr", g)):
+        assert torch.equal(got[name], want.to(dtype)), name
+
+
 @pytest.mark.parametrize("pad_x,pad_w", [(0, 0), (0, 1), (1, 0), (1, 1)])
 def test_alignment_changes_the_kernel_not_the_result(pad_x, pad_w):
     """One wave of tiles in fp32: rows of 16-byte alignment need no workspace, others may go through a laid-out copy.
