@@ -1,5 +1,6 @@
-// Backward pass of the dense layer for a few rows on the FFMA units: up to 16 of fp32, up to eight of 16 bits.
+// The dense layer for a few rows on the FFMA units: forward for up to eight, backward for up to 16 of fp32 and eight of 16 bits.
 //
+// Backward.
 // With so few rows the pass is W read once (dx = g W) and dW written once (dW = g^T x): 2 N K elements against 4 M N K
 // operations, bound by memory and, from eight rows on, by the FFMA units. A block takes a slab of rows n and a chunk of
 // columns k of one of the two; g of the slab is formed in shared memory (fp32, not rounded), a warp passes over the slab's
@@ -271,7 +272,116 @@ cudaError_t launch_few(const LinearGrad& f, float* work, size_t have, size_t* ne
     return vec ? launch_vec<T, V>(f, P, work, have, need, st) : launch_vec<T, 1>(f, P, work, have, need, st);
 }
 
+// ------------------------------------------------------------------------------------------------------- --- forward
+
+constexpr int ROWS = 4;  // rows of W per block
+
+// y = act(x W^T + b + r) for M <= MB rows of x: W is read once, 2 M operations for each element, so memory bounds it. A block
+// takes four rows of W, its warps share the reduction; a lane's part of x, loaded from L1, serves the four rows, and the next
+// step's part of W is on its way meanwhile. Sums are fp32 in a fixed order. 1 x 4096 x 4096 fp32 7.8 us out of L2.
+template <typename T, int VEC, int MB>
+__global__ void __launch_bounds__(THREADS, 2) linear_few_k(const __grid_constant__ LinearFwd f) {
+    constexpr int C = MB * ROWS;
+    __shared__ float part[WARPS][C];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, M = (int)f.M;
+    const long long n0 = (long long)blockIdx.x * ROWS;
+    const T* w[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) w[r] = (const T*)f.W + min(n0 + r, f.N - 1LL) * f.ldw;
+    float acc[C] = {}, a[ROWS][VEC] = {}, b[ROWS][VEC] = {};  // acc[m * ROWS + r]
+    long long k = (long long)threadIdx.x * VEC;
+    if (k < f.K)
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) load_row<T, VEC>(w[r] + k, a[r]);
+    while (k < f.K) {
+        const T* x = (const T*)f.x + k;
+        k += THREADS * VEC;
+        if (k < f.K)
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) load_row<T, VEC>(w[r] + k, b[r]);
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+            float v[VEC];
+            load_row<T, VEC>(x, v);
+            if (m + 1 < M) x += f.ldx;  // rows that do not exist repeat the last; their sums are not stored
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                for (int u = 0; u < VEC; ++u) acc[m * ROWS + r] = fmaf(v[u], a[r][u], acc[m * ROWS + r]);
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int u = 0; u < VEC; ++u) a[r][u] = b[r][u];
+    }
+    // Sums over the lanes: at each step a lane hands half of its sums to its partner, until each has one or two finished.
+    int first = 0, c = C;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        if (c > 1) {
+            c /= 2;
+            const bool upper = (lane & o) != 0;
+            first += upper ? c : 0;
+#pragma unroll
+            for (int i = 0; i < C / 2; ++i)
+                if (i < c) {
+                    const float give = upper ? acc[i] : acc[i + c], keep = upper ? acc[i + c] : acc[i];
+                    acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+        } else {
+            acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < (C > 32 ? 2 : 1); ++i) part[warp][first + i] = acc[i];  // lanes of one sum hold the same
+    __syncthreads();
+    const int m = threadIdx.x / ROWS;
+    const long long n = n0 + threadIdx.x % ROWS;
+    if (m >= M || n >= f.N) return;
+    float z = 0.f;
+#pragma unroll
+    for (int t = 0; t < WARPS; ++t) z += part[t][threadIdx.x];
+    if (f.b != nullptr) z += to_f32(((const T*)f.b)[n]);
+    if (f.r != nullptr) z += to_f32(((const T*)f.r)[m * f.ldr + n]);
+    if (f.z != nullptr) ((T*)f.z)[m * f.ldz + n] = from_f32<T>(z);
+    ((T*)f.y)[m * f.ldy + n] = from_f32<T>(act_value<sizeof(T) == 2>(z, f.act));
+}
+
+template <typename T, int VEC>
+cudaError_t launch_rows(const LinearFwd& f, cudaStream_t s) {
+    const unsigned grid = (unsigned)((f.N + ROWS - 1LL) / ROWS);
+    switch (rows_built((int)f.M)) {
+        case 1: linear_few_k<T, VEC, 1><<<grid, THREADS, 0, s>>>(f); break;
+        case 2: linear_few_k<T, VEC, 2><<<grid, THREADS, 0, s>>>(f); break;
+        case 4: linear_few_k<T, VEC, 4><<<grid, THREADS, 0, s>>>(f); break;
+        default: linear_few_k<T, VEC, 8><<<grid, THREADS, 0, s>>>(f);
+    }
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_few_forward(const LinearFwd& f, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    const bool vec = f.K % V == 0 && rows_of<T>(f.x, f.ldx, V) && rows_of<T>(f.W, f.ldw, V);
+    return vec ? launch_rows<T, V>(f, s) : launch_rows<T, 1>(f, s);
+}
+
 }  // namespace
+
+// Up to eight rows. M x N x K, us here and on the tensor cores (k_linear_direct.cu for fp32, k_linear_tc.cu for 16 bits, replayed
+// from a graph, W in L2): fp32 1x1024x1024 2.5 and 6.8, 1x4096x4096 7.8 and 19.6, 8x4096x4096 15.4 and 19.6, 16x4096x4096 48.8
+// and 19.5; bf16 1x1024x1024 2.5 and 5.6, 8x1024x4096 6.1 and 6.8, rows without alignment 8x1021x1023 4.4 and 7.3, but with
+// more blocks than two per SM 1x4096x1024 6.0 and 5.8, 8x4096x4096 17.5 and 8.4.
+bool linear_few_forward(int dtype, long long M, int N, int K, bool in_place) {
+    return M >= 1 && M <= 8 && N >= 1 && K >= 1 && (dtype == VF_F32 || !in_place || N <= 148 * 2 * ROWS);
+}
+
+cudaError_t launch_linear_few(const LinearFwd& f, cudaStream_t s) {
+    switch (f.dtype) {
+        case VF_F32: return launch_few_forward<float>(f, s);
+        case VF_BF16: return launch_few_forward<__nv_bfloat16>(f, s);
+        default: return launch_few_forward<__half>(f, s);
+    }
+}
 
 bool linear_few_supported(int dtype, long long M, int N, int K) {
     return M >= 1 && M <= max_rows(dtype == VF_F32 ? 4 : 2) && N >= 1 && K >= 1 &&

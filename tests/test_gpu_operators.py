@@ -275,6 +275,26 @@ def test_backward_of_a_few_rows_is_exact_on_whole_numbers(dtype, M, N, K, pad):
         assert torch.equal(got[name], want.to(dtype)), name
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M", [1, 2, 3, 5, 8, 9])
+@pytest.mark.parametrize("N,K,pad", [(1, 1, 0), (6, 33, 0), (1183, 264, 8), (1190, 2056, 0), (130, 1030, 1), (4097, 8, 8)])
+def test_forward_of_a_few_rows_is_exact_on_whole_numbers(dtype, M, N, K, pad):
+    """As above, with bias and z, the output in the residual's place; what lies beside and behind it stays."""
+    gen = torch.Generator(device="cuda").manual_seed(M * 5 + N)
+
+    def whole(rows, cols):
+        return torch.randint(-3, 4, (rows, cols + pad), generator=gen, device="cuda").to(dtype)[:, :cols]
+
+    x, W, b = whole(M, K), whole(N, K), whole(1, N + 8)[0, :N].contiguous()
+    buf = torch.randint(-3, 4, (M + 1, N + 3), generator=gen, device="cuda").to(dtype)
+    before, r = buf.clone(), buf[:M, :N]
+    want = x.double() @ W.double().t() + b.double() + r.double()
+    got = vf.linear(x, W, b, residual=r, act="relu", want_z=True, out=r)
+    assert torch.equal(got["z"], want.to(dtype))
+    assert torch.equal(r, want.clamp(min=0).to(dtype))
+    assert torch.equal(buf[M], before[M]) and torch.equal(buf[:, N:], before[:, N:])
+
+
 @pytest.mark.parametrize("pad_x,pad_w", [(0, 0), (0, 1), (1, 0), (1, 1)])
 def test_alignment_changes_the_kernel_not_the_result(pad_x, pad_w):
     """One wave of tiles in fp32: rows of 16-byte alignment need no workspace, others may go through a laid-out copy.
