@@ -276,26 +276,28 @@ cudaError_t launch_few(const LinearGrad& f, float* work, size_t have, size_t* ne
 
 constexpr int ROWS = 4;  // rows of W per block
 
-// y = act(x W^T + b + r) for M <= MB rows of x: W is read once, 2 M operations for each element, so memory bounds it. A block
-// takes four rows of W, its warps share the reduction; a lane's part of x, loaded from L1, serves the four rows, and the next
-// step's part of W is on its way meanwhile. Sums are fp32 in a fixed order. 1 x 4096 x 4096 fp32 7.8 us out of L2.
+// y = act(x W^T + b + r) for M <= MB rows of x: W is read once, 2 M operations for each element, so memory bounds it. A group
+// of warps takes four rows of W and shares the reduction; a lane's part of x, loaded from L1, serves the four rows, and the
+// next step's part of W is on its way meanwhile. Sums are fp32 in a fixed order. 1 x 4096 x 4096 fp32 7.8 us out of L2.
 template <typename T, int VEC, int MB>
-__global__ void __launch_bounds__(THREADS, 2) linear_few_k(const __grid_constant__ LinearFwd f) {
+__global__ void __launch_bounds__(THREADS, 2) linear_few_k(const __grid_constant__ LinearFwd f, int glog) {
     constexpr int C = MB * ROWS;
     __shared__ float part[WARPS][C];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, M = (int)f.M;
-    const long long n0 = (long long)blockIdx.x * ROWS;
+    // 2^glog warps share the reduction of four rows
+    const int group = warp >> glog, share = warp & ((1 << glog) - 1), step = (32 << glog) * VEC;
+    const long long n0 = (((long long)blockIdx.x << (3 - glog)) + group) * ROWS;
     const T* w[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) w[r] = (const T*)f.W + min(n0 + r, f.N - 1LL) * f.ldw;
     float acc[C] = {}, a[ROWS][VEC] = {}, b[ROWS][VEC] = {};  // acc[m * ROWS + r]
-    long long k = (long long)threadIdx.x * VEC;
+    long long k = (share * 32 + lane) * VEC;
     if (k < f.K)
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) load_row<T, VEC>(w[r] + k, a[r]);
     while (k < f.K) {
         const T* x = (const T*)f.x + k;
-        k += THREADS * VEC;
+        k += step;
         if (k < f.K)
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) load_row<T, VEC>(w[r] + k, b[r]);
@@ -335,26 +337,30 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_k(const __grid_constant
 #pragma unroll
     for (int i = 0; i < (C > 32 ? 2 : 1); ++i) part[warp][first + i] = acc[i];  // lanes of one sum hold the same
     __syncthreads();
-    const int m = threadIdx.x / ROWS;
-    const long long n = n0 + threadIdx.x % ROWS;
-    if (m >= M || n >= f.N) return;
+    const int g = threadIdx.x / C, m = threadIdx.x % C / ROWS;
+    const long long n = (((long long)blockIdx.x << (3 - glog)) + g) * ROWS + threadIdx.x % ROWS;
+    if (g >= WARPS >> glog || m >= M || n >= f.N) return;
     float z = 0.f;
-#pragma unroll
-    for (int t = 0; t < WARPS; ++t) z += part[t][threadIdx.x];
+    for (int t = 0; t < 1 << glog; ++t) z += part[(g << glog) + t][threadIdx.x % C];
     if (f.b != nullptr) z += to_f32(((const T*)f.b)[n]);
     if (f.r != nullptr) z += to_f32(((const T*)f.r)[m * f.ldr + n]);
     if (f.z != nullptr) ((T*)f.z)[m * f.ldz + n] = from_f32<T>(z);
     ((T*)f.y)[m * f.ldy + n] = from_f32<T>(act_value<sizeof(T) == 2>(z, f.act));
 }
 
+// All eight warps share a reduction, or fewer where there would be more than two blocks per SM and a warp fewer than four steps:
+// 1 x 4096 x 1024 bf16 6.0 us with eight, 3.7 us with two; 8 x 4096 x 4096 fp32 15.4 us with eight, 18.7 us with two.
 template <typename T, int VEC>
 cudaError_t launch_rows(const LinearFwd& f, cudaStream_t s) {
-    const unsigned grid = (unsigned)((f.N + ROWS - 1LL) / ROWS);
+    const long long rows = (f.N + ROWS - 1LL) / ROWS;
+    int glog = 3;
+    while (glog > 0 && ((rows << glog) + WARPS - 1) / WARPS > 148 * 2 && f.K < 4 * (32 << glog) * VEC) --glog;
+    const unsigned grid = (unsigned)(((rows << glog) + WARPS - 1) / WARPS);
     switch (rows_built((int)f.M)) {
-        case 1: linear_few_k<T, VEC, 1><<<grid, THREADS, 0, s>>>(f); break;
-        case 2: linear_few_k<T, VEC, 2><<<grid, THREADS, 0, s>>>(f); break;
-        case 4: linear_few_k<T, VEC, 4><<<grid, THREADS, 0, s>>>(f); break;
-        default: linear_few_k<T, VEC, 8><<<grid, THREADS, 0, s>>>(f);
+        case 1: linear_few_k<T, VEC, 1><<<grid, THREADS, 0, s>>>(f, glog); break;
+        case 2: linear_few_k<T, VEC, 2><<<grid, THREADS, 0, s>>>(f, glog); break;
+        case 4: linear_few_k<T, VEC, 4><<<grid, THREADS, 0, s>>>(f, glog); break;
+        default: linear_few_k<T, VEC, 8><<<grid, THREADS, 0, s>>>(f, glog);
     }
     return cudaGetLastError();
 }
@@ -367,12 +373,13 @@ cudaError_t launch_few_forward(const LinearFwd& f, cudaStream_t s) {
 
 }  // namespace
 
-// Up to eight rows. M x N x K, us here and on the tensor cores (k_linear_direct.cu for fp32, k_linear_tc.cu for 16 bits, replayed
-// from a graph, W in L2): fp32 1x1024x1024 2.5 and 6.8, 1x4096x4096 7.8 and 19.6, 8x4096x4096 15.4 and 19.6, 16x4096x4096 48.8
-// and 19.5; bf16 1x1024x1024 2.5 and 5.6, 8x1024x4096 6.1 and 6.8, rows without alignment 8x1021x1023 4.4 and 7.3, but with
-// more blocks than two per SM 1x4096x1024 6.0 and 5.8, 8x4096x4096 17.5 and 8.4.
-bool linear_few_forward(int dtype, long long M, int N, int K, bool in_place) {
-    return M >= 1 && M <= 8 && N >= 1 && K >= 1 && (dtype == VF_F32 || !in_place || N <= 148 * 2 * ROWS);
+// Up to eight rows, in 16 bits up to 2^24 multiplications. M x N x K, us here and on the tensor cores (k_linear_direct.cu for
+// fp32, k_linear_tc.cu for 16 bits; replayed from a graph, W in L2):
+//   fp32  1x1024x1024 2.5 and 6.8   1x4096x4096 7.8 and 19.6   8x4096x4096 15.4 and 19.6   16x4096x4096 48.8 and 19.5
+//   bf16  1x1024x1024 2.7 and 5.7   1x4096x1024 3.8 and 5.8   1x4096x4096 9.0 and 8.4   8x2048x1024 4.4 and 5.8
+//         2x4096x4096 9.9 and 8.5   8x4096x1024 6.2 and 5.8   8x4096x4096 16.9 and 8.3
+bool linear_few_forward(int dtype, long long M, int N, int K) {
+    return M >= 1 && M <= 8 && N >= 1 && K >= 1 && (dtype == VF_F32 || (double)M * N * K <= 16777216.0);
 }
 
 cudaError_t launch_linear_few(const LinearFwd& f, cudaStream_t s) {

@@ -151,7 +151,7 @@ int vf_linear_workspace(int dtype, long long M, int N, int K, int grad, size_t* 
         if (grad < 0 || grad > VF_FORWARD_ALIGNED) return ops_fail(VF_ERR_ARG, "grad = %d", grad);
         if (grad == 1 && linear_few_supported(dtype, M, N, K))
             *bytes = linear_few_workspace(dtype, M, N, K);
-        else if (!use_tc(M, N, K) || (grad != 1 && linear_few_forward(dtype, M, N, K, false)) ||
+        else if (!use_tc(M, N, K) || (grad != 1 && linear_few_forward(dtype, M, N, K)) ||
                  (aligned && (dtype != VF_F32 || linear_direct_fits(dtype, M, N, K, true, true))) ||
                  (grad == 0 && linear_direct_fits(dtype, M, N, K, false, false)))
             *bytes = 0;
@@ -175,7 +175,7 @@ int vf_linear(int dtype, int act, const void* x, long long ldx, const void* W, l
         OPS_TRY(check_matrix("y", y, M, N, ldy, dtype));
         if (z != nullptr) OPS_TRY(check_matrix("z", z, M, N, ldz, dtype));
         const LinearFwd p{dtype, act, x, ldx, W, ldw, b, r, ldr, M, N, K, y, ldy, z, ldz};
-        if (linear_few_forward(dtype, M, N, K, linear_tc_in_place(p))) return launched(launch_linear_few(p, (cudaStream_t)stream));
+        if (linear_few_forward(dtype, M, N, K)) return launched(launch_linear_few(p, (cudaStream_t)stream));
         if (!use_tc(M, N, K)) return launched(launch_linear_ffma(p, (cudaStream_t)stream));
         if (!linear_tc_in_place(p) && linear_direct_fits(dtype, M, N, K, aligned16(x, ldx, dtype), aligned16(W, ldw, dtype)))
             return launched(launch_linear_direct(p, (cudaStream_t)stream));

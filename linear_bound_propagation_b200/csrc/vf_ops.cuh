@@ -256,8 +256,8 @@ struct LinearGrad {
 cudaError_t launch_linear_ffma(const LinearFwd& p, cudaStream_t s);
 cudaError_t launch_linear_grad_ffma(const LinearGrad& p, cudaStream_t s);
 
-// A few rows, forward (k_linear_few.cu): any strides and alignment, no workspace. in_place: TMA can read x and W.
-bool linear_few_forward(int dtype, long long M, int N, int K, bool in_place);
+// A few rows, forward (k_linear_few.cu): any strides and alignment, no workspace.
+bool linear_few_forward(int dtype, long long M, int N, int K);
 cudaError_t launch_linear_few(const LinearFwd& p, cudaStream_t s);
 
 // Backward pass of a few rows (k_linear_few.cu); workspace as for the tensor-core launches below.
