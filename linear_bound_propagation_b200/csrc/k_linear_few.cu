@@ -272,9 +272,9 @@ cudaError_t launch_few(const LinearGrad& f, float* work, size_t have, size_t* ne
     return vec ? launch_vec<T, V>(f, P, work, have, need, st) : launch_vec<T, 1>(f, P, work, have, need, st);
 }
 
-// ------------------------------------------------------------------------------------------------------- --- forward
+// ------------------------------------------------------------------------------------------------------- forward
 
-constexpr int ROWS = 4;  // rows of W per block
+constexpr int ROWS = 4;  // rows of W per group of warps
 
 // y = act(x W^T + b + r) for M <= MB rows of x: W is read once, 2 M operations for each element, so memory bounds it. A group
 // of warps takes four rows of W and shares the reduction; a lane's part of x, loaded from L1, serves the four rows, and the
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_k(const __grid_constant
 #pragma unroll
             for (int u = 0; u < VEC; ++u) a[r][u] = b[r][u];
     }
-    // Sums over the lanes: at each step a lane hands half of its sums to its partner, until each has one or two finished.
+    // Sums over the lanes: at each step a lane hands half of its sums to its partner, until each has one.
     int first = 0, c = C;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -334,8 +334,8 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_k(const __grid_constant
             acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
         }
     }
-#pragma unroll
-    for (int i = 0; i < (C > 32 ? 2 : 1); ++i) part[warp][first + i] = acc[i];  // lanes of one sum hold the same
+    static_assert(C <= 32, "a lane ends with one sum");
+    part[warp][first] = acc[0];  // the lanes that share a sum hold the same
     __syncthreads();
     const int g = threadIdx.x / C, m = threadIdx.x % C / ROWS;
     const long long n = (((long long)blockIdx.x << (3 - glog)) + g) * ROWS + threadIdx.x % ROWS;
