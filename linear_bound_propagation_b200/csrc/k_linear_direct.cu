@@ -26,9 +26,11 @@ __device__ int g_direct_timeout;
 constexpr int BK = 64;             // steps of the reduction per block: 128-byte rows in shared memory
 constexpr int WORKERS = 512;       // loading and finishing threads
 constexpr int THREADS = WORKERS + 32;
-constexpr int CHUNK = 4;           // fp32: blocks added up in one accumulator (256 products, as k_linear_tc.cu)
-// fp32: accumulators of h h products, one after the other, all added in registers at the end; TMEM has 512 columns.
-constexpr int accumulators(int bn) { return bn == 64 ? 4 : 8; }
+// Blocks added up in one accumulator, as in k_linear_tc.cu.
+constexpr int chunk_blocks(int pl) { return (pl == 3 ? 256 : CHUNK_16) / BK; }
+// Accumulators (fp32: of h h products), one after the other, all added in registers at the end; TMEM has 512 columns, and fp32's small
+// products take one accumulator more.
+constexpr int accumulators(int pl, int bn) { return pl == 3 && bn == 64 ? 4 : 8; }
 
 // rows x Tn operand at p: element (r, t) at p[r * ld + t].
 struct Source {
@@ -141,8 +143,9 @@ template <typename T, int PL, int BN, bool VA, bool VB>
 __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_constant__ DirectParams P) {
     constexpr int A_PLANE = BM * 128, B_PLANE = BN * 128;
     constexpr int STAGE = direct_stage<PL, BN>();
-    constexpr int COR = accumulators(BN) * BN;                     // columns of the small products
-    constexpr int TMEM_COLS = PL == 3 ? (BN == 16 ? 256 : 512) : BN < 32 ? 32 : BN;
+    constexpr int CHUNK = chunk_blocks(PL);
+    constexpr int COR = accumulators(PL, BN) * BN;                 // columns of the small products
+    constexpr int TMEM_COLS = PL == 3 ? (BN == 16 ? 256 : 512) : COR;
     constexpr int FW = BN >= 32 ? 16 : 8;                          // finishing warps
     constexpr int PART = BN / (FW / 4);                            // columns of one
     constexpr int NA = BM * 8 / WORKERS;                           // times eight elements of A per thread
@@ -199,12 +202,12 @@ __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_const
                 tc_fence_after();
                 const uint64_t ah = a0 + (uint32_t)(g.slot * (STAGE / 16)), bh = b0 + (uint32_t)(g.slot * (STAGE / 16));
                 const int at = kb - kb0;
-                const uint32_t d = PL == 3 ? tmem + at / CHUNK * BN : tmem;
+                const uint32_t d = tmem + at / CHUNK * BN;
 #pragma unroll
                 for (int kk = 0; kk < BK / 16; ++kk) {
                     const uint64_t h = ah + kk * 2, H = bh + kk * 2;  // 32 bytes along a line
-                    const uint32_t more = at > 0 || kk > 0 ? 1u : 0u;
                     if (PL == 3) {
+                        const uint32_t more = at > 0 || kk > 0 ? 1u : 0u;
                         const uint64_t m = h + A_PLANE / 16, l = m + A_PLANE / 16;
                         const uint64_t M = H + B_PLANE / 16, L = M + B_PLANE / 16;
                         mma_f16_ss<1>(tmem + COR, l, H, idesc, more);
@@ -213,7 +216,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_const
                         mma_f16_ss<1>(tmem + COR, m, H, idesc, 1u);
                         mma_f16_ss<1>(tmem + COR, h, M, idesc, 1u);
                     }
-                    mma_f16_ss<1>(d, h, H, idesc, PL == 3 ? (at % CHUNK > 0 || kk > 0 ? 1u : 0u) : more);
+                    mma_f16_ss<1>(d, h, H, idesc, at % CHUNK > 0 || kk > 0 ? 1u : 0u);
                 }
                 mma_commit(&empty[g.slot]);
             }
@@ -267,19 +270,18 @@ __global__ void __launch_bounds__(THREADS, 1) linear_direct_k(const __grid_const
             for (int c = 0; c < PART; c += LD) {
                 uint32_t v[LD];
                 float o[LD];
-                tmem_ld<LD>(acc + (PL == 3 ? COR : 0) + c, v);
+                tmem_ld<LD>(acc + (PL == 3 ? COR : 0) + c, v);  // the small products, or the first accumulator
                 if (S == 1 && c + LD < PART) res_lane<T>(p, i, (long long)jw + c + LD, rn);
                 tmem_wait_ld();
 #pragma unroll
                 for (int k = 0; k < LD; ++k) o[k] = kb1 > kb0 ? __uint_as_float(v[k]) : 0.f;  // a share may hold no blocks
-                if (PL == 3)
 #pragma unroll 1
-                    for (int a = 0; a < (kb1 - kb0 + CHUNK - 1) / CHUNK; ++a) {
-                        tmem_ld<LD>(acc + a * BN + c, v);
-                        tmem_wait_ld();
+                for (int a = PL == 3 ? 0 : 1; a < (kb1 - kb0 + CHUNK - 1) / CHUNK; ++a) {
+                    tmem_ld<LD>(acc + a * BN + c, v);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < LD; ++k) o[k] += __uint_as_float(v[k]);
-                    }
+                    for (int k = 0; k < LD; ++k) o[k] += __uint_as_float(v[k]);
+                }
                 if (S > 1) {
 #pragma unroll
                     for (int k = 0; k < LD; ++k)
@@ -346,7 +348,7 @@ cudaError_t launch_bn(DirectParams& P, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int need = direct_stage<PL, BN>();
     P.stages = std::min(4, (SMEM_LIMIT - 1024 - BN * 512) / need);
-    P.split_log = split_log(p.tiles, p.nk, PL == 3 ? CHUNK * accumulators(BN) : 1 << 30, sms);
+    P.split_log = split_log(p.tiles, p.nk, chunk_blocks(PL) * accumulators(PL, BN), sms);
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(THREADS);
     cfg.gridDim = dim3((unsigned)(p.tiles << P.split_log));
@@ -390,7 +392,7 @@ bool aligned(const void* p, long long ld, int e) { return (reinterpret_cast<uint
 
 }  // namespace
 
-// Every tile has an SM to itself: fp32 with the reduction cut into as many parts as the accumulators ask for, up to eight.
+// Every tile has an SM to itself, with the reduction cut into as many parts as the accumulators ask for, up to eight.
 // Against a laid-out copy and k_linear_tc.cu (M x N x K, us, here and there): fp32 16x512x512 5.2 and 8.4, 1024x256x784
 // 10.3 and 13.2, 512x1024x1024 14.2 and 16.9; many waves of tiles, fp32 297x3712x1472 118 and 33.
 // Rows that are not 16-byte aligned are loaded element by element. In fp32 that costs more than the copy where several
@@ -401,7 +403,7 @@ bool aligned(const void* p, long long ld, int e) { return (reinterpret_cast<uint
 bool linear_direct_fits(int dtype, long long M, int N, int K, bool x_aligned, bool w_aligned) {
     int sms = 0, parts = 1;
     if (device_sms(&sms) != cudaSuccess) return false;
-    const int bn = columns(M), nk = blocks_of(K), most = dtype == VF_F32 ? CHUNK * accumulators(bn) : 1 << 30;
+    const int bn = columns(M), nk = blocks_of(K), pl = dtype == VF_F32 ? 3 : 1, most = chunk_blocks(pl) * accumulators(pl, bn);
     while (parts * most < nk && parts <= 8) parts *= 2;
     const long long tiles = ((long long)N + BM - 1) / BM * ((M + bn - 1) / bn);
     if (parts > 8 || tiles * parts > sms) return false;

@@ -13,7 +13,7 @@
 // bits and bf16's exponent range is fp32's. Six of the nine products are formed (h h, h m, m h, m m, h l, l h); the
 // three left out are below 2^-24 of the largest. An MMA adds its products to the accumulator with truncation (measured:
 // 2.2e-8 of the sum per MMA, low for sums of positive terms), so the five small products go to an accumulator of their own, and
-// both are added to registers, rounding to nearest: h h every CHUNK blocks, the small ones every COR_CHUNKS chunks. Error against
+// both are added to registers, rounding to nearest: h h every 256 steps, the small ones every COR_CHUNKS chunks. Error against
 // 64 bits at a reduction of 1024, signed normal values: 3.0e-7 (2-norm; a plain fp32 product 5.7e-7);
 // at 4096, positive values: 6.2e-7 (8.4e-7).
 //
@@ -58,8 +58,7 @@ constexpr int threads_of() {
 }
 constexpr int MAX_STAGES = 8;
 constexpr int SMEM_LIMIT = 232448;  // 227 KB, static shared memory included
-constexpr int CHUNK = 8;       // fp32: blocks of 32 between two additions of the h h accumulator
-constexpr int COR_CHUNKS = 8;  // and chunks between two of the small products'
+constexpr int COR_CHUNKS = 8;  // fp32: chunks between two additions of the small products' accumulator
 
 template <int PL>
 constexpr int block_k() {
@@ -217,6 +216,11 @@ template <int PL, int BN>
 constexpr int stage_bytes() {
     return stage_blocks<PL, BN>() * PL * (BM + BN / pair_of<BN>()) * block_k<PL>() * 2;
 }
+// Stages between two additions of an accumulator to registers: 256 steps of the reduction in fp32, CHUNK_16 in 16 bits.
+template <int PL, int BN>
+constexpr int chunk_stages() {
+    return (PL == 3 ? 256 : CHUNK_16) / (block_k<PL>() * stage_blocks<PL, BN>());
+}
 
 // N columns of this lane, 32 elements apart. The 16-bit conversions work on pairs.
 template <int N>
@@ -265,6 +269,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
     constexpr int STAGE = stage_bytes<PL, BN>();
     constexpr int KS = stage_blocks<PL, BN>(), BLOCK = STAGE / KS;  // blocks of a stage lie one after the other
     constexpr int NB = (PL == 1 || BN <= 128) ? 2 : 1;       // accumulator sets in TMEM
+    constexpr int CHUNK = chunk_stages<PL, BN>();
     constexpr int ACC_COLS = NB * BN;
     constexpr int USED_COLS = PL == 3 ? 2 * ACC_COLS : ACC_COLS;
     constexpr int TMEM_COLS = USED_COLS < 32 ? 32 : USED_COLS;
@@ -455,7 +460,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                     }
                     commit<CG>(&empty[g.slot]);
                     ++in_chunk;
-                    if (kb + 1 == kb1 || (PL == 3 && in_chunk == CHUNK)) {
+                    if (kb + 1 == kb1 || in_chunk == CHUNK) {
                         commit<CG>(&acc_full[chunk.slot]);
                         chunk.next(NB);
                         in_chunk = 0;
@@ -519,11 +524,11 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
             const int kb0 = at.kb0, kb1 = at.kb1;
             uint32_t acc_t = 0;  // TMEM columns that hold this warp's part of the finished tile
             bool alive = true;
-            if (PL == 3) {
+            const int nc = (kb1 - kb0 + CHUNK - 1) / CHUNK;
+            if (PL == 3 || nc > 1) {
                 float acc[PART];
 #pragma unroll
                 for (int c = 0; c < PART; ++c) acc[c] = 0.f;
-                const int nc = (kb1 - kb0 + CHUNK - 1) / CHUNK;
                 for (int ch = 0; ch < nc; ++ch) {
                     if (!__all_sync(0xffffffffu, wait_phase(&acc_full[chunk.slot], chunk.lap & 1, abort_flag))) {
                         alive = false;
@@ -544,7 +549,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                         __syncwarp();
                         if (lane == 0) arrive_leader<CG>(&acc_empty[chunk.slot]);
                         chunk.next(NB);
-                        if ((ch + 1) % COR_CHUNKS == 0) {
+                        if (PL == 3 && (ch + 1) % COR_CHUNKS == 0) {
                             const uint32_t cor_t = tmem + lane_base + ACC_COLS + cor.slot * BN;
 #pragma unroll
                             for (int c = 0; c < PART; c += LD) {
@@ -565,19 +570,23 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                 const uint32_t cor_t = tmem + lane_base + ACC_COLS + cor.slot * BN;
 #pragma unroll
                 for (int c = 0; c < PART; c += LD) {  // the finished sums go back to TMEM for the rolled loops below
-                    uint32_t v[LD];
-                    tmem_ld<LD>(cor_t + c, v);
-                    tmem_wait_ld();
+                    if (PL == 3) {
+                        uint32_t v[LD];
+                        tmem_ld<LD>(cor_t + c, v);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < LD; ++k) acc[c + k] += __uint_as_float(v[k]);
+                        for (int k = 0; k < LD; ++k) acc[c + k] += __uint_as_float(v[k]);
+                    }
 #pragma unroll
                     for (int k = 0; k < LD; k += 8) tmem_st8(acc_t + c + k, acc + c + k);
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_leader<CG>(&cor_empty[cor.slot]);
-                cor.next(NB);
+                if (PL == 3) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_leader<CG>(&cor_empty[cor.slot]);
+                    cor.next(NB);
+                }
             } else {
                 if (!__all_sync(0xffffffffu, wait_phase(&acc_full[chunk.slot], chunk.lap & 1, abort_flag))) break;
                 tc_fence_after();
