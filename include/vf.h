@@ -358,11 +358,11 @@ int vf_concretize_dense_noalloc(const float* lambda, long long lambda_bstride, i
  * ([device], 256-byte aligned, used only by work enqueued by the call, so calls that may overlap on the GPU need a
  * workspace each). Nothing is kept from one call for the next and nothing synchronises, so a call can be captured in a
  * CUDA graph. All matrices of a call have one element type; sums are held in fp32 or more and every output is
- * rounded to the element type once. The tensor cores cut what they add instead of rounding it; their accumulators are added
- * to rounded fp32 sums every 2048 steps of a reduction (16 bits) or 256 (fp32), so that terms of one sign come out low by about 1.2e-5
- * of the sum in float16, 7e-6 in bf16 and 7e-7 in fp32, however long the reduction is. Row strides (ld*) are in elements, at least the row's length; any alignment of
- * the element type is served. Results do not change from run to run. Outputs must not overlap inputs, save where
- * an entry point says so. */
+ * rounded to the element type once. The tensor cores cut what they add instead of rounding it; their accumulators are
+ * added to rounded fp32 sums every 2048 steps of a reduction (16 bits) or 256 (fp32), so that terms of one sign come out
+ * low by about 1.2e-5 of the sum in float16, 7e-6 in bf16 and 7e-7 in fp32, however long the reduction is. Row strides
+ * (ld*) are in elements, at least the row's length; any alignment of the element type is served. Results do not change
+ * from run to run. Outputs must not overlap inputs, save where an entry point says so. */
 typedef enum { VF_F32 = 0, VF_BF16 = 1, VF_F16 = 2 } vf_dtype;
 typedef enum {
     VF_ACT_NONE = 0,
@@ -391,8 +391,10 @@ int vf_linear(int dtype, int act, const void* x, long long ldx, const void* W, l
 /* Backward pass of vf_linear for dy [M, N], the gradient of y:  g = dy act'(z),
  *   dx [M, K] = g W,  dW [N, K] = g^T x,  db [N] = sum over rows of g,  dr [M, N] = g.
  * Every output may be NULL (not computed); z may be NULL for VF_ACT_NONE, W without dx, x without dW. Outputs are
- * written, not accumulated; M = 0 writes zeros to dW and db, N = 0 zeros to dx. For 16-bit types g may be rounded to the
- * element type where it enters the products (relu's and none's g is exact); db adds the unrounded g. */
+ * written, not accumulated; M = 0 writes zeros to dW and db, N = 0 zeros to dx. For 16-bit types g may be rounded to
+ * 16 bits where it enters the products (relu's and none's g is exact): the error of dx and dW is then about 1.4 times that
+ * of their own rounding. float16's g is rounded with a power of two taken out, so that its range does not bound g: what is
+ * lost lies below 2^-38 of the largest |dy|. db adds the unrounded g. */
 int vf_linear_grad(int dtype, int act, const void* dy, long long lddy, const void* z, long long ldz, const void* x,
                    long long ldx, const void* W, long long ldw, long long M, int N, int K, void* dx, long long lddx,
                    void* dW, long long lddw, void* db, void* dr, long long lddr, void* work, size_t work_bytes,

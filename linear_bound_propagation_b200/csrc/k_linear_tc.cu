@@ -71,6 +71,7 @@ struct TcParams {
     int workers;         // CTAs, pairs or clusters that walk the tiles
     int split, split_log;  // CTAs per tile (cluster size), a power of two
     int stages;
+    const float* unscale;  // float16: what the sums are multiplied by, a power of two; or nullptr
     int test_stall;        // tests only: the first CTA never makes its first copies, so that a bounded wait expires
     // column sums of g, joined here: db[n] = sum_q part[q * N + n]
     const float* part;
@@ -495,6 +496,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                 ((T*)P.db)[n] = from_f32<T>(s);
             }
         constexpr int ROUND = epi_round<T, BN>(), RL = ROUND < 16 ? 8 : 16;
+        const float unscale = std::is_same<T, __half>::value && P.unscale != nullptr ? *P.unscale : 1.f;
         T* buf = reinterpret_cast<T*>(base + (size_t)NS * STAGE + (EPI_TMA ? e * (65536 / EW) : 0));  // 4 x 32 x ROUND
         Ring chunk, cor;      // as the MMA issuer counts them
         Ring rin;             // residual rounds consumed
@@ -602,7 +604,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         push_column<BN>(smem_u32(base + (size_t)NS * STAGE), part_no * PART + c + k, q * 32 + lane, rank,
-                                        P.split_log, __uint_as_float(v[k]));
+                                        P.split_log, __uint_as_float(v[k]) * unscale);
                 }
                 pushed = true;
             } else if (by_tma) {
@@ -615,7 +617,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                     tmem_wait_ld();
                     float o[ROUND];
 #pragma unroll
-                    for (int c = 0; c < ROUND; ++c) o[c] = __uint_as_float(v[c]) + bias;
+                    for (int c = 0; c < ROUND; ++c) o[c] = fmaf(__uint_as_float(v[c]), unscale, bias);
                     if (p.res != nullptr) {
                         alive = __all_sync(0xffffffffu, wait_phase(&res_full[e][rin.slot], rin.lap & 1, abort_flag));
                         if (!alive) break;
@@ -654,7 +656,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                     tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < LD; ++k)
-                        if (i < p.I && c + k < n) o[k * p.I] = __uint_as_float(v[k]);
+                        if (i < p.I && c + k < n) o[k * p.I] = __uint_as_float(v[k]) * unscale;
                 }
             } else {
                 float rn[LD];
@@ -666,7 +668,7 @@ linear_tc_k(const __grid_constant__ Maps maps, const __grid_constant__ TcParams 
                     tmem_wait_ld();
                     float o[LD];
 #pragma unroll
-                    for (int k = 0; k < LD; ++k) o[k] = __uint_as_float(v[k]);
+                    for (int k = 0; k < LD; ++k) o[k] = __uint_as_float(v[k]) * unscale;
                     if ((long long)j0 + c < p.J) finish_lane<T>(p, i, (long long)j0 + c, o, bias, r);
 #pragma unroll
                     for (int k = 0; k < LD; ++k) r[k] = rn[k];
@@ -780,7 +782,12 @@ struct GradJob {
     float* part;  // or nullptr
     long long blocks;
     int blocks_c, steps;
+    // float16: the largest finite |dy| of each block of linear_peak_k, and where the inverse of the operand's scale goes; or nullptr
+    const unsigned* peaks;
+    int npeaks;
+    float* unscale;
 };
+constexpr int MAX_PEAKS = 592;  // blocks of that pass at most: four per SM
 
 // U rows of dy and z on their way into registers while the U before are worked on.
 template <typename T, int ACT, int U>
@@ -795,7 +802,7 @@ struct GradRows {
             if (ACT != VF_ACT_NONE) load_raw8((const T*)j.z + r * j.ldz + c, n, j.vec, z[k]);
         }
     }
-    __device__ __forceinline__ void work(const GradJob& j, long long r0, int k0, int c, float (&s)[8]) {
+    __device__ __forceinline__ void work(const GradJob& j, long long r0, int k0, int c, float scale, float (&s)[8]) {
         const int n = j.N - c;
 #pragma unroll
         for (int k = 0; k < U; ++k) {
@@ -809,32 +816,91 @@ struct GradRows {
                 if (ACT != VF_ACT_NONE) v[u] = act_grad<sizeof(T) == 2>(v[u], x[u], ACT);
                 s[u] += v[u];
             }
-            if (j.dst != nullptr) store_operand<T>(j.dst + r * j.ldp + c, j.M * j.ldp, v);
+            constexpr bool SCALED = std::is_same<T, __half>::value;
+            if (!SCALED && j.dst != nullptr) store_operand<T>(j.dst + r * j.ldp + c, j.M * j.ldp, v);
             if (j.dr != nullptr) {
                 Pack8<T> p;
                 pack8(p, v);
                 store_raw8((T*)j.dr + r * j.lddr + c, n, j.vec_r, p);
             }
+            if (SCALED && j.dst != nullptr) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[u] *= scale;
+                store_operand<T>(j.dst + r * j.ldp + c, j.M * j.ldp, v);
+            }
         }
     }
 };
 template <typename T, int ACT>
-__device__ __forceinline__ void grad_rows(const GradJob& j, long long r0, int c, float (&s)[8]) {
+__device__ __forceinline__ void grad_rows(const GradJob& j, long long r0, int c, float scale, float (&s)[8]) {
     constexpr int U = sizeof(T) == 2 ? 2 : 1;
     GradRows<T, ACT, U> a, b;
     a.load(j, r0, 0, c);
 #pragma unroll 1
     for (int k = 0; k < j.steps; k += 2 * U) {
         b.load(j, r0, k + U, c);
-        a.work(j, r0, k, c, s);
+        a.work(j, r0, k, c, scale, s);
         a.load(j, r0, k + 2 * U, c);
-        b.work(j, r0, k + U, c, s);
+        b.work(j, r0, k + U, c, scale, s);
     }
+}
+
+// Largest of a block's values, in every thread.
+__device__ __forceinline__ unsigned block_peak(unsigned m) {
+    __shared__ unsigned w[PACK_THREADS / 32];
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < PACK_THREADS / 32; ++k) m = max(m, w[k]);
+    return m;
+}
+
+// float16 has 11 bits from 2^-14 to 2^16 only: gradients of 1e-6 would keep four of them, and 65504 times a slope above one
+// would be infinite. So where g has to be rounded (gelu, silu: slopes up to 1.13) it is first multiplied by the power of two that
+// brings dy's largest magnitude to 2^13 .. 2^14, which needs a pass over dy before, and the products' sums by its inverse. What
+// is lost then lies below 2^-38 of the largest. bf16 has fp32's range and needs none.
+// This pass: the largest finite |dy| of each block's rows, as the bits of a float16.
+__global__ void __launch_bounds__(PACK_THREADS) linear_peak_k(const __grid_constant__ GradJob j, unsigned* peaks) {
+    constexpr int U = 4;
+    grid_trigger();
+    grid_wait();
+    unsigned m = 0;
+    for (long long blk = blockIdx.x; blk < j.blocks; blk += gridDim.x) {
+        const int c = (int)(blk % j.blocks_c) * PACK_COLS + (threadIdx.x & 31) * 8;
+        if (c >= j.N) continue;
+        const long long r0 = blk / j.blocks_c * (8 * j.steps) + (threadIdx.x >> 5);
+#pragma unroll 1
+        for (int k = 0; k < j.steps; k += U) {
+            GradRows<__half, VF_ACT_NONE, U> rows;
+            rows.load(j, r0, k, c);
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const unsigned lo = rows.d[q].w[u] & 0x7fff, hi = rows.d[q].w[u] >> 16 & 0x7fff;
+                    m = max(m, max(lo < 0x7c00 ? lo : 0, hi < 0x7c00 ? hi : 0));
+                }
+        }
+    }
+    m = block_peak(m);
+    if (threadIdx.x == 0) peaks[blockIdx.x] = m;
+}
+// The scale, from the blocks' largest; the first block hands its inverse on.
+__device__ __forceinline__ float grad_scale(const GradJob& j, long long blk) {
+    unsigned m = 0;
+    for (int k = threadIdx.x; k < j.npeaks; k += PACK_THREADS) m = max(m, j.peaks[k]);
+    m = block_peak(m);
+    const float peak = __half2float(__ushort_as_half((unsigned short)m));  // 0, or 2^-24 to 65504: a normal number
+    const int e = m == 0 ? 0 : 13 + 127 - (int)(__float_as_uint(peak) >> 23);
+    if (blk == 0 && threadIdx.x == 0) *j.unscale = __uint_as_float((unsigned)(127 - e) << 23);
+    return __uint_as_float((unsigned)(127 + e) << 23);
 }
 
 template <typename T>
 __device__ void grad_block(const GradJob& j, long long blk) {
     __shared__ float sums[8][PACK_COLS];
+    const float scale = std::is_same<T, __half>::value && j.peaks != nullptr ? grad_scale(j, blk) : 1.f;
     const int w = threadIdx.x >> 5;
     const long long rb = blk / j.blocks_c;
     const int c0 = (int)(blk % j.blocks_c) * PACK_COLS, cl = (threadIdx.x & 31) * 8, c = c0 + cl;
@@ -842,10 +908,10 @@ __device__ void grad_block(const GradJob& j, long long blk) {
     if (c < j.N) {
         const long long r0 = rb * (8 * j.steps) + w;
         switch (j.act) {
-            case VF_ACT_RELU: grad_rows<T, VF_ACT_RELU>(j, r0, c, s); break;
-            case VF_ACT_GELU: grad_rows<T, VF_ACT_GELU>(j, r0, c, s); break;
-            case VF_ACT_SILU: grad_rows<T, VF_ACT_SILU>(j, r0, c, s); break;
-            default: grad_rows<T, VF_ACT_NONE>(j, r0, c, s);
+            case VF_ACT_RELU: grad_rows<T, VF_ACT_RELU>(j, r0, c, scale, s); break;
+            case VF_ACT_GELU: grad_rows<T, VF_ACT_GELU>(j, r0, c, scale, s); break;
+            case VF_ACT_SILU: grad_rows<T, VF_ACT_SILU>(j, r0, c, scale, s); break;
+            default: grad_rows<T, VF_ACT_NONE>(j, r0, c, scale, s);
         }
     }
     if (j.part == nullptr) return;
@@ -1026,6 +1092,19 @@ cudaError_t launch_operands(int dtype, const GradJob& g, const PackJob& a, const
         case VF_BF16: return cudaLaunchKernelEx(&cfg, linear_operands_k<__nv_bfloat16>, g, a, b);
         default: return cudaLaunchKernelEx(&cfg, linear_operands_k<__half>, g, a, b);
     }
+}
+
+cudaError_t launch_peaks(const GradJob& g, unsigned* peaks, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    cfg.gridDim = dim3((unsigned)g.npeaks);
+    cfg.blockDim = dim3(PACK_THREADS);
+    cfg.stream = s;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, linear_peak_k, g, peaks);
 }
 
 struct Side {
@@ -1283,6 +1362,7 @@ cudaError_t launch_pl(TcParams& P, const Side (&A)[2], const Side (&B)[2], int c
     } else {
         TcParams Q{};
         Q.p[0] = P.p[1];
+        Q.unscale = P.unscale;
         const Side A1[2] = {A[1], {}}, B1[2] = {B[1], {}};
         P.p[1] = TcProduct{};
         e = launch_as<T, PL>(P, A, B, 1, plans.a, sms, s);
@@ -1329,6 +1409,7 @@ size_t linear_tc_workspace(int dtype, long long M, int N, int K, bool grad) {
     size_t n = operand_bytes(dtype, M, K) + operand_bytes(dtype, N, K);
     if (!grad) return n;
     n += operand_bytes(dtype, M, N) + (size_t)round_up(row_blocks(M, N) * N * 4, 256);
+    if (dtype == VF_F16) n += (size_t)round_up((MAX_PEAKS + 1) * 4, 256);
     int sms = 0;
     if (device_sms(&sms) != cudaSuccess) return n;
     size_t sums = 0;
@@ -1392,10 +1473,11 @@ cudaError_t launch_linear_grad_tc(const LinearGrad& f, void* work, size_t have, 
     gj.lddr = f.lddr;
     gj.vec_r = f.dr != nullptr && aligned16(f.dr, f.lddr, e);
     Operand16 g{};
+    const bool scaled = products && f.dtype == VF_F16 && (f.act == VF_ACT_GELU || f.act == VF_ACT_SILU);
     if (products) {
         if (e == 2 && f.act == VF_ACT_NONE && aligned16(f.dy, f.lddy, e)) {
             g = Operand16{f.dy, f.M, f.lddy, f.N};  // dy is g, and TMA can read it
-        } else if (e == 2 && gj.vec_r) {
+        } else if (e == 2 && gj.vec_r && !scaled) {
             g = Operand16{f.dr, f.M, f.lddr, f.N};  // dr is g
         } else {
             gj.ldp = round_up(f.N, 64);
@@ -1408,6 +1490,11 @@ cudaError_t launch_linear_grad_tc(const LinearGrad& f, void* work, size_t have, 
         gj.blocks_c = col_blocks(f.N);
         gj.steps = pack_steps(f.M, gj.blocks_c);
         gj.blocks = row_blocks(f.M, f.N) * gj.blocks_c;
+    }
+    unsigned* peaks = nullptr;
+    if (scaled) {
+        peaks = (unsigned*)w.take((MAX_PEAKS + 1) * 4);
+        gj.npeaks = (int)std::min<long long>(gj.blocks, MAX_PEAKS);
     }
     PackJob jw{}, jx{};
     Side A[2] = {}, B[2] = {};
@@ -1448,6 +1535,11 @@ cudaError_t launch_linear_grad_tc(const LinearGrad& f, void* work, size_t have, 
         if (plog_of(how, k) > 0) P.p[k].sums = (float*)w.take((size_t)((P.p[k].I * P.p[k].J) << plog_of(how, k)) * 4);
     *need = w.used;
     if (w.used > have) return cudaSuccess;  // the caller reports it
+    if (scaled) {
+        if ((err = launch_peaks(gj, peaks, s)) != cudaSuccess) return err;
+        gj.peaks = peaks;
+        P.unscale = gj.unscale = (float*)(peaks + MAX_PEAKS);
+    }
     err = launch_operands(f.dtype, gj, jw, jx, s);
     if (err != cudaSuccess) return err;
     if (count == 0 && f.db == nullptr) return cudaSuccess;
