@@ -360,7 +360,7 @@ int vf_concretize_dense_noalloc(const float* lambda, long long lambda_bstride, i
  * CUDA graph. All matrices of a call have one element type; sums are held in fp32 or more and every output is
  * rounded to the element type once. The tensor cores cut what they add instead of rounding it; their accumulators are
  * added to rounded fp32 sums every 2048 steps of a reduction (16 bits) or 256 (fp32), so that terms of one sign come out
- * low by about 1.2e-5 of the sum in float16, 7e-6 in bf16 and 7e-7 in fp32, however long the reduction is. Row strides
+ * low by about 1.2e-5 of the sum in float16, 7e-6 in bf16 and 4e-7 in fp32, however long the reduction is. Row strides
  * (ld*) are in elements, at least the row's length; any alignment of the element type is served. Results do not change
  * from run to run. Outputs must not overlap inputs, save where an entry point says so. */
 typedef enum { VF_F32 = 0, VF_BF16 = 1, VF_F16 = 2 } vf_dtype;
@@ -382,8 +382,8 @@ int vf_linear_workspace(int dtype, long long M, int N, int K, int grad, size_t* 
  * x [M, K], W [N, K], b [N] or NULL, r [M, N] or NULL, y [M, N]; z [M, N] or NULL receives the pre-activation that
  * vf_linear_grad reads (y itself is formed from the unrounded z). With r the output of an earlier layer this is the
  * closing layer of a residual block, as VF_ADD followed by VF_RELU. y may be r (same pointer and stride).
- * K = 0 gives act(b + r); M = 0 or N = 0 is a no-op. A non-finite input makes the outputs that depend on it
- * non-finite, not necessarily the value IEEE arithmetic would give. */
+ * K = 0 gives act(b + r); M = 0 or N = 0 is a no-op. Infinities and NaN pass through z as in fp32 arithmetic, save that
+ * the product of two infinities may be NaN in fp32 layers; act takes its limits (of minus infinity: 0 for all but none). */
 int vf_linear(int dtype, int act, const void* x, long long ldx, const void* W, long long ldw, const void* b,
               const void* r, long long ldr, long long M, int N, int K, void* y, long long ldy, void* z, long long ldz,
               void* work, size_t work_bytes, void* stream);

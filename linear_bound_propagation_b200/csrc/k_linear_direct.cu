@@ -122,11 +122,11 @@ __device__ __forceinline__ void store_block(uint8_t* dst, int plane, const Held<
             uint8_t* o = dst + swizzled(line, e >> 3) + (e & 7) * 2;
             if (PL == 3) {
                 const float v = to_f32(h.e[x]);
-                float r, l;
-                split3(v, r, l);
-                *reinterpret_cast<uint16_t*>(o) = (uint16_t)(__float_as_uint(v) >> 16);
-                *reinterpret_cast<uint16_t*>(o + plane) = (uint16_t)(__float_as_uint(r) >> 16);
-                *reinterpret_cast<uint16_t*>(o + 2 * plane) = (uint16_t)(__float_as_uint(l) >> 16);
+                float hi, mid, lo;
+                split3(v, hi, mid, lo);
+                *reinterpret_cast<uint16_t*>(o) = (uint16_t)(__float_as_uint(hi) >> 16);
+                *reinterpret_cast<uint16_t*>(o + plane) = (uint16_t)(__float_as_uint(mid) >> 16);
+                *reinterpret_cast<uint16_t*>(o + 2 * plane) = (uint16_t)(__float_as_uint(lo) >> 16);
             } else {
                 *reinterpret_cast<T*>(o) = h.e[x];
             }

@@ -9,13 +9,13 @@
 // along the MMA's M (128 TMEM lanes), j along its N: the small dimension of a call of few rows is the one that can be
 // as narrow as 16 columns, and a warp's 32 lanes hold consecutive elements of an output row.
 //
-// fp32 (PL = 3): x = h + m + l, three bf16 pieces of 8 significand bits each, by truncation, so the pieces hold all 24
+// fp32 (PL = 3): x = h + m + l, three bf16 pieces of 8 significand bits each, rounded to nearest, so the pieces hold all 24
 // bits and bf16's exponent range is fp32's. Six of the nine products are formed (h h, h m, m h, m m, h l, l h); the
-// three left out are below 2^-24 of the largest. An MMA adds its products to the accumulator with truncation (measured:
-// 2.2e-8 of the sum per MMA, low for sums of positive terms), so the five small products go to an accumulator of their own, and
-// both are added to registers, rounding to nearest: h h every 256 steps, the small ones every COR_CHUNKS chunks. Error against
-// 64 bits at a reduction of 1024, signed normal values: 3.0e-7 (2-norm; a plain fp32 product 5.7e-7);
-// at 4096, positive values: 6.2e-7 (8.4e-7).
+// three left out are at most 2^-24 of the product together, of either sign. An MMA cuts what it adds to its accumulator
+// (linear_tc.cuh), so the five small products go to an accumulator of their own, and both are added to registers, rounding to
+// nearest: h h every 256 steps, the small ones every COR_CHUNKS chunks. Error against 64 bits (2-norm, in parentheses a plain
+// fp32 product): signed normal values 2.3e-7 (5.7e-7) at a reduction of 1024 and 2.4e-7 (1.1e-6) at 4096; positive ones 3.8e-7
+// (4.9e-7 and 9.9e-7) at either, nearly all of it low by 3.8e-7.
 //
 // Roles (one CTA per SM, or a pair of CTAs on two SMs for 256 x 256 tiles; persistent over the tiles): warp 0 TMA
 // producer, warp 1 MMA issuer, warps 2 and up epilogue (lane quarter warp % 4 of TMEM, four warps to a share of the

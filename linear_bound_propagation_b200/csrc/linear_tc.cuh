@@ -240,23 +240,57 @@ __device__ __forceinline__ void finish_lane(const TcProduct& p, long long i, lon
         if (u < n) o[u * p.ldo] = from_f32<T>(v[u]);
 }
 
-// x = h + m + l: three bf16 by truncation, 8 significand bits each (the subtractions are exact). What is not finite gives
-// a piece that is not finite, and so products that are not.
-__device__ __forceinline__ void split3(float x, float& r, float& l) {
-    r = x - __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-    l = r - __uint_as_float(__float_as_uint(r) & 0xffff0000u);
+// x = h + m + l: three bf16, each what is left rounded to nearest, of 8 significand bits. The subtractions are exact, |m| is at most
+// 2^-8 and |l| at most 2^-17 of x's leading power of two, so l holds the rest. (Pieces cut instead of rounded leave twice as
+// much in m and l, all of x's sign: products without m l and l m then came out low by up to 4.7e-7.) What bf16 would round to
+// infinity is cut. An infinity or NaN goes to l alone: a piece that is not finite meets h of the other operand, which is zero
+// only where that is zero, so the product is the one of fp32 (infinity times infinity excepted: NaN), and none of another sign.
+constexpr float LARGEST_ROUNDED = 0x1.fefffep127f;  // the largest fp32 value that bf16 rounds to a finite one
+__device__ __forceinline__ uint32_t round2(float a, float b) {
+    const __nv_bfloat162 w = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&w);
 }
-// The upper halves of two floats: their leading bf16 pieces.
+// The pieces as floats.
+__device__ __forceinline__ void split3(float x, float& h, float& m, float& l) {
+    h = __uint_as_float(round2(x, 0.f) << 16);
+    const bool finite = fabsf(x) < __uint_as_float(0x7f800000u);
+    if (!(fabsf(x) <= LARGEST_ROUNDED)) h = finite ? __uint_as_float(__float_as_uint(x) & 0xffff0000u) : 0.f;
+    const float r = x - h;
+    m = finite ? __uint_as_float(round2(r, 0.f) << 16) : 0.f;
+    l = __uint_as_float(round2(r - m, 0.f) << 16);
+}
+// The upper halves of two floats.
 __device__ __forceinline__ uint32_t upper2(float a, float b) {
     return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
 __device__ __forceinline__ void split3x8(const float (&v)[8], uint4& h, uint4& m, uint4& l) {
-    float r[8], t[8];
+    uint32_t hw[4], mw[4], lw[4];
+    float big = 0.f;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) split3(v[u], r[u], t[u]);
-    h = make_uint4(upper2(v[0], v[1]), upper2(v[2], v[3]), upper2(v[4], v[5]), upper2(v[6], v[7]));
-    m = make_uint4(upper2(r[0], r[1]), upper2(r[2], r[3]), upper2(r[4], r[5]), upper2(r[6], r[7]));
-    l = make_uint4(upper2(t[0], t[1]), upper2(t[2], t[3]), upper2(t[4], t[5]), upper2(t[6], t[7]));
+    for (int u = 0; u < 8; ++u) big = max_nan(big, fabsf(v[u]));
+    if (big <= LARGEST_ROUNDED) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float a = v[2 * u], b = v[2 * u + 1];
+            hw[u] = round2(a, b);
+            const float ra = a - __uint_as_float(hw[u] << 16), rb = b - __uint_as_float(hw[u] & 0xffff0000u);
+            mw[u] = round2(ra, rb);
+            lw[u] = round2(ra - __uint_as_float(mw[u] << 16), rb - __uint_as_float(mw[u] & 0xffff0000u));
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            float ha, ma, la, hb, mb, lb;
+            split3(v[2 * u], ha, ma, la);
+            split3(v[2 * u + 1], hb, mb, lb);
+            hw[u] = upper2(ha, hb);
+            mw[u] = upper2(ma, mb);
+            lw[u] = upper2(la, lb);
+        }
+    }
+    h = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+    m = make_uint4(mw[0], mw[1], mw[2], mw[3]);
+    l = make_uint4(lw[0], lw[1], lw[2], lw[3]);
 }
 
 // Split reductions. Each of the 2^log CTAs of a cluster finishes its share of the tile's BN columns; its shared memory at
