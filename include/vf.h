@@ -410,8 +410,8 @@ int vf_ops_check(void);
  * grads, outs [host] n device pointers; sizes [host] elements of each (contiguous; 0 allowed); dtypes [host] vf_dtype of
  * each (input and output alike; they may differ between gradients); norm [device] one float. scale >= 0 undoes a loss
  * scale (1 for none); max_norm >= 0, INFINITY to measure and scale only. outs[t] is grads[t] itself (in place) or
- * overlaps no gradient and no other output; overlaps are refused. A norm that is not finite clips nothing: the gradients
- * are scaled by `scale` alone and *norm reports it. Squares are summed in fp64 beyond 16 terms, with
+ * overlaps no gradient and no other output; overlaps are refused. A *norm that is not finite (beyond fp32's range among
+ * them) clips nothing: the gradients are scaled by `scale` alone. Squares are summed in fp64 beyond 16 terms, with
  * no overflow or underflow for finite elements. The slope gradients of vf_alpha_grad and vf_alpha_beta_grad and the
  * weight gradients of vf_linear_grad are the intended input. The workspace is vf_clip_workspace(n) bytes (of
  * the current device). */

@@ -9,7 +9,8 @@
 //
 // Squares are added in fp32 over one thread's 32 bytes (at most 16 terms) and in fp64 beyond that. Where such a
 // partial sum leaves the range in which fp32 squares are exact enough (overflow above 1e19, underflow below 1e-15 per
-// element), that thread's elements are squared again in fp64, so norms of any finite fp32 or bf16 values come out.
+// element), that thread's elements are squared again in fp64, so norms of any finite fp32 or bf16 values come out. Whether a norm
+// is finite is decided on the float that the caller sees.
 #include <algorithm>
 
 #include "vf_internal.cuh"
@@ -136,15 +137,29 @@ __global__ void __launch_bounds__(THREADS) clip_norm_k(const __grid_constant__ T
     if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
+// f as two factors: fp32 holds fewer than 24 bits of an f below 2^-126 (a norm of 1e38 clipped to 1), so 2^-126 is taken out of it
+// there, and a product that is not subnormal keeps its bits. `low` is 1 elsewhere.
+struct Factor {
+    float high, low;
+    __device__ __forceinline__ explicit Factor(double f) {
+        low = f < 1.1754943508222875e-38 ? 1.17549435e-38f : 1.f;
+        high = (float)(f / (double)low);
+    }
+    template <typename T>
+    __device__ __forceinline__ T operator()(T x) const {
+        return from_f32<T>(to_f32(x) * high * low);
+    }
+};
+
 template <typename T, int V>
-__device__ __forceinline__ void chunk_scale(const T* p, T* out, long long e0, long long e1, float f) {
+__device__ __forceinline__ void chunk_scale(const T* p, T* out, long long e0, long long e1, const Factor& f) {
     constexpr int N = 16 / sizeof(T);
     const T* q = p + e0;
     T* o = out + e0;
     const int len = (int)(e1 - e0);
     const int head = min(len, (int)(((16 - (reinterpret_cast<uintptr_t>(q) & 15)) & 15) / sizeof(T)));
     if (((reinterpret_cast<uintptr_t>(q) ^ reinterpret_cast<uintptr_t>(o)) & 15) != 0) {
-        for (int i = threadIdx.x; i < len; i += THREADS) o[i] = from_f32<T>(to_f32(q[i]) * f);
+        for (int i = threadIdx.x; i < len; i += THREADS) o[i] = f(q[i]);
         return;
     }
     const int nv = (len - head) / N;
@@ -157,20 +172,20 @@ __device__ __forceinline__ void chunk_scale(const T* p, T* out, long long e0, lo
 #pragma unroll
         for (int u = 0; u < V; ++u) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[u].v[i] = from_f32<T>(to_f32(v[u].v[i]) * f);
+            for (int i = 0; i < N; ++i) v[u].v[i] = f(v[u].v[i]);
             ob[threadIdx.x + u * THREADS] = v[u];
         }
     } else {
         for (int i = threadIdx.x; i < nv; i += THREADS) {
             Vec<T, N> w = b[i];
 #pragma unroll
-            for (int k = 0; k < N; ++k) w.v[k] = from_f32<T>(to_f32(w.v[k]) * f);
+            for (int k = 0; k < N; ++k) w.v[k] = f(w.v[k]);
             ob[i] = w;
         }
     }
-    if (threadIdx.x < head) o[threadIdx.x] = from_f32<T>(to_f32(q[threadIdx.x]) * f);
+    if (threadIdx.x < head) o[threadIdx.x] = f(q[threadIdx.x]);
     const int tail = head + nv * N + threadIdx.x;
-    if (tail < len) o[tail] = from_f32<T>(to_f32(q[tail]) * f);
+    if (tail < len) o[tail] = f(q[tail]);
 }
 
 template <int V>
@@ -181,14 +196,14 @@ clip_scale_k(const __grid_constant__ Table tab, const double* part, int nparts, 
     for (int i = threadIdx.x; i < nparts; i += THREADS) d += part[i];
     const double n = (double)scale * sqrt(block_sum(d));
     if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
-    const bool clip = n > (double)max_norm && !isinf(n);  // NaN compares false
-    const float f = (float)(clip ? (double)scale * ((double)max_norm / n) : (double)scale);
+    const bool clip = n > (double)max_norm && !isinf((float)n);  // NaN compares false
+    const Factor f(clip ? (double)scale * ((double)max_norm / n) : (double)scale);
     if (tab.n == 0) return;
     // backwards: what the norm's pass read last is still in L2
     int c = tab.first[tab.n] - 1 - (int)blockIdx.x;
     for (int t = c < 0 ? 0 : tensor_of(tab, c); c >= 0; c -= gridDim.x) {
         while (c < tab.first[t]) --t;
-        if (tab.in[t] == tab.out[t] && f == 1.f) continue;
+        if (tab.in[t] == tab.out[t] && f.high == 1.f && f.low == 1.f) continue;
         const long long e = chunk_elems(tab.dtype[t], V);
         const long long e0 = (c - tab.first[t]) * e, e1 = min(tab.size[t], e0 + e);
         switch (tab.dtype[t]) {
