@@ -495,6 +495,14 @@ class _On:
             g.__exit__(*exc)
 
 
+def _used_on(stream, *tensors):
+    """Memory of `tensors` that is freed on their own stream is not handed out again before `stream` has done what it holds now."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _matrix(name, t, shape, dtype, dev):
     """(pointer, row stride) of a matrix argument with unit column stride."""
     if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
@@ -549,11 +557,15 @@ def linear(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tensor] = None,
     """vf_linear: act(x W^T + b + residual) for x [M, K], W [N, K], b [N], residual [M, N], all of one type (float32,
     bfloat16 or float16); rows may be any distance apart. act: "none", "relu", "gelu" (normal distribution) or
     "silu". Returns dict(y=[M, N], z=the pre-activation for linear_grad or None). out: y's buffer; it may be
-    `residual` itself. Runs on the current stream of x's device unless `stream` is given."""
+    `residual` itself. Runs on the current stream of x's device unless `stream` is given. `stream`
+    has to wait for its inputs' makers and their users for `stream`, as with any work on several streams; the inputs may be
+    dropped right after the call, and what it returns belongs to `stream`."""
     tt, dtype, a, dev, M, N, K = _layer(x, W, act)
     if stream is not None or dev != torch._C._cuda_getDevice():
         with _On(dev, stream):
-            return linear(x, W, b, residual, act, want_z, out)
+            result = linear(x, W, b, residual, act, want_z, out)
+        _used_on(stream, x, W, b, residual, out)
+        return result
     xp, ldx = _matrix("x", x, (M, K), tt, dev)
     wp, ldw = _matrix("W", W, (N, K), tt, dev)
     shape = (M, N)
@@ -586,7 +598,9 @@ def linear_grad(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, act: str = "
         raise ValueError(f"act={act!r} needs the pre-activation z")
     if stream is not None or dev != torch._C._cuda_getDevice():
         with _On(dev, stream):
-            return linear_grad(dy, x, W, act, z, need)
+            result = linear_grad(dy, x, W, act, z, need)
+        _used_on(stream, dy, x, W, z)
+        return result
     shape = (M, N)
     dyp, lddy = _matrix("dy", dy, shape, tt, dev)
     zp, ldz = (None, 0) if z is None else _matrix("z", z, shape, tt, dev)
@@ -627,7 +641,9 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, scale: float 
     dev = grads[0].get_device() if n else torch.cuda.current_device()
     if stream is not None or (dev >= 0 and dev != torch._C._cuda_getDevice()):
         with _On(dev, stream):
-            return clip_grad_norm(grads, max_norm, scale, out)
+            result = clip_grad_norm(grads, max_norm, scale, None if out is None else outs)
+        _used_on(stream, *grads, *outs)
+        return result
     dtypes = [VF_DTYPES.get(g.dtype) for g in grads]
     for i, g in enumerate(grads):
         if dtypes[i] is None or dev < 0 or g.get_device() != dev or not g.is_contiguous():

@@ -1,0 +1,52 @@
+"""The dense-layer and gradient operators on a stream of their own: memory of temporaries, on a B200."""
+import pytest
+import torch
+
+vf = pytest.importorskip("linear_bound_propagation_b200.vf")
+pytestmark = pytest.mark.gpu
+
+
+def busy_stream():
+    """A stream that has waited for the current one and is held up for a while."""
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    return s
+
+
+def overwrite(like, count=4):
+    """What the allocator hands out next for this size, overwritten."""
+    return [torch.full_like(t, float("nan")) for t in like for _ in range(count)]
+
+
+@pytest.mark.parametrize("M", [4, 900])
+def test_temporaries_outlive_the_call_on_another_stream(M):
+    """Arguments dropped right after a call on a stream that has not begun: their memory is not handed out before it has."""
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    N, K = 520, 264
+    x, W, b, r, dy, z = (torch.randn(s, generator=gen, device="cuda") for s in ((M, K), (N, K), (N,), (M, N), (M, N), (M, N)))
+    want = vf.linear(x * 2, W * 2, b * 2, residual=r * 2, act="gelu")["y"]
+    wg = vf.linear_grad(dy * 2, x * 2, W * 2, act="gelu", z=z * 2)
+    wn, wc = vf.clip_grad_norm([x * 2, W * 2], 1.0)
+    for call in ("linear", "grad", "clip"):
+        s = busy_stream()
+        t = [v * 2 for v in (x, W, b, r, dy, z)]
+        s.wait_stream(torch.cuda.current_stream())
+        if call == "linear":
+            got = vf.linear(t[0], t[1], t[2], residual=t[3], act="gelu", stream=s)["y"]
+        elif call == "grad":
+            got = vf.linear_grad(t[4], t[0], t[1], act="gelu", z=t[5], stream=s)
+        else:
+            norm, _ = vf.clip_grad_norm(t[:2], 1.0, out=[torch.empty_like(v) for v in t[:2]], stream=s)
+        assert not s.query()
+        del t
+        junk = overwrite((x, W, b, r, dy, z))
+        torch.cuda.synchronize()
+        if call == "linear":
+            assert torch.equal(got, want)
+        elif call == "grad":
+            assert all(torch.equal(got[k], wg[k]) for k in ("dx", "dW", "db"))
+        else:
+            assert torch.equal(norm, wn)
+        del junk
