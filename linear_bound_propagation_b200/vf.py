@@ -135,6 +135,14 @@ def _stream_ptr(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _used_on(stream, *tensors):
+    """Memory of `tensors` that is freed on their own stream is not handed out again before `stream` has done what it holds now."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _ptr(t: Optional[torch.Tensor]):
     if t is None:
         return None
@@ -201,6 +209,7 @@ class Net:
         lb = torch.empty(B * self.total, device=centres.device, dtype=torch.float32)
         ub = torch.empty_like(lb)
         _check(lib().vf_ibp(self.h, _ptr(centres), B, float(eps), _ptr(lb), _ptr(ub), _stream_ptr(stream)))
+        _used_on(stream, centres, lb, ub)
         return lb, ub
 
     def node_block(self, flat: torch.Tensor, v: int, B: int) -> torch.Tensor:
@@ -216,6 +225,7 @@ class Net:
         arr = self._alpha_array(alpha)
         _check(lib().vf_crown_backward(self.h, start_node, _ptr(lambda0), R, bstride, _ptr(lb_all), _ptr(ub_all),
                                        arr, B, _ptr(lam_in), _ptr(cst), _stream_ptr(stream)))
+        _used_on(stream, lambda0, lb_all, ub_all, lam_in, cst, *(alpha or {}).values())
         return lam_in, cst
 
     def _alpha_array(self, alpha):
@@ -273,6 +283,7 @@ class Net:
         _check(lib().vf_verify_batch(self.h, _ptr(centres), B, float(eps), _ptr(C), R, bstride, ctypes.byref(o),
                                      _ptr(out["lb"]), _ptr(out.get("ub")), _ptr(out.get("lb_ibp")),
                                      _ptr(out.get("verified")), _stream_ptr(stream)))
+        _used_on(stream, centres, C, *out.values(), *(alpha or {}).values(), *(splits or {}).values())
         return out
 
     def _split_array(self, splits):
@@ -328,6 +339,7 @@ class Net:
         o.beta_rows_out = be.data_ptr() if be is not None else None
         _check(lib().vf_alpha_crown(self.h, _ptr(centres), B, float(eps), _ptr(C), R, bstride, ctypes.byref(o), iters,
                                     float(lr), _ptr(lb), _ptr(lb0), _ptr(al), _stream_ptr(stream)))
+        _used_on(stream, centres, C, lb, lb0, al, be, alpha_init, beta_init, *(splits or {}).values())
         return {"lb": lb, "lb_start": lb0, "alpha": al, "beta": be}
 
     def alpha_grad(self, centres: torch.Tensor, eps: float, C: torch.Tensor, alpha: torch.Tensor, crown_relus=None,
@@ -340,6 +352,7 @@ class Net:
         o, keep = self._opts(crown_relus)
         _check(lib().vf_alpha_grad(self.h, _ptr(centres), B, float(eps), _ptr(C), R, bstride, ctypes.byref(o),
                                    _ptr(alpha), _ptr(lb), _ptr(grad), _stream_ptr(stream)))
+        _used_on(stream, centres, C, alpha, lb, grad)
         return lb, grad
 
     def alpha_beta_grad(self, centres: torch.Tensor, eps: float, C: torch.Tensor, alpha: torch.Tensor,
@@ -354,6 +367,7 @@ class Net:
         o, keep = self._opts(crown_relus, splits)
         _check(lib().vf_alpha_beta_grad(self.h, _ptr(centres), B, float(eps), _ptr(C), R, bstride, ctypes.byref(o),
                                         _ptr(alpha), _ptr(beta), _ptr(lb), _ptr(ga), _ptr(gb), _stream_ptr(stream)))
+        _used_on(stream, centres, C, alpha, beta, lb, ga, gb, *(splits or {}).values())
         return lb, ga, gb
 
     def bab(self, centre: torch.Tensor, eps: float, C: torch.Tensor, max_domains: int = 1000, batch: int = 16,
@@ -380,8 +394,10 @@ class Net:
             o.relu_crown = ctypes.cast(keep, ctypes.POINTER(ctypes.c_int))
         r = BabResult()
         C2 = C.reshape(-1, C.shape[-1]).contiguous()
-        _check(lib().vf_bab_verify(self.h, _ptr(centre.contiguous()), float(eps), _ptr(C2), C2.shape[0],
+        c2 = centre.contiguous()
+        _check(lib().vf_bab_verify(self.h, _ptr(c2), float(eps), _ptr(C2), C2.shape[0],
                                    ctypes.byref(o), ctypes.byref(r), _stream_ptr(stream)))
+        _used_on(stream, c2, C2)
         out = {"status": BAB_STATUS[r.status], "domains": r.domains, "rounds": r.rounds, "max_depth": r.max_depth,
                "lb": r.lb}
         if trace:
@@ -447,6 +463,7 @@ def concretize(lam: torch.Tensor, cst: Optional[torch.Tensor], centres: torch.Te
     lb = torch.empty(B, R, device=lam.device)
     _check(lib().vf_concretize(_ptr(lam), _ptr(cst), _ptr(centres), float(eps), B, R, n0, _ptr(lb),
                                _stream_ptr(stream)))
+    _used_on(stream, lam, cst, centres, lb)
     return lb
 
 
@@ -475,6 +492,7 @@ def concretize_dense_noalloc(lam: torch.Tensor, W: torch.Tensor, b: torch.Tensor
         raise ValueError(f"out must be float32 [{B}, {R}], got {out.dtype} {tuple(out.shape)}")
     _check(lib().vf_concretize_dense_noalloc(_ptr(lam), bstride, R, _ptr(W), _ptr(b), _ptr(centres), float(eps), B,
                                              n_in, n_out, _ptr(out), _stream_ptr(stream)))
+    _used_on(stream, lam, W, b, centres, out)
     return out
 
 
@@ -493,14 +511,6 @@ class _On:
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
-
-
-def _used_on(stream, *tensors):
-    """Memory of `tensors` that is freed on their own stream is not handed out again before `stream` has done what it holds now."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
 
 
 def _matrix(name, t, shape, dtype, dev):
