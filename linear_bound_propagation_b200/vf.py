@@ -502,6 +502,8 @@ class _On:
     def __init__(self, dev, stream):
         self.guards = [torch.cuda.device(dev)]
         if stream is not None:
+            if stream.device.index != dev:
+                raise ValueError(f"stream is on {stream.device}, the tensors are on CUDA device {dev}")
             self.guards.append(torch.cuda.stream(stream))
 
     def __enter__(self):
@@ -648,7 +650,7 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, scale: float 
     n = len(grads)
     if len(outs) != n:
         raise ValueError(f"{n} gradients and {len(outs)} outputs")
-    dev = grads[0].get_device() if n else torch.cuda.current_device()
+    dev = grads[0].get_device() if n else torch.cuda.current_device() if stream is None else stream.device.index
     if stream is not None or (dev >= 0 and dev != torch._C._cuda_getDevice()):
         with _On(dev, stream):
             result = clip_grad_norm(grads, max_norm, scale, None if out is None else outs)

@@ -23,3 +23,10 @@ def test_tensors_are_recorded_on_the_stream_that_is_given():
     assert a.streams == b.streams == []
     vf._used_on("s", a, None, b)
     assert a.streams == b.streams == ["s"]
+
+
+def test_a_stream_of_another_device_is_refused():
+    """It would be left for the tensors' device, and the call would run on that device's current stream."""
+    other = types.SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        vf._On(0, other)
