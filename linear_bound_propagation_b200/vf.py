@@ -15,6 +15,7 @@ from typing import Dict, Optional, Sequence
 
 import numpy as np
 import torch
+from torch.autograd.graph import increment_version
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libvf.so")
@@ -569,7 +570,8 @@ def linear(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tensor] = None,
     """vf_linear: act(x W^T + b + residual) for x [M, K], W [N, K], b [N], residual [M, N], all of one type (float32,
     bfloat16 or float16); rows may be any distance apart. act: "none", "relu", "gelu" (normal distribution) or
     "silu". Returns dict(y=[M, N], z=the pre-activation for linear_grad or None). out: y's buffer; it may be
-    `residual` itself. Runs on the current stream of x's device unless `stream` is given. `stream`
+    `residual` itself, and overlaps no other argument. Not part of an autograd graph: linear_grad is the backward pass, to
+    be called or put into a torch.autograd.Function by the caller. Runs on the current stream of x's device unless `stream` is given. `stream`
     has to wait for its inputs' makers and their users for `stream`, as with any work on several streams; the inputs may be
     dropped right after the call, and what it returns belongs to `stream`."""
     tt, dtype, a, dev, M, N, K = _layer(x, W, act)
@@ -595,6 +597,8 @@ def linear(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tensor] = None,
     _check(lib().vf_linear(dtype, a, xp, ldx, wp, ldw, bp, rp, ldr, M, N, K, yp, ldy, None if z is None else z.data_ptr(),
                            N, None if work is None else work.data_ptr(), nbytes,
                            torch._C._cuda_getCurrentRawStream(dev)))
+    if out is not None:
+        increment_version(out)
     return {"y": y, "z": z}
 
 
@@ -602,7 +606,7 @@ def linear_grad(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, act: str = "
                 need: Sequence[str] = ("dx", "dW", "db"), stream=None):
     """vf_linear_grad: the backward pass of linear for dy [M, N], the gradient of y, and the z that linear returned
     (not needed for act="none"). Returns dict(dx=[M, K], dW=[N, K], db=[N], dr=[M, N], the gradient of the
-    residual), None for those not in `need`."""
+    residual), None for those not in `need`. Not part of an autograd graph; `stream` as for linear."""
     tt, dtype, a, dev, M, N, K = _layer(x, W, act)
     if not set(need) <= {"dx", "dW", "db", "dr"}:
         raise ValueError(f"need names dx, dW, db and dr, got {list(need)}")
@@ -644,7 +648,7 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, scale: float 
     """vf_clip_grad_norm: (norm, out). norm is a float32 scalar tensor, scale * the global L2 norm of all gradients;
     out are the gradients times scale, and times max_norm / norm where the norm is larger than max_norm. Without
     `out` the gradients are overwritten. They may differ in type; each is contiguous. Nothing synchronises: a norm that
-    is not finite clips nothing and is left for the caller to look at."""
+    is not finite clips nothing and is left for the caller to look at. `stream` as for linear."""
     grads = list(grads)
     outs = grads if out is None else list(out)
     n = len(grads)
@@ -677,6 +681,7 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, scale: float 
     _check(lib().vf_clip_grad_norm(n, gp.buffer_info()[0], op.buffer_info()[0], sizes.buffer_info()[0],
                                    types.buffer_info()[0], scale, max_norm, norm.data_ptr(), buf.data_ptr(), nbytes,
                                    torch._C._cuda_getCurrentRawStream(dev)))
+    increment_version(outs)
     return norm, outs
 
 
