@@ -371,10 +371,10 @@ typedef enum {
     VF_ACT_SILU = 3  /* z / (1 + exp(-z)) */
 } vf_act;
 
-/* Bytes of workspace that vf_linear (grad = 0) or vf_linear_grad (grad = 1) may need for these sizes, whatever the
- * strides and alignment; with grad = VF_FORWARD_ALIGNED, vf_linear where x and W are 16-byte aligned and their row
- * strides are multiples of 16 bytes. May be 0 (NULL is then accepted). A call whose workspace is too small launches
- * nothing. [host] */
+/* Bytes of workspace that vf_linear (grad = 0) or vf_linear_grad (grad = 1) may need for these sizes on the current device,
+ * whatever the strides and alignment; with grad = VF_FORWARD_ALIGNED, vf_linear where x and W are 16-byte aligned and
+ * their row strides are multiples of 16 bytes. May be 0 (NULL is then accepted). A call whose workspace is too small
+ * launches nothing. [host] */
 enum { VF_FORWARD_ALIGNED = 2 };
 int vf_linear_workspace(int dtype, long long M, int N, int K, int grad, size_t* bytes);
 

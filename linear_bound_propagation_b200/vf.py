@@ -549,11 +549,15 @@ def _layer(x, W, act):
 
 
 @functools.lru_cache(maxsize=4096)
-def _linear_work(dtype, M, N, K, grad):
-    """Bytes of workspace for these sizes (a function of the sizes alone)."""
+def _linear_work_on(dtype, M, N, K, grad, dev):
+    """Bytes of workspace for these sizes on device dev, which is the current one: the plan of a call depends on its SMs."""
     n = ctypes.c_size_t()
     _check(lib().vf_linear_workspace(dtype, M, N, K, grad, ctypes.byref(n)))
     return n.value
+
+
+def _linear_work(dtype, M, N, K, grad):
+    return _linear_work_on(dtype, M, N, K, grad, torch.cuda.current_device())
 
 
 @functools.lru_cache(maxsize=None)
@@ -592,7 +596,7 @@ def linear(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tensor] = None,
         y = out
         yp, ldy = _matrix("out", y, shape, tt, dev)
     z = torch.empty_strided(shape, (N, 1), device=x.device, dtype=tt) if want_z else None
-    nbytes = _linear_work(dtype, M, N, K, 0 if (xp | wp | (ldx | ldw) * tt.itemsize) & 15 else VF_FORWARD_ALIGNED)
+    nbytes = _linear_work_on(dtype, M, N, K, 0 if (xp | wp | (ldx | ldw) * tt.itemsize) & 15 else VF_FORWARD_ALIGNED, dev)
     work = torch.empty_strided((nbytes,), (1,), device=x.device, dtype=torch.uint8) if nbytes else None
     _check(lib().vf_linear(dtype, a, xp, ldx, wp, ldw, bp, rp, ldr, M, N, K, yp, ldy, None if z is None else z.data_ptr(),
                            N, None if work is None else work.data_ptr(), nbytes,
@@ -627,7 +631,7 @@ def linear_grad(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, act: str = "
     dW = torch.empty_strided((N, K), (K, 1), device=device, dtype=tt) if "dW" in need else None
     db = torch.empty_strided((N,), (1,), device=device, dtype=tt) if "db" in need else None
     dr = torch.empty_strided(shape, (N, 1), device=device, dtype=tt) if "dr" in need else None
-    nbytes = _linear_work(dtype, M, N, K, 1)
+    nbytes = _linear_work_on(dtype, M, N, K, 1, dev)
     work = torch.empty_strided((nbytes,), (1,), device=device, dtype=torch.uint8) if nbytes else None
     _check(lib().vf_linear_grad(dtype, a, dyp, lddy, zp, ldz, xp, ldx, wp, ldw, M, N, K,
                                 None if dx is None else dx.data_ptr(), K, None if dW is None else dW.data_ptr(), K,

@@ -30,3 +30,23 @@ def test_a_stream_of_another_device_is_refused():
     other = types.SimpleNamespace(device=torch.device("cuda", 1))
     with pytest.raises(ValueError, match="stream is on cuda:1"):
         vf._On(0, other)
+
+
+def test_workspace_sizes_are_kept_for_each_device(monkeypatch):
+    """Plans depend on the number of SMs: a size asked on one device is not another's."""
+    on = [0]
+
+    class Lib:
+        def vf_linear_workspace(self, dtype, M, N, K, grad, n):
+            n._obj.value = 1000 + on[0]
+            return vf.VF_OK
+
+    monkeypatch.setattr(vf, "lib", lambda: Lib())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: on[0])
+    sizes = (0, 123457, 11, 13, 1)  # asked nowhere else
+    assert vf._linear_work(*sizes) == 1000
+    on[0] = 1
+    assert vf._linear_work(*sizes) == 1001
+    on[0] = 0
+    assert vf._linear_work(*sizes) == 1000
+    vf._linear_work_on.cache_clear()
