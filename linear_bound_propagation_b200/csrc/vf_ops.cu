@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <exception>
 #include <vector>
 
 #include "vf.h"
@@ -85,8 +86,12 @@ int launched(cudaError_t e) {
 template <typename F>
 int guarded(F body) {
     try {
-        return body();
-    } catch (...) {
+        try {
+            return body();
+        } catch (const std::exception& e) {
+            return ops_fail(VF_ERR_CUDA, "host: %s", e.what());
+        }
+    } catch (...) {  // nor does the message's own memory
         return VF_ERR_CUDA;
     }
 }
@@ -219,21 +224,25 @@ int vf_linear_grad(int dtype, int act, const void* dy, long long lddy, const voi
 }
 
 int vf_ops_check(void) {
-    int timeout = 0;
-    cudaError_t e = cudaDeviceSynchronize();
-    if (e == cudaSuccess) e = ops_take_timeout(&timeout);
-    if (e != cudaSuccess) return ops_fail(VF_ERR_CUDA, "asynchronous CUDA error: %s", cudaGetErrorString(e));
-    if (timeout) return ops_fail(VF_ERR_TIMEOUT, "a kernel gave up a bounded wait; its outputs are not valid");
-    return VF_OK;
+    return guarded([]() -> int {
+        int timeout = 0;
+        cudaError_t e = cudaDeviceSynchronize();
+        if (e == cudaSuccess) e = ops_take_timeout(&timeout);
+        if (e != cudaSuccess) return ops_fail(VF_ERR_CUDA, "asynchronous CUDA error: %s", cudaGetErrorString(e));
+        if (timeout) return ops_fail(VF_ERR_TIMEOUT, "a kernel gave up a bounded wait; its outputs are not valid");
+        return VF_OK;
+    });
 }
 
 int vf_clip_workspace(int n, size_t* bytes) {
-    if (bytes == nullptr) return ops_fail(VF_ERR_ARG, "NULL pointer");
-    if (n < 0) return ops_fail(VF_ERR_ARG, "negative number of gradients");
-    int sms = 0;
-    OPS_TRY(sm_count(&sms));
-    *bytes = (size_t)clip_work_doubles(n, sms) * sizeof(double);
-    return VF_OK;
+    return guarded([&]() -> int {
+        if (bytes == nullptr) return ops_fail(VF_ERR_ARG, "NULL pointer");
+        if (n < 0) return ops_fail(VF_ERR_ARG, "negative number of gradients");
+        int sms = 0;
+        OPS_TRY(sm_count(&sms));
+        *bytes = (size_t)clip_work_doubles(n, sms) * sizeof(double);
+        return VF_OK;
+    });
 }
 
 int vf_clip_grad_norm(int n, const void* const* grads, void* const* outs, const long long* sizes, const int* dtypes,

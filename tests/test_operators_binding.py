@@ -1,4 +1,7 @@
 """The Python side of the dense-layer and gradient operators, with a library and tensors that stand in for the GPU's."""
+import os
+import subprocess
+import sys
 import types
 
 import pytest
@@ -50,3 +53,25 @@ def test_workspace_sizes_are_kept_for_each_device(monkeypatch):
     on[0] = 0
     assert vf._linear_work(*sizes) == 1000
     vf._linear_work_on.cache_clear()
+
+
+def test_running_out_of_host_memory_is_an_error_with_a_message():
+    """A list of gradients whose table does not fit into what the process may still allocate."""
+    code = """
+import ctypes, resource
+from linear_bound_propagation_b200 import vf
+L, n = vf.lib(), 4_000_000
+ptrs = (ctypes.c_void_p * n)(*range(1 << 20, (1 << 20) + 16 * n, 16))
+sizes, types = (ctypes.c_longlong * n)(*([4] * n)), (ctypes.c_int * n)()
+args = (ptrs, ptrs, sizes, types, 1.0, 1.0, 1 << 20, None, 0, None)
+assert L.vf_clip_grad_norm(-1, *args) == vf.VF_ERR_ARG  # leaves a message of its own
+now = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (now + (48 << 20), resource.RLIM_INFINITY))
+rc = L.vf_clip_grad_norm(n, *args)
+resource.setrlimit(resource.RLIMIT_AS, (resource.RLIM_INFINITY, resource.RLIM_INFINITY))
+assert rc == vf.VF_ERR_CUDA, rc
+assert b"alloc" in L.vf_last_error(), L.vf_last_error()
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
