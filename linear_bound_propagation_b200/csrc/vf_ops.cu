@@ -60,6 +60,9 @@ int check_matrix(const char* name, const void* p, long long rows, long long cols
     return VF_OK;
 }
 
+// The stride of a single row is not used; where rows have to be 16 bytes apart it must not decide either.
+long long stride(long long rows, long long cols, long long ld) { return rows > 1 ? ld : (cols + 7) / 8 * 8; }
+
 int check_vector(const char* name, const void* p, int dtype) {
     if (reinterpret_cast<uintptr_t>(p) % elem_bytes(dtype) != 0)
         return ops_fail(VF_ERR_ARG, "%s is not aligned to its element", name);
@@ -179,6 +182,7 @@ int vf_linear(int dtype, int act, const void* x, long long ldx, const void* W, l
         if (r != nullptr) OPS_TRY(check_matrix("r", r, M, N, ldr, dtype));
         OPS_TRY(check_matrix("y", y, M, N, ldy, dtype));
         if (z != nullptr) OPS_TRY(check_matrix("z", z, M, N, ldz, dtype));
+        ldx = stride(M, K, ldx), ldw = stride(N, K, ldw), ldr = stride(M, N, ldr), ldy = stride(M, N, ldy), ldz = stride(M, N, ldz);
         const LinearFwd p{dtype, act, x, ldx, W, ldw, b, r, ldr, M, N, K, y, ldy, z, ldz};
         if (linear_few_forward(dtype, M, N, K)) return launched(launch_linear_few(p, (cudaStream_t)stream));
         if (!use_tc(M, N, K)) return launched(launch_linear_ffma(p, (cudaStream_t)stream));
@@ -211,6 +215,8 @@ int vf_linear_grad(int dtype, int act, const void* dy, long long lddy, const voi
         }
         OPS_TRY(check_vector("db", db, dtype));
         if (dr != nullptr) OPS_TRY(check_matrix("dr", dr, M, N, lddr, dtype));
+        lddy = stride(M, N, lddy), ldz = stride(M, N, ldz), ldx = stride(M, K, ldx), ldw = stride(N, K, ldw);
+        lddx = stride(M, K, lddx), lddw = stride(N, K, lddw), lddr = stride(M, N, lddr);
         const LinearGrad p{dtype, act, dy, lddy, z, ldz, x, ldx, W, ldw, M, N, K, dx, lddx, dW, lddw, db, dr, lddr};
         const bool few = linear_few_supported(dtype, M, N, K);
         if (!few && !use_tc(M, N, K)) return launched(launch_linear_grad_ffma(p, (cudaStream_t)stream));
