@@ -36,6 +36,7 @@ VF_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 VF_FORWARD_ALIGNED = 2
 VF_ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 NOALLOC_SCRATCH_FLOATS = 1 << 22
+MAX_EXTENT = 0x7fffff00
 
 
 class VfError(RuntimeError):
@@ -545,6 +546,8 @@ def _layer(x, W, act):
     if dev < 0 or x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1]:
         raise ValueError(f"x [M, K] and W [N, K] on a CUDA device expected, got {list(x.shape)} and {list(W.shape)}")
     M, K = x.shape
+    if K > MAX_EXTENT or W.shape[0] > MAX_EXTENT:  # C ints: they would arrive as other sizes
+        raise ValueError(f"N and K must stay below 2^31 - 256, got W {list(W.shape)}")
     return x.dtype, dtype, a, dev, M, W.shape[0], K
 
 

@@ -75,3 +75,21 @@ assert b"alloc" in L.vf_last_error(), L.vf_last_error()
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("M,N,K", [(1, (1 << 32) + 8, 1), (1, 8, (1 << 32) + 8), (2, 1 << 31, 4)])
+def test_sizes_that_a_c_int_would_wrap_are_refused(M, N, K):
+    """2^32 + 8 rows of W would arrive as 8: the rest of the output would be left as it was."""
+
+    class OnGpu(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    x, W = (torch.empty(s, device="meta", dtype=torch.bfloat16).as_subclass(OnGpu) for s in ((M, K), (N, K)))
+    with pytest.raises(ValueError, match="below 2.31"):
+        vf._layer(x, W, "none")
+    if N <= 8:
+        with pytest.raises(ValueError, match="below 2.31"):
+            vf._layer(W, x, "relu")
+    x, W = (torch.empty(s, device="meta", dtype=torch.bfloat16).as_subclass(OnGpu) for s in ((1 << 33, 3), (vf.MAX_EXTENT, 3)))
+    assert vf._layer(x, W, "none")[4:] == (1 << 33, vf.MAX_EXTENT, 3)  # rows are a long long: left to the library
