@@ -360,7 +360,8 @@ int vf_concretize_dense_noalloc(const float* lambda, long long lambda_bstride, i
  * CUDA graph. All matrices of a call have one element type; sums are held in fp32 or more and every output is
  * rounded to the element type once. The tensor cores cut what they add instead of rounding it; their accumulators are
  * added to rounded fp32 sums every 2048 steps of a reduction (16 bits) or 256 (fp32), so that terms of one sign come out
- * low by about 1.2e-5 of the sum in float16, 7e-6 in bf16 and 4e-7 in fp32, however long the reduction is. Row strides
+ * low by about 1.2e-5 of the sum in float16, 7e-6 in bf16 and 4e-7 in fp32, however long the reduction is. They take
+ * fp32 as bf16 pieces, so that of operands below 2^-110 what lies under 2^-133 is lost. Row strides
  * (ld*) are in elements, at least the row's length (of a single row: any); any alignment of the element type is served. Results do not change
  * from run to run. Outputs must not overlap inputs, save where an entry point says so. */
 typedef enum { VF_F32 = 0, VF_BF16 = 1, VF_F16 = 2 } vf_dtype;

@@ -245,6 +245,7 @@ __device__ __forceinline__ void finish_lane(const TcProduct& p, long long i, lon
 // much in m and l, all of x's sign: products without m l and l m then came out low by up to 4.7e-7.) What bf16 would round to
 // infinity is cut. An infinity or NaN goes to l alone: a piece that is not finite meets h of the other operand, which is zero
 // only where that is zero, so the product is the one of fp32 (infinity times infinity excepted: NaN), and none of another sign.
+// Of values below 2^-110 the pieces hold what lies above 2^-133, bf16's last place (the MMAs take its subnormal numbers as they are).
 constexpr float LARGEST_ROUNDED = 0x1.fefffep127f;  // the largest fp32 value that bf16 rounds to a finite one
 __device__ __forceinline__ uint32_t round2(float a, float b) {
     const __nv_bfloat162 w = __floats2bfloat162_rn(a, b);

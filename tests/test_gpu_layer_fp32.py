@@ -174,3 +174,22 @@ def test_infinities_are_those_of_fp32(M, pad, dtype):
     dx = vf.linear_grad(x, torch.zeros(M, N, device="cuda", dtype=dtype), Wt, need=("dx",))["dx"]
     assert torch.equal(dx[:2], want[:2].to(dtype)) and dx[2].isnan().all()
     vf.ops_check()
+
+
+@pytest.mark.parametrize("M", [4, 40, 700])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_small_values_keep_their_bits_down_to_2_to_the_minus_110(M, pad):
+    """The lowest of 24 bits of a value of 2^-110 is 2^-133, the lowest that bf16 holds; below that what lies under 2^-133 is cut off or
+    rounded there, and the few-row kernels keep all."""
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    N, T = 264, 520
+    for e in (-80, -110, -118, -126):
+        x = torch.randint(2 ** 23, 2 ** 24, (M, T + pad), generator=gen, device="cuda").float()[:, :T] * 2.0 ** (e - 23)
+        W, at, v = one_hot(gen, N, T, pad)
+        W, v = W * 2.0 ** 60, v * 2.0 ** 60
+        y, want = vf.linear(x, W)["y"], x[:, at].double() * v.double()
+        if e >= -110 or M == 4:
+            assert torch.equal(y.double(), want)
+        else:
+            assert float(((y.double() - want).abs() / v.double()).max()) <= 2.0 ** -134 + 2.0 ** (e - 24)
+    vf.ops_check()
