@@ -393,12 +393,12 @@ bool aligned(const void* p, long long ld, int e) { return (reinterpret_cast<uint
 }  // namespace
 
 // Every tile has an SM to itself, with the reduction cut into as many parts as the accumulators ask for, up to eight.
-// Against a laid-out copy and k_linear_tc.cu (M x N x K, us, here and there): fp32 16x512x512 5.2 and 8.4, 1024x256x784
-// 10.3 and 13.2, 512x1024x1024 14.2 and 16.9; many waves of tiles, fp32 297x3712x1472 118 and 33.
+// Against a laid-out copy and k_linear_tc.cu (M x N x K, us out of L2, here and there): fp32 16x512x512 6.1 and 9.0, 1024x256x784
+// 11.0 and 13.8, 512x1024x1024 15.0 and 18.2, 16x4096x4096 21.1 and 53.9; many waves of tiles, 297x3712x1472 118 and 35.
 // Rows that are not 16-byte aligned are loaded element by element. In fp32 that costs more than the copy where several
-// columns of tiles load the same W and a CTA takes many such lines: x and W unaligned, 256x256x256 8.4 and 9.7,
-// 1024x256x784 16.1 and 14.0, 512x1024x1024 26.5 and 17.7; one column of tiles, 16x2048x4096, 35.8 and 37.9. In 16 bits the
-// two are close (bf16 1024x256x784 9.5 and 10.1, 777x1001x512 12.8 and 9.5), and a call that waits for the host is shorter
+// columns of tiles load the same W and a CTA takes many such lines: x and W unaligned, 256x256x256 9.0 and 10.0,
+// 1024x256x784 16.1 and 14.4, 512x1024x1024 26.5 and 18.5; one column of tiles, 16x2048x4096, 38.5 and 36.5. In 16 bits the
+// two are close (bf16 1024x256x784 10.1 and 10.4, 777x1001x512 13.2 and 10.0), and a call that waits for the host is shorter
 // with one launch (9.9 and 14.3).
 bool linear_direct_fits(int dtype, long long M, int N, int K, bool x_aligned, bool w_aligned) {
     int sms = 0, parts = 1;

@@ -9,10 +9,11 @@
 // twice the registers: 8 x 4096 x 4096 bf16 52 us, apart 36 us; with the inputs' g together in shared memory (a load for
 // four of them) and the blocks chosen below 24.7 us.
 //
-// Measured here and on the tensor cores (k_linear_tc.cu), which pad the rows to 16, with relu in us:
-//   bf16   x 4096 x 4096   1: 12.4 and 28.7   4: 14.4 and 28.4   8: 24.7 and 28.5   8 x 1024 x 1024: 7.6 and 9.7
-//   fp32   x 4096 x 4096   1: 23.6 and 85.9   8: 35.3 and 85.9  16: 57.0 and 86.8  16 x 1024 x 1024: 9.9 and 12.9
-// One row: 2 N K elements in 23.6 us (fp32, 5.7 TB/s) and 12.4 us (bf16, 5.4 TB/s).
+// Measured here and on the tensor cores (k_linear_tc.cu), which pad the rows to 16, with relu in us out of L2:
+//   bf16   x 4096 x 4096   1: 12.7 and 29.3   4: 14.7 and 29.3   8: 25.1 and 29.3   8 x 1024 x 1024: 7.9 and 9.8
+//   fp32   x 4096 x 4096   1: 23.9 and 89.5   8: 36.1 and 89.7  16: 57.4 and 90.3  16 x 1024 x 1024: 10.0 and 14.1
+// One row: 2 N K elements in 23.9 us (fp32, 5.6 TB/s) and 12.7 us (bf16, 5.3 TB/s); with W out of HBM 28.0 and 22.4 us (tensor
+// cores 89.4 and 30.7), eight rows of bf16 30.6 (30.9).
 #include <algorithm>
 
 #include "linear_tc.cuh"
@@ -278,7 +279,8 @@ constexpr int ROWS = 4;  // rows of W per group of warps
 
 // y = act(x W^T + b + r) for M <= MB rows of x: W is read once, 2 M operations for each element, so memory bounds it. A group
 // of warps takes four rows of W and shares the reduction; a lane's part of x, loaded from L1, serves the four rows, and the
-// next step's part of W is on its way meanwhile. Sums are fp32 in a fixed order. 1 x 4096 x 4096 fp32 7.8 us out of L2.
+// next step's part of W is on its way meanwhile. Sums are fp32 in a fixed order. 1 x 4096 x 4096 fp32 8.4 us out of L2, 18.6 us out
+// of HBM.
 template <typename T, int VEC, int MB>
 __global__ void __launch_bounds__(THREADS, 2) linear_few_k(const __grid_constant__ LinearFwd f, int glog) {
     constexpr int C = MB * ROWS;
@@ -349,7 +351,8 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_k(const __grid_constant
 }
 
 // All eight warps share a reduction, or fewer where there would be more than two blocks per SM and a warp fewer than four steps:
-// 1 x 4096 x 1024 bf16 6.0 us with eight, 3.7 us with two; 8 x 4096 x 4096 fp32 15.4 us with eight, 18.7 us with two.
+// 1 x 4096 x 1024 bf16 6.6 us with eight, 4.0 us with two (W out of HBM 9.7 and 6.1); 8 x 4096 x 4096 fp32 18.4 us with eight,
+// 18.8 us with two (29.2 and 37).
 template <typename T, int VEC>
 cudaError_t launch_rows(const LinearFwd& f, cudaStream_t s) {
     const long long rows = (f.N + ROWS - 1LL) / ROWS;
@@ -374,10 +377,13 @@ cudaError_t launch_few_forward(const LinearFwd& f, cudaStream_t s) {
 }  // namespace
 
 // Up to eight rows, in 16 bits up to 2^24 multiplications. M x N x K, us here and on the tensor cores (k_linear_direct.cu for
-// fp32, k_linear_tc.cu for 16 bits; replayed from a graph, W in L2):
-//   fp32  1x1024x1024 2.5 and 6.8   1x4096x4096 7.8 and 19.6   8x4096x4096 15.4 and 19.6   16x4096x4096 48.8 and 19.5
-//   bf16  1x1024x1024 2.7 and 5.7   1x4096x1024 3.8 and 5.8   1x4096x4096 9.0 and 8.4   8x2048x1024 4.4 and 5.8
-//         2x4096x4096 9.9 and 8.5   8x4096x1024 6.2 and 5.8   8x4096x4096 16.9 and 8.3
+// fp32, k_linear_tc.cu for 16 bits; replayed from a graph, W in L2, in parentheses with W out of HBM):
+//   fp32  1x1024x1024 2.6 and 7.2 (3.4 and 8.6)   1x4096x4096 8.4 and 21.5 (18.6 and 27.6)   8x4096x4096 18.4 and 21.6 (29.2 and 28.0)
+//   bf16  1x1024x1024 3.0 and 6.1 (3.7 and 6.8)   1x4096x1024 4.2 and 6.1 (6.5 and 7.9)   8x2048x1024 4.6 and 6.1 (6.5 and 7.3)
+//         8x4096x512 4.7 and 5.1 (6.2 and 6.4)   1x4096x4096 9.4 and 9.6 (14.5 and 14.3)   8x4096x1024 6.5 and 6.2 (9.0 and 7.9)
+//         2x4096x4096 11.1 and 8.9 (16.5 and 14.2)   8x4096x4096 18.2 and 8.6 (24.1 and 13.8)
+// The rule does not look at the alignment, off which this kernel loads single elements and the other side (k_linear_direct.cu in
+// every type) is the faster one: bf16 4x4093x1023 12.4 and 6.1, 8x2040x1023 8.0 and 6.1, fp32 8x4093x1023 11.7 and 10.5.
 bool linear_few_forward(int dtype, long long M, int N, int K) {
     return M >= 1 && M <= 8 && N >= 1 && K >= 1 && (dtype == VF_F32 || (double)M * N * K <= 16777216.0);
 }

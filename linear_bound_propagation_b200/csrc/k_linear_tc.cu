@@ -767,7 +767,9 @@ __device__ void pack_block(const PackJob& j, long long blk) {
 }
 
 // g = dy act'(z) of 8 * steps rows x PACK_COLS columns: to the operand (dst, unless g is dy itself), to dr, and its column sums
-// over the rows, in fp32, to part[row block][N].
+// over the rows, in fp32, to part[row block][N]. In 16 bits g of gelu and silu is rounded to the element type (float16: scaled
+// first, below): the error of dx and dW then is 1.4 times that of their own rounding (bf16 8192 x 4096 x 4096 2.3e-3 against
+// 1.7e-3, float16 2.9e-4 against 2.1e-4); a second 16-bit piece of g would double the products' time.
 struct GradJob {
     const void* dy;
     long long lddy;

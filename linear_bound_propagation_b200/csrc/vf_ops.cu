@@ -137,9 +137,11 @@ int check_overlaps(const ClipList& l) {
 }
 
 // Small products, and empty ones, run on the FFMA kernels, whose time goes with the reduction's length. M x N x K in us, FFMA
-// and tensor cores: fp32 forward 16x32x64 4.4 and 3.9, 64x32x16 3.4 and 4.8, 16x16x256 11.1 and 5.0, backward 16x32x64 4.2
-// and 5.8, 64x32x32 8.1 and 6.6; bf16 forward 64x32x16 4.8 and 4.0, 16x16x256 17.3 and 4.1, backward 16x64x128 5.6 and 6.1,
-// 128x64x32 11.3 and 6.4.
+// and tensor cores: fp32 forward 64x32x8 3.7 and 5.1, 64x32x16 3.4 and 5.1, 16x32x64 4.4 and 4.3, 16x16x256 11.1 and 5.5, backward
+// 20x32x32 4.9 and 6.2, 16x32x64 4.2 and 6.0, 64x32x32 8.1 and 7.0; bf16 forward 64x32x16 4.8 and 4.3, 16x16x256 17.3 and 4.4,
+// backward 16x64x128 5.6 and 6.1, 128x64x32 11.3 and 6.7. The rule goes by the volume alone and so takes the slower side for few
+// outputs of a long reduction below it: fp32 forward 32x1x1000 38 and 7.5, 9x1x3640 129 and 13, backward 64x16x16 8.2 and 6.5,
+// 2000x4x4 194 and 16, 8191x1x3 505 and 20.
 bool use_tc(long long M, int N, int K) { return linear_tc_supported(M, N, K) && (double)M * N * K >= 32768.0; }
 
 bool aligned16(const void* p, long long ld, int dtype) {
