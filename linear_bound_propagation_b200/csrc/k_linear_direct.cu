@@ -388,7 +388,6 @@ cudaError_t launch_vec(DirectParams& P, bool va, bool vb, cudaStream_t s) {
 }
 
 int elem(int dtype) { return dtype == VF_F32 ? 4 : 2; }
-bool aligned(const void* p, long long ld, int e) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * e) % 16 == 0; }
 
 }  // namespace
 
@@ -429,9 +428,9 @@ cudaError_t launch_linear_direct(const LinearFwd& f, cudaStream_t s) {
     p.zout = f.z;
     p.ldz = f.ldz;
     p.act = f.act;
-    p.vec = aligned(f.y, f.ldy, e) && (f.r == nullptr || aligned(f.r, f.ldr, e)) &&
-            (f.z == nullptr || aligned(f.z, f.ldz, e));
-    const bool va = aligned(f.W, f.ldw, e), vb = aligned(f.x, f.ldx, e);
+    p.vec = aligned16(f.y, f.ldy, e) && (f.r == nullptr || aligned16(f.r, f.ldr, e)) &&
+            (f.z == nullptr || aligned16(f.z, f.ldz, e));
+    const bool va = aligned16(f.W, f.ldw, e), vb = aligned16(f.x, f.ldx, e);
     switch (f.dtype) {
         case VF_F32: return launch_vec<float, 3>(P, va, vb, s);
         case VF_BF16: return launch_vec<__nv_bfloat16, 1>(P, va, vb, s);

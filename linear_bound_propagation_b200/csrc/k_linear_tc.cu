@@ -1024,11 +1024,6 @@ bool make_rows(CUtensorMap* map, const void* ptr, long long cols, long long rows
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 16-byte rows that TMA can address too (its strides end at 2^40 bytes).
-bool aligned16(const void* p, long long ld, int e) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * e) % 16 == 0 && ld < (1LL << 37);
-}
-
 // Rows of a block are 8 * steps: 256, or fewer (down to 8) until there are three blocks per SM, and on to six as long as no
 // more than 64 partial column sums result. 8192 x 4096, g, dr and db of a gelu: 512 blocks, little over three per SM, 52.9 us
 // in bf16 and 111.8 in fp32; 1024 blocks 48.0 and 96.4. Depends on the sizes alone, so that column sums are added in the

@@ -144,10 +144,6 @@ int check_overlaps(const ClipList& l) {
 // 2000x4x4 194 and 16, 8191x1x3 505 and 20.
 bool use_tc(long long M, int N, int K) { return linear_tc_supported(M, N, K) && (double)M * N * K >= 32768.0; }
 
-bool aligned16(const void* p, long long ld, int dtype) {
-    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)ld * elem_bytes(dtype)) & 15) == 0;
-}
-
 }  // namespace
 
 extern "C" {
@@ -188,7 +184,7 @@ int vf_linear(int dtype, int act, const void* x, long long ldx, const void* W, l
         const LinearFwd p{dtype, act, x, ldx, W, ldw, b, r, ldr, M, N, K, y, ldy, z, ldz};
         if (linear_few_forward(dtype, M, N, K)) return launched(launch_linear_few(p, (cudaStream_t)stream));
         if (!use_tc(M, N, K)) return launched(launch_linear_ffma(p, (cudaStream_t)stream));
-        if (!linear_tc_in_place(p) && linear_direct_fits(dtype, M, N, K, aligned16(x, ldx, dtype), aligned16(W, ldw, dtype)))
+        if (!linear_tc_in_place(p) && linear_direct_fits(dtype, M, N, K, aligned16(x, ldx, elem_bytes(dtype)), aligned16(W, ldw, elem_bytes(dtype))))
             return launched(launch_linear_direct(p, (cudaStream_t)stream));
         OPS_TRY(check_aligned(work));
         size_t need = 0;

@@ -212,6 +212,11 @@ __device__ __forceinline__ float act_grad(float dy, float z, int act) {
 }
 
 // ------------------------------------------------------------------------------------------ launch interfaces
+// Rows of 16-byte alignment (ld in elements of e bytes) that TMA can address too: its strides end at 2^40 bytes.
+inline bool aligned16(const void* p, long long ld, int e) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * e) % 16 == 0 && ld < (1LL << 37);
+}
+
 // One dense layer, forward: y = act(z), z = x W^T + b + r. Row strides in elements.
 struct LinearFwd {
     int dtype, act;
